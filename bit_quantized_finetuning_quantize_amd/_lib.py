@@ -64,6 +64,24 @@ SIGNATURES = {
     "qlora_linear_bwd_profiled": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64,
                                            _c_i64, _c_i32, _c_f32, _vp, _vp, _vp, _vp, _c_size,
                                            _vp, _vp, _vp]),
+    "qlora_act8_row_bytes": (_c_i64, [_c_i64]),
+    "qlora_act8_scale_row_bytes": (_c_i64, [_c_i64]),
+    "qlora_act8_quantize": (_c_int, [_vp, _c_i64, _c_i64, _c_i64, _c_i32, _vp, _vp, _vp]),
+    "qlora_act8_dequantize": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_i32, _vp, _c_i64, _vp]),
+    "qlora_swiglu_act8_fwd": (_c_int, [_vp, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _c_i32, _vp,
+                                       _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qlora_swiglu_act8_bwd": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i32,
+                                       _vp, _c_i64, _vp, _c_i64, _vp]),
+    "qlora_fp8_weight_quantize": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp]),
+    "qlora_act8_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "qlora_linear_bwd_act8": (_c_int, [_vp, _vp, _vp, _c_i32, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64,
+                                       _c_i64, _c_i64, _c_i32, _c_f32, _vp, _c_f32, _vp, _vp, _vp,
+                                       _vp, _c_size, _c_i32, _vp]),
+    "qlora_fp8_linear_fwd": (_c_int, [_vp, _vp, _c_i32, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64,
+                                      _c_i32, _c_f32, _vp, _vp, _vp, _c_size, _vp]),
+    "qlora_fp8_linear_bwd": (_c_int, [_vp, _c_i32, _vp, _vp, _c_i32, _vp, _vp, _vp, _vp, _vp,
+                                      _c_i64, _c_i64, _c_i64, _c_i32, _c_f32, _vp, _vp, _vp, _vp,
+                                      _c_size, _vp]),
     "qlora_gemv_wait_limit": (_c_int, [_c_i64]),
     "qlora_status_string": (ctypes.c_char_p, [_c_int]),
     "qlora_last_hip_error": (_c_int, []),

@@ -17,6 +17,9 @@ GROUP = 256
 STORE_NF4 = 0
 STORE_FP4 = 1
 STORE_DQ_FP8 = 2
+# code formats of the 8-bit blocks (include/qlora.h)
+ACT8_E4M3 = 0
+ACT8_E5M2 = 1
 
 
 class QloraError(RuntimeError):
@@ -375,3 +378,305 @@ def qlora_linear_bwd_dropout(dY, X, T, W, A, B, scale, keep_mask, p, want_dX=Tru
                                         _ptr(dX) if want_dX else None, _ptr(dA), _ptr(dB),
                                         _ptr(ws), ws.numel(), _stream()))
     return (dX if want_dX else None), dA, dB
+
+
+# ---- 8-bit blocks ------------------------------------------------------------
+
+
+class Act8:
+    """A matrix [M x K] in 8-bit blocks: uint8 codes [M, row bytes] and scale
+    bytes [M, scale row bytes] (include/qlora.h), `fmt` ACT8_E4M3 or ACT8_E5M2."""
+
+    __slots__ = ("codes", "scales", "shape", "fmt")
+
+    def __init__(self, codes, scales, shape, fmt=ACT8_E4M3):
+        self.codes, self.scales = codes, scales
+        self.shape = tuple(shape)
+        self.fmt = int(fmt)
+
+    def nbytes(self):
+        return self.codes.numel() + self.scales.numel()
+
+
+class Fp8Weight:
+    """A frozen weight [N x K] in 128 x 128 blocks of E4M3 codes; `codes_t`
+    and `scales_t` hold it transposed (for the input gradient) or are None."""
+
+    __slots__ = ("codes", "scales", "codes_t", "scales_t", "shape")
+
+    def __init__(self, codes, scales, codes_t, scales_t, shape):
+        self.codes, self.scales = codes, scales
+        self.codes_t, self.scales_t = codes_t, scales_t
+        self.shape = tuple(shape)
+
+    def nbytes(self):
+        return sum(t.numel() for t in (self.codes, self.scales, self.codes_t, self.scales_t)
+                   if t is not None)
+
+
+def act8_row_bytes(K):
+    return (K + 127) // 128 * 128
+
+
+def act8_scale_row_bytes(K):
+    return ((K + 127) // 128 + 3) // 4 * 4
+
+
+def empty_act8(M, K, device, fmt=ACT8_E4M3):
+    return Act8(torch.empty(M, act8_row_bytes(K), dtype=torch.uint8, device=device),
+                torch.empty(M, act8_scale_row_bytes(K), dtype=torch.uint8, device=device),
+                (M, K), fmt)
+
+
+def _rows(t, shape, name):
+    """Leading dimension of a bf16 matrix of `shape` on the GPU whose rows are contiguous."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or tuple(t.shape) != tuple(shape):
+        raise QloraError(f"{name} must be a bfloat16 tensor of shape {tuple(shape)} on the GPU")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise QloraError(f"{name} must have contiguous rows")
+    ld = t.stride(0)
+    if t.shape[0] == 1:  # one row: the stride has no meaning
+        return max(ld, t.shape[1])
+    if ld < t.shape[1]:
+        raise QloraError(f"{name} must not have overlapping rows")
+    return ld
+
+
+def _bytes(t, shape, name):
+    if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise QloraError(f"{name} must be a contiguous uint8 tensor of shape {shape} on the GPU")
+
+
+def _need_act8(a, name):
+    M, K = a.shape
+    _bytes(a.codes, (M, act8_row_bytes(K)), f"{name}.codes")
+    _bytes(a.scales, (M, act8_scale_row_bytes(K)), f"{name}.scales")
+
+
+def _need_weight(codes, scales, N, K, name):
+    if codes is None or scales is None:
+        raise QloraError(f"{name}: the weight does not hold this order")
+    _bytes(codes, (N, act8_row_bytes(K)), f"{name} codes")
+    _bytes(scales, ((N + 127) // 128, act8_scale_row_bytes(K)), f"{name} scales")
+
+
+def qlora_act8_quantize(X, fmt=ACT8_E4M3, out=None):
+    """The 8-bit blocks of a bf16 matrix [M x K] (rows may be strided)."""
+    if X.dim() != 2:
+        raise QloraError("X must be a matrix")
+    M, K = X.shape
+    ld = _rows(X, (M, K), "X")
+    a = out if out is not None else empty_act8(M, K, X.device, fmt)
+    if out is not None:
+        if a.shape != (M, K):
+            raise QloraError("out must have the shape of X")
+        _need_act8(a, "out")
+        a.fmt = int(fmt)
+    _check(LIB.qlora_act8_quantize(_ptr(X), M, K, ld, a.fmt, _ptr(a.codes), _ptr(a.scales),
+                                   _stream()))
+    return a
+
+
+def qlora_act8_dequantize(a, out=None):
+    """bf16 [M x K] of 8-bit blocks (exact)."""
+    _need_act8(a, "a")
+    M, K = a.shape
+    out = out if out is not None else torch.empty(M, K, dtype=torch.bfloat16, device=a.codes.device)
+    ld = _rows(out, (M, K), "out")
+    _check(LIB.qlora_act8_dequantize(_ptr(a.codes), _ptr(a.scales), M, K, a.fmt, _ptr(out), ld,
+                                     _stream()))
+    return out
+
+
+def qlora_swiglu_act8_fwd(G, U, fmt=ACT8_E4M3, want_h=True, want_h8=True, want_checkpoint=True,
+                          H=None, h8=None, g8=None, u8=None):
+    """H = bf16(G sigmoid(G) U) with its 8-bit blocks and those of G and U in
+    one pass; returns (H, h8, g8, u8), each None where not wanted."""
+    if G.dim() != 2:
+        raise QloraError("G must be a matrix")
+    M, F = G.shape
+    ldg, ldu = _rows(G, (M, F), "G"), _rows(U, (M, F), "U")
+    if want_h and H is None:
+        H = torch.empty(M, F, dtype=torch.bfloat16, device=G.device)
+    ldh = _rows(H, (M, F), "H") if H is not None else 0
+
+    def blocks(a, want, name):
+        if a is None:
+            return empty_act8(M, F, G.device, fmt) if want else None
+        if a.shape != (M, F):
+            raise QloraError(f"{name} must have the shape of G")
+        _need_act8(a, name)
+        a.fmt = int(fmt)
+        return a
+
+    h8 = blocks(h8, want_h8, "h8")
+    g8 = blocks(g8, want_checkpoint, "g8")
+    u8 = blocks(u8, want_checkpoint, "u8")
+    args = []
+    for a in (h8, g8, u8):
+        args += [_ptr(a.codes), _ptr(a.scales)] if a is not None else [None, None]
+    _check(LIB.qlora_swiglu_act8_fwd(_ptr(G), ldg, _ptr(U), ldu, M, F, int(fmt), _ptr(H), ldh, *args,
+                                     _stream()))
+    return H, h8, g8, u8
+
+
+def qlora_swiglu_act8_bwd(dH, g8, u8, dG=None, dU=None):
+    """(dG, dU) of the gated activation from the 8-bit blocks of G and U."""
+    _need_act8(g8, "g8")
+    _need_act8(u8, "u8")
+    if g8.shape != u8.shape or g8.fmt != u8.fmt:
+        raise QloraError("g8 and u8 must have one shape and one format")
+    M, F = g8.shape
+    lddh = _rows(dH, (M, F), "dH")
+    dG = dG if dG is not None else torch.empty(M, F, dtype=torch.bfloat16, device=dH.device)
+    dU = dU if dU is not None else torch.empty(M, F, dtype=torch.bfloat16, device=dH.device)
+    lddg, lddu = _rows(dG, (M, F), "dG"), _rows(dU, (M, F), "dU")
+    _check(LIB.qlora_swiglu_act8_bwd(_ptr(dH), lddh, _ptr(g8.codes), _ptr(g8.scales),
+                                     _ptr(u8.codes), _ptr(u8.scales), M, F, g8.fmt, _ptr(dG), lddg,
+                                     _ptr(dU), lddu, _stream()))
+    return dG, dU
+
+
+def qlora_act8_workspace_bytes(M, N, K, r):
+    return int(LIB.qlora_act8_workspace_bytes(M, N, K, r))
+
+
+def act8_workspace(M, N, K, r, device):
+    """Workspace of qlora_linear_bwd_act8 and the 8-bit weight's linear calls
+    (r = 0 without an adapter)."""
+    n = qlora_act8_workspace_bytes(M, N, K, r)
+    if n == 0:
+        raise QloraError(f"unsupported linear shape M={M} N={N} K={K} r={r}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _adapter(A, B, N, K):
+    """Rank of an adapter, checked; 0 without one."""
+    if A is None and B is None:
+        return 0
+    if A is None or B is None:
+        raise QloraError("A and B come together")
+    _need(A, torch.bfloat16, "A")
+    _need(B, torch.bfloat16, "B")
+    r = A.shape[1] if A.dim() == 2 else -1
+    if tuple(A.shape) != (K, r) or tuple(B.shape) != (r, N):
+        raise QloraError("A must be [K x r] and B [r x N]")
+    return r
+
+
+def _out(t, shape, dtype, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise QloraError(f"{name} must have shape {shape}")
+    return t
+
+
+def _given(t, shape, dtype, name):
+    if t is not None:
+        _need(t, dtype, name)
+        if tuple(t.shape) != shape:
+            raise QloraError(f"{name} must have shape {shape}")
+
+
+def qlora_linear_bwd_act8(dY, X8, T, W, A, B, scale, want_dX=True, keep_mask=None, p=0.0, dX=None,
+                          dA=None, dB=None, ws=None):
+    """qlora_linear_bwd from the 8-bit blocks of X (keep_mask and p: the
+    forward's LoRA dropout); returns (dX or None, dA, dB)."""
+    _need_act8(X8, "X8")
+    M, K = X8.shape
+    N = W.shape[0]
+    if tuple(W.shape) != (N, K):
+        raise QloraError("W must be [N x K] with the K of X8")
+    r = _adapter(A, B, N, K)
+    if r == 0:
+        raise QloraError("the backward of the NF4 layer needs its adapter")
+    _given(dY, (M, N), torch.bfloat16, "dY")
+    _given(T, (M, r), torch.float32, "T")
+    _given(keep_mask, (M, K // 32), torch.int32, "keep_mask")
+    dev = dY.device
+    dX = _out(dX, (M, K), torch.bfloat16, dev, "dX") if want_dX else None
+    dA = _out(dA, (K, r), torch.float32, dev, "dA")
+    dB = _out(dB, (r, N), torch.float32, dev, "dB")
+    ws = ws if ws is not None else act8_workspace(M, N, K, r, dev)
+    _check(LIB.qlora_linear_bwd_act8(_ptr(dY), _ptr(X8.codes), _ptr(X8.scales), X8.fmt, _ptr(T),
+                                     _ptr(W.codes), _ptr(W.absmax_q), _ptr(W.absmax_s2), _ptr(A),
+                                     _ptr(B), M, N, K, r, float(scale), _ptr(keep_mask), float(p),
+                                     _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
+                                     W.store_type, _stream()))
+    return dX, dA, dB
+
+
+def qlora_fp8_weight_quantize(W, transposed=True):
+    """A bf16 weight [N x K] in 128 x 128 blocks of E4M3 codes; `transposed`
+    keeps the other order too, which the input gradient reads."""
+    if W.dim() != 2:
+        raise QloraError("W must be a matrix")
+    _need(W, torch.bfloat16, "W")
+    N, K = W.shape
+
+    def pair(rows, cols):
+        return (torch.empty(rows, act8_row_bytes(cols), dtype=torch.uint8, device=W.device),
+                torch.empty((rows + 127) // 128, act8_scale_row_bytes(cols), dtype=torch.uint8,
+                            device=W.device))
+
+    codes, scales = pair(N, K)
+    codes_t, scales_t = pair(K, N) if transposed else (None, None)
+    _check(LIB.qlora_fp8_weight_quantize(_ptr(W), N, K, _ptr(codes), _ptr(scales), _ptr(codes_t),
+                                         _ptr(scales_t), _stream()))
+    return Fp8Weight(codes, scales, codes_t, scales_t, (N, K))
+
+
+def qlora_fp8_linear_fwd(X8, W, A=None, B=None, scale=1.0, want_T=True, Y=None, T=None, ws=None):
+    """Y = dec(X8) dec(W)^T + scale (dec(X8) A) B; returns (Y, T), T fp32 or
+    None. Without A and B it is the plain product."""
+    _need_act8(X8, "X8")
+    M, K = X8.shape
+    N = W.shape[0]
+    if W.shape != (N, K):
+        raise QloraError("W must be [N x K] with the K of X8")
+    _need_weight(W.codes, W.scales, N, K, "W")
+    r = _adapter(A, B, N, K)
+    dev = X8.codes.device
+    Y = _out(Y, (M, N), torch.bfloat16, dev, "Y")
+    T = _out(T, (M, r), torch.float32, dev, "T") if want_T and r else None
+    ws = ws if ws is not None else act8_workspace(M, N, K, r, dev)
+    _check(LIB.qlora_fp8_linear_fwd(_ptr(X8.codes), _ptr(X8.scales), X8.fmt, _ptr(W.codes),
+                                    _ptr(W.scales), _ptr(A), _ptr(B), M, N, K, r, float(scale),
+                                    _ptr(Y), _ptr(T), _ptr(ws), ws.numel(), _stream()))
+    return Y, T
+
+
+def qlora_fp8_linear_bwd(dY, X8, T, W, A=None, B=None, scale=1.0, fmt=ACT8_E4M3, want_dX=True,
+                         dX=None, dA=None, dB=None, ws=None):
+    """Backward of qlora_fp8_linear_fwd; dY enters dX in 8-bit blocks of
+    `fmt`. Returns (dX or None, dA, dB); without an adapter (dX, None, None),
+    and X8 may then be None."""
+    N, K = W.shape
+    r = _adapter(A, B, N, K)
+    if dY.dim() != 2:
+        raise QloraError("dY must be a matrix")
+    M = dY.shape[0]
+    _given(dY, (M, N), torch.bfloat16, "dY")
+    dev = dY.device
+    if r:
+        _need_act8(X8, "X8")
+        if X8.shape != (M, K):
+            raise QloraError("X8 must be [M x K]")
+        _given(T, (M, r), torch.float32, "T")
+        dA = _out(dA, (K, r), torch.float32, dev, "dA")
+        dB = _out(dB, (r, N), torch.float32, dev, "dB")
+    elif T is not None or dA is not None or dB is not None or not want_dX:
+        raise QloraError("without an adapter only dX is formed")
+    if want_dX:
+        _need_weight(W.codes_t, W.scales_t, K, N, "W transposed")
+        dX = _out(dX, (M, K), torch.bfloat16, dev, "dX")
+    else:
+        dX = None
+    x = (_ptr(X8.codes), _ptr(X8.scales), X8.fmt) if r else (None, None, ACT8_E4M3)
+    ws = ws if ws is not None else act8_workspace(M, N, K, r, dev)
+    _check(LIB.qlora_fp8_linear_bwd(_ptr(dY), int(fmt), *x, _ptr(T), _ptr(W.codes_t),
+                                    _ptr(W.scales_t), _ptr(A), _ptr(B), M, N, K, r, float(scale),
+                                    _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream()))
+    return dX, dA, dB

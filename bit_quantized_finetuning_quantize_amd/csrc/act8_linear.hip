@@ -1,0 +1,138 @@
+// The linear layer on 8-bit inputs: backward of the NF4 layer from an 8-bit
+// copy of its input, and forward and backward of a frozen weight held in
+// 8-bit blocks, both with a LoRA adapter beside it.
+//
+//   forward   T = dec(X8) A, split along K             row product
+//             T (float32), bf16(s T), B^T padded       one launch
+//             Y = dec(X8) dec(W8)^T + (s T) B          8-bit product
+//   backward  G = dY B^T, split along N                row product
+//             bf16(s G); s G and s T in three terms    one launch
+//             dX                                       NF4 contraction, or dY to
+//                                                      8 bits and the 8-bit product
+//             dA and dB                                column products, one launch
+#include "act8.h"
+#include "kernels.h"
+
+#include <algorithm>
+
+namespace qlora {
+
+namespace {
+
+#define QLORA_TRY(x)                       \
+  do {                                     \
+    hipError_t e_ = (x);                   \
+    if (e_ != hipSuccess) return e_;       \
+  } while (0)
+
+struct Ws8 {
+  int64_t r64;
+  size_t v, u, g3, t3, part, dy8, dys, total;
+};
+
+// Byte offsets in the workspace, 256-aligned. Each part grows with every
+// size (the split partials by their bound of one workgroup per compute
+// unit), so a workspace for a larger call serves a smaller one.
+Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
+  Ws8 w{};
+  w.r64 = ((int64_t)r + 63) / 64 * 64;
+  const int64_t Mp = (M + 63) / 64 * 64;
+  size_t off = 0;
+  auto take = [&](int64_t bytes) { size_t o = off; off += ((size_t)bytes + 255) / 256 * 256; return o; };
+  w.v = take(std::max(N, K) * w.r64 * 2);   // B^T or A, padded
+  w.u = take(Mp * w.r64 * 2);               // bf16(s T) or bf16(s G)
+  w.g3 = take(3 * w.r64 * Mp * 2);
+  w.t3 = take(3 * w.r64 * Mp * 2);
+  // splits * M * columns: 256 tiles of 64 x 64 at most, or one split
+  w.part = take(r ? std::max<int64_t>(256 * 64 * 64, Mp * w.r64) * 4 : 0);
+  w.dy8 = take(M * act8_row_bytes(N));
+  w.dys = take(M * act8_scale_row_bytes(N));
+  w.total = off;
+  return w;
+}
+
+struct Ptrs {
+  uint16_t *v, *u, *g3, *t3;
+  float* part;
+  uint8_t *dy8, *dys;
+};
+Ptrs carve(void* ws_, const Ws8& w) {
+  char* ws = reinterpret_cast<char*>(ws_);
+  auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
+  return Ptrs{at(w.v), at(w.u), at(w.g3), at(w.t3), reinterpret_cast<float*>(ws + w.part),
+              reinterpret_cast<uint8_t*>(ws + w.dy8), reinterpret_cast<uint8_t*>(ws + w.dys)};
+}
+
+// The adapter's rows serve as they are when they are whole 64-column tiles.
+bool in_place(const uint16_t* A, int r) {
+  return r % 64 == 0 && (reinterpret_cast<uintptr_t>(A) & 15) == 0;
+}
+
+// The adapter's part of a backward pass before dX: bf16(s G) in u, A padded
+// in v (unless it serves as it is), s G and s T in three terms.
+hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, const uint16_t* A,
+                     const uint16_t* B, int64_t M, int64_t N, int64_t K, int r, float scale,
+                     const Ptrs& w, const Dropout& dr, hipStream_t stream) {
+  const float f = dr.mask ? dr.keep_scale : 1.0f;
+  const int ldp = lowrank_cols(r);
+  int splits = 0;
+  if (!T) {  // recomputed from the 8-bit input
+    QLORA_TRY(launch_rows_act8(x, fmt, M, K, dr.mask, A, r, w.part, &splits, stream));
+    const LowrankOut t{w.part, splits, ldp, f, nullptr, nullptr, w.t3};
+    QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{}, M, r, scale, stream));
+  }
+  QLORA_TRY(launch_rows_bf16(dY, M, N, B, r, w.part, &splits, stream));
+  const LowrankOut o[2] = {{w.part, splits, ldp, f, nullptr, w.u, w.g3},
+                           {T, 1, r, 1.0f, nullptr, nullptr, w.t3}};
+  const LowrankPad pad = in_place(A, r) ? LowrankPad{} : LowrankPad{A, false, K, w.v};
+  return launch_lowrank_out(o, T ? 2 : 1, pad, M, r, scale, stream);
+}
+
+}  // namespace
+
+size_t act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
+  return ws8_layout(M, N, K, r).total;
+}
+
+hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, Nf4Weight W,
+                           const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K,
+                           int r, float scale, uint16_t* dX, float* dA, float* dB, void* ws,
+                           hipStream_t stream, Dropout dr) {
+  const Ws8 l = ws8_layout(M, N, K, r);
+  const Ptrs w = carve(ws, l);
+  QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, stream));
+  if (dX)
+    QLORA_TRY(launch_input_grad(dY, W, w.u, in_place(A, r) ? A : w.v, M, N, K, l.r64, dX, stream, dr));
+  return launch_columns(x, fmt, dr.mask, dY, w.g3, w.t3, M, N, K, r, dA, dB, stream);
+}
+
+hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A, const uint16_t* B,
+                          int64_t M, int64_t N, int64_t K, int r, float scale, uint16_t* Y,
+                          float* T_out, void* ws, hipStream_t stream) {
+  if (!r) return launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, stream);
+  const Ws8 l = ws8_layout(M, N, K, r);
+  const Ptrs w = carve(ws, l);
+  int splits = 0;
+  QLORA_TRY(launch_rows_act8(x, fmt, M, K, nullptr, A, r, w.part, &splits, stream));
+  const LowrankOut t{w.part, splits, lowrank_cols(r), 1.0f, T_out, w.u, nullptr};
+  QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{B, true, N, w.v}, M, r, scale, stream));
+  return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, stream);
+}
+
+hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, const float* T,
+                          ConstAct8 w8t, const uint16_t* A, const uint16_t* B, int64_t M, int64_t N,
+                          int64_t K, int r, float scale, uint16_t* dX, float* dA, float* dB,
+                          void* ws, hipStream_t stream) {
+  const Ws8 l = ws8_layout(M, N, K, r);
+  const Ptrs w = carve(ws, l);
+  if (r) QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, Dropout{}, stream));
+  if (dX) {
+    QLORA_TRY(launch_act8_quantize(dY, M, N, N, dyfmt, w.dy8, w.dys, stream));
+    QLORA_TRY(launch_fp8_gemm(ConstAct8{w.dy8, w.dys}, dyfmt, w8t, M, K, N, r ? w.u : nullptr,
+                              r ? (in_place(A, r) ? A : w.v) : nullptr, (int)l.r64, dX, stream));
+  }
+  if (!r) return hipSuccess;
+  return launch_columns(x, fmt, nullptr, dY, w.g3, w.t3, M, N, K, r, dA, dB, stream);
+}
+
+}  // namespace qlora

@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "../../include/qlora.h"
+#include "act8.h"
 #include "common.h"
 #include "kernels.h"
 
@@ -66,6 +67,42 @@ int check_dropout(const uint32_t* mask, float p, qlora::Dropout* dr) {
   if (!aligned(mask, 4)) return QLORA_ERR_UNSUPPORTED;
   dr->mask = mask;
   dr->keep_scale = (float)(65536.0 / (double)(65536 - thr));
+  return QLORA_OK;
+}
+
+bool valid_fmt(int32_t f) { return f == QLORA_ACT8_E4M3 || f == QLORA_ACT8_E5M2; }
+
+// Shape of a matrix in 8-bit blocks: one lane group per block of 128 in one
+// launch (32-bit block index), and rows that 32-bit offsets can reach.
+int check_act8_shape(int64_t M, int64_t K) {
+  if (M <= 0 || K <= 0) return QLORA_ERR_INVALID_ARG;
+  if (M > (int64_t)1 << 30 || K > (int64_t)1 << 21) return QLORA_ERR_UNSUPPORTED;
+  const int64_t kb = (K + QLORA_ACT8_BLOCK - 1) / QLORA_ACT8_BLOCK;
+  if (M * kb > (int64_t)1 << 30) return QLORA_ERR_UNSUPPORTED;
+  return QLORA_OK;
+}
+
+int check_act8(const uint8_t* codes, const uint8_t* scales) {
+  if (!codes || !scales) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(scales, 4)) return QLORA_ERR_UNSUPPORTED;
+  return QLORA_OK;
+}
+
+// Shapes of the linear calls on 8-bit inputs; r = 0 is a call without an adapter.
+int check_fp8_shape(int64_t M, int64_t N, int64_t K, int32_t r) {
+  if (M <= 0 || N <= 0 || K <= 0) return QLORA_ERR_INVALID_ARG;
+  if (r) {
+    const int st = check_linear_shape(M, N, K, r);
+    // the three-term factors of dA and dB, [3][r][M] bf16, have 32-bit offsets
+    if (st == QLORA_OK && (M + 63) / 64 * ((r + 63) / 64) >= (int64_t)1 << 16)
+      return QLORA_ERR_UNSUPPORTED;
+    return st;
+  }
+  if (N > (int64_t)1 << 21 || K > (int64_t)1 << 21 || M > (int64_t)1 << 30)
+    return QLORA_ERR_UNSUPPORTED;
+  const int64_t np = (N + 127) / 128 * 128, kp = (K + 127) / 128 * 128;
+  if (M * np >= (int64_t)1 << 30 || M * kp >= (int64_t)1 << 30 || np * kp >= (int64_t)1 << 32)
+    return QLORA_ERR_UNSUPPORTED;
   return QLORA_OK;
 }
 
@@ -380,6 +417,179 @@ int qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* X, const float*
   return hip_status(qlora::launch_bwd(dY, X, T, W, A, B, M, N, K, r, scale, dX, dA, dB, ws,
                                       reinterpret_cast<hipStream_t>(stream), nullptr, nullptr,
                                       dr));
+}
+
+int64_t qlora_act8_row_bytes(int64_t K) { return K < 0 ? -1 : qlora::act8_row_bytes(K); }
+int64_t qlora_act8_scale_row_bytes(int64_t K) {
+  return K < 0 ? -1 : qlora::act8_scale_row_bytes(K);
+}
+
+int qlora_act8_quantize(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, int32_t fmt,
+                        uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!X || !valid_fmt(fmt)) return QLORA_ERR_INVALID_ARG;
+  int st = check_act8_shape(M, K);
+  if (st != QLORA_OK) return st;
+  if (ldx < K) return QLORA_ERR_INVALID_ARG;
+  st = check_act8(codes, scales);
+  if (st != QLORA_OK) return st;
+  if (!aligned(X, 2)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_act8_quantize(X, M, K, ldx, fmt, codes, scales,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_act8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K,
+                          int32_t fmt, uint16_t* X, int64_t ldx, void* stream) {
+  if (!X || !valid_fmt(fmt)) return QLORA_ERR_INVALID_ARG;
+  int st = check_act8_shape(M, K);
+  if (st != QLORA_OK) return st;
+  if (ldx < K) return QLORA_ERR_INVALID_ARG;
+  st = check_act8(codes, scales);
+  if (st != QLORA_OK) return st;
+  if (!aligned(X, 2)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_act8_dequantize(codes, scales, M, K, fmt, X, ldx,
+                                                  reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_swiglu_act8_fwd(const uint16_t* G, int64_t ldg, const uint16_t* U, int64_t ldu, int64_t M,
+                          int64_t F, int32_t fmt, uint16_t* H, int64_t ldh, uint8_t* h_codes,
+                          uint8_t* h_scales, uint8_t* g_codes, uint8_t* g_scales, uint8_t* u_codes,
+                          uint8_t* u_scales, void* stream) {
+  if (!G || !U || !valid_fmt(fmt)) return QLORA_ERR_INVALID_ARG;
+  int st = check_act8_shape(M, F);
+  if (st != QLORA_OK) return st;
+  if (ldg < F || ldu < F || (H && ldh < F)) return QLORA_ERR_INVALID_ARG;
+  // each 8-bit output comes whole or not at all, and there is some output
+  const uint8_t* pairs[3][2] = {{h_codes, h_scales}, {g_codes, g_scales}, {u_codes, u_scales}};
+  bool any = H != nullptr;
+  for (const auto& p : pairs) {
+    if (!p[0] && !p[1]) continue;
+    st = check_act8(p[0], p[1]);
+    if (st != QLORA_OK) return st;
+    any = true;
+  }
+  if (!any) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(G, 2) || !aligned(U, 2) || !aligned(H, 2)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_swiglu_act8_fwd(
+      G, ldg, U, ldu, M, F, fmt, H, ldh, qlora::Act8{h_codes, h_scales},
+      qlora::Act8{g_codes, g_scales}, qlora::Act8{u_codes, u_scales},
+      reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_swiglu_act8_bwd(const uint16_t* dH, int64_t lddh, const uint8_t* g_codes,
+                          const uint8_t* g_scales, const uint8_t* u_codes, const uint8_t* u_scales,
+                          int64_t M, int64_t F, int32_t fmt, uint16_t* dG, int64_t lddg,
+                          uint16_t* dU, int64_t lddu, void* stream) {
+  if (!dH || !dG || !dU || !valid_fmt(fmt)) return QLORA_ERR_INVALID_ARG;
+  int st = check_act8_shape(M, F);
+  if (st != QLORA_OK) return st;
+  if (lddh < F || lddg < F || lddu < F) return QLORA_ERR_INVALID_ARG;
+  st = check_act8(g_codes, g_scales);
+  if (st == QLORA_OK) st = check_act8(u_codes, u_scales);
+  if (st != QLORA_OK) return st;
+  if (!aligned(dH, 2) || !aligned(dG, 2) || !aligned(dU, 2)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_swiglu_act8_bwd(
+      dH, lddh, qlora::ConstAct8{g_codes, g_scales}, qlora::ConstAct8{u_codes, u_scales}, M, F, fmt,
+      dG, lddg, dU, lddu, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, uint8_t* codes,
+                              uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, void* stream) {
+  if (!W || N <= 0 || K <= 0) return QLORA_ERR_INVALID_ARG;
+  if (N > (int64_t)1 << 21 || K > (int64_t)1 << 21 ||
+      (N + 127) / 128 * ((K + 127) / 128) >= (int64_t)1 << 18)
+    return QLORA_ERR_UNSUPPORTED;
+  int st = check_act8(codes, scales);
+  if (st == QLORA_OK && (codes_t || scales_t)) st = check_act8(codes_t, scales_t);
+  if (st != QLORA_OK) return st;
+  if (!aligned(W, 2)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_fp8_weight_quantize(W, N, K, qlora::Act8{codes, scales},
+                                                      qlora::Act8{codes_t, scales_t},
+                                                      reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
+  if (check_fp8_shape(M, N, K, r) != QLORA_OK) return 0;
+  return qlora::act8_workspace_bytes(M, N, K, r);
+}
+
+static int check_act8_ws(int64_t M, int64_t N, int64_t K, int32_t r, const void* ws,
+                         size_t ws_bytes) {
+  if (!ws || ws_bytes < qlora::act8_workspace_bytes(M, N, K, r)) return QLORA_ERR_WORKSPACE;
+  return aligned(ws, 256) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
+}
+
+int qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* x_codes, const uint8_t* x_scales,
+                          int32_t fmt, const float* T, const uint8_t* codes,
+                          const uint8_t* absmax_q, const float* absmax_s2, const uint16_t* A,
+                          const uint16_t* B, int64_t M, int64_t N, int64_t K, int32_t r,
+                          float scale, const uint32_t* keep_mask, float p, uint16_t* dX, float* dA,
+                          float* dB, void* ws, size_t ws_bytes, int32_t store_type, void* stream) {
+  if (!dY || !A || !B || !dA || !dB || !valid_fmt(fmt)) return QLORA_ERR_INVALID_ARG;
+  if (!valid_store_type(store_type)) return QLORA_ERR_INVALID_ARG;
+  int st = check_act8(x_codes, x_scales);
+  // the weight is read for dX only
+  if (st == QLORA_OK && dX) st = check_store(codes, absmax_q, absmax_s2);
+  if (st == QLORA_OK && M > 0 && N > 0 && K > 0 && r == 0) st = QLORA_ERR_UNSUPPORTED;
+  if (st == QLORA_OK) st = check_fp8_shape(M, N, K, r);
+  if (st != QLORA_OK) return st;
+  qlora::Dropout dr;
+  if (keep_mask) {
+    st = check_dropout(keep_mask, p, &dr);
+    if (st != QLORA_OK) return st;
+    if (dX && r > QLORA_MAX_DROPOUT_RANK) return QLORA_ERR_UNSUPPORTED;
+  }
+  if (!aligned(dY, 16) || !aligned(B, 16) || !aligned(A, 2) || (T && !aligned(T, 4)) ||
+      (dX && !aligned(dX, 2)) || !aligned(dA, 4) || !aligned(dB, 4))
+    return QLORA_ERR_UNSUPPORTED;
+  st = check_act8_ws(M, N, K, r, ws, ws_bytes);
+  if (st != QLORA_OK) return st;
+  qlora::Nf4Weight W{codes, absmax_q, absmax_s2, store_type};
+  return hip_status(qlora::launch_bwd_act8(dY, qlora::ConstAct8{x_codes, x_scales}, fmt, T, W, A, B,
+                                           M, N, K, r, scale, dX, dA, dB, ws,
+                                           reinterpret_cast<hipStream_t>(stream), dr));
+}
+
+int qlora_fp8_linear_fwd(const uint8_t* x_codes, const uint8_t* x_scales, int32_t fmt,
+                         const uint8_t* w_codes, const uint8_t* w_scales, const uint16_t* A,
+                         const uint16_t* B, int64_t M, int64_t N, int64_t K, int32_t r, float scale,
+                         uint16_t* Y, float* T_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!Y || !valid_fmt(fmt)) return QLORA_ERR_INVALID_ARG;
+  if (r ? (!A || !B) : (A || B || T_out)) return QLORA_ERR_INVALID_ARG;
+  int st = check_act8(x_codes, x_scales);
+  if (st == QLORA_OK) st = check_act8(w_codes, w_scales);
+  if (st == QLORA_OK) st = check_fp8_shape(M, N, K, r);
+  if (st != QLORA_OK) return st;
+  if (!aligned(B, 16) || !aligned(A, 2) || !aligned(Y, 2) || !aligned(T_out, 4))
+    return QLORA_ERR_UNSUPPORTED;
+  st = check_act8_ws(M, N, K, r, ws, ws_bytes);
+  if (st != QLORA_OK) return st;
+  return hip_status(qlora::launch_fp8_fwd(qlora::ConstAct8{x_codes, x_scales}, fmt,
+                                          qlora::ConstAct8{w_codes, w_scales}, A, B, M, N, K, r,
+                                          scale, Y, T_out, ws,
+                                          reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_fp8_linear_bwd(const uint16_t* dY, int32_t dy_fmt, const uint8_t* x_codes,
+                         const uint8_t* x_scales, int32_t fmt, const float* T,
+                         const uint8_t* w_codes_t, const uint8_t* w_scales_t, const uint16_t* A,
+                         const uint16_t* B, int64_t M, int64_t N, int64_t K, int32_t r, float scale,
+                         uint16_t* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
+                         void* stream) {
+  if (!dY || !valid_fmt(fmt) || !valid_fmt(dy_fmt)) return QLORA_ERR_INVALID_ARG;
+  if (r ? (!A || !B || !dA || !dB) : (A || B || T || dA || dB || !dX)) return QLORA_ERR_INVALID_ARG;
+  int st = r ? check_act8(x_codes, x_scales) : QLORA_OK;
+  if (st == QLORA_OK && dX) st = check_act8(w_codes_t, w_scales_t);
+  if (st == QLORA_OK) st = check_fp8_shape(M, N, K, r);
+  if (st != QLORA_OK) return st;
+  if (!aligned(dY, r ? 16 : 2) || !aligned(B, 16) || !aligned(A, 2) || !aligned(T, 4) ||
+      !aligned(dX, 2) || !aligned(dA, 4) || !aligned(dB, 4))
+    return QLORA_ERR_UNSUPPORTED;
+  st = check_act8_ws(M, N, K, r, ws, ws_bytes);
+  if (st != QLORA_OK) return st;
+  return hip_status(qlora::launch_fp8_bwd(dY, dy_fmt, qlora::ConstAct8{x_codes, x_scales}, fmt, T,
+                                          qlora::ConstAct8{w_codes_t, w_scales_t}, A, B, M, N, K, r,
+                                          scale, dX, dA, dB, ws,
+                                          reinterpret_cast<hipStream_t>(stream)));
 }
 
 int qlora_gemv_wait_limit(int64_t microseconds) {

@@ -98,6 +98,97 @@ hipError_t launch_bwd(const uint16_t* dY, const uint16_t* X, const float* T,
                       hipStream_t stream, hipEvent_t ev0 = nullptr,
                       hipEvent_t ev1 = nullptr, Dropout dr = Dropout{});
 
+// dX = dY W' + sg apad^T with sg = bf16(s G) [M x r64] (zero past r) and
+// apad = A padded to [K x r64]; under dropout the second term passes the mask.
+hipError_t launch_input_grad(const uint16_t* dY, Nf4Weight W, const uint16_t* sg,
+                             const uint16_t* apad, int64_t M, int64_t N, int64_t K, int64_t r64,
+                             uint16_t* dX, hipStream_t stream, Dropout dr = Dropout{});
+
+// ---- 8-bit blocks -------------------------------------------------------------
+
+struct Act8 {
+  uint8_t* codes;
+  uint8_t* scales;
+};
+struct ConstAct8 {
+  const uint8_t* codes;
+  const uint8_t* scales;
+};
+
+// fmt: 0 E4M3, 1 E5M2 (include/qlora.h, "8-bit blocks"); ld: elements between rows.
+hipError_t launch_act8_quantize(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, int fmt,
+                                uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_act8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K,
+                                  int fmt, uint16_t* X, int64_t ldx, hipStream_t stream);
+hipError_t launch_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, Act8 w8, Act8 w8t,
+                                      hipStream_t stream);
+hipError_t launch_swiglu_act8_fwd(const uint16_t* g, int64_t ldg, const uint16_t* u, int64_t ldu,
+                                  int64_t M, int64_t F, int fmt, uint16_t* h, int64_t ldh, Act8 h8,
+                                  Act8 g8, Act8 u8, hipStream_t stream);
+hipError_t launch_swiglu_act8_bwd(const uint16_t* dh, int64_t lddh, ConstAct8 g8, ConstAct8 u8,
+                                  int64_t M, int64_t F, int fmt, uint16_t* dg, int64_t lddg,
+                                  uint16_t* du, int64_t lddu, hipStream_t stream);
+
+// Y [M x N] = dec(x) dec(w)^T + U V^T; x [M x K], w [N x K] in 128 x 128
+// blocks (E4M3), U bf16 [M x r64] and V bf16 [N x r64] or null.
+hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
+                           const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
+                           hipStream_t stream);
+
+// The adapter's products beside an 8-bit input (lowrank8.hip).
+// Columns of a low-rank partial or term matrix: r rounded up to 16, 32 or a
+// multiple of 64.
+int lowrank_cols(int r);
+// Split partials [splits][M][lowrank_cols(r)] of D(dec x) A (A [K x r]) and
+// of S B^T (S bf16 [M x C], B [r x C]); K and C multiples of 64, at most
+// max(256 * 64 * 64, M * lowrank_cols(r)) elements with M rounded up to 64.
+hipError_t launch_rows_act8(ConstAct8 x, int fmt, int64_t M, int64_t K, const uint32_t* mask,
+                            const uint16_t* A, int r, float* part, int* splits, hipStream_t stream);
+hipError_t launch_rows_bf16(const uint16_t* S, int64_t M, int64_t C, const uint16_t* B, int r,
+                            float* part, int* splits, hipStream_t stream);
+// V = f * (sum of partials, rows ldp apart), as float32 [M x r], as bf16(s V)
+// [Mp x r64], and as three bf16 terms of s V [3][lowrank_cols(r)][Mp]; each
+// output may be null. Up to two of them and one padded copy per launch:
+// dst [rows x r64] from src [rows x r], or from the columns of src [r x rows].
+struct LowrankOut {
+  const float* part;
+  int splits;
+  int64_t ldp;
+  float f;
+  float* out32;
+  uint16_t* u;
+  uint16_t* v3;
+};
+struct LowrankPad {
+  const uint16_t* src = nullptr;
+  bool columns = false;
+  int64_t rows = 0;
+  uint16_t* dst = nullptr;
+};
+hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_t M, int r, float s,
+                              hipStream_t stream);
+// dA = D(dec x)^T g, dB = t^T dY from the three-term g and t.
+hipError_t launch_columns(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY,
+                          const uint16_t* g3, const uint16_t* t3, int64_t M, int64_t N, int64_t K,
+                          int r, float* dA, float* dB, hipStream_t stream);
+
+// Workspace of the three calls below (r may be 0 for the 8-bit weight's).
+size_t act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
+// launch_bwd with the input in 8-bit blocks.
+hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, Nf4Weight W,
+                           const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K,
+                           int r, float scale, uint16_t* dX, float* dA, float* dB, void* ws,
+                           hipStream_t stream, Dropout dr = Dropout{});
+// Y = dec(x) dec(w)^T + s T B, T = dec(x) A (no adapter when r = 0).
+hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w, const uint16_t* A, const uint16_t* B,
+                          int64_t M, int64_t N, int64_t K, int r, float scale, uint16_t* Y,
+                          float* T_out, void* ws, hipStream_t stream);
+// dX = dec(q(dY)) dec(w) + s G A^T, dA = s dec(x)^T G, dB = s T^T dY; w^T given.
+hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, const float* T,
+                          ConstAct8 w_t, const uint16_t* A, const uint16_t* B, int64_t M, int64_t N,
+                          int64_t K, int r, float scale, uint16_t* dX, float* dA, float* dB,
+                          void* ws, hipStream_t stream);
+
 // Forward with the library's own scratch array (one per device, this many
 // bytes) in place of a caller workspace.
 constexpr size_t kNoAllocScratchBytes = (size_t)32 << 20;

@@ -108,6 +108,11 @@ enum {
 #define QLORA_STORE_FP4 1
 #define QLORA_STORE_DQ_FP8 2
 
+/* 8-bit code formats of the 8-bit blocks (see "8-bit blocks"). */
+#define QLORA_ACT8_E4M3 0
+#define QLORA_ACT8_E5M2 1
+#define QLORA_ACT8_BLOCK 128
+
 #define QLORA_NF4_BLOCK 64
 #define QLORA_NF4_GROUP 256
 #define QLORA_MAX_RANK 256
@@ -467,6 +472,148 @@ int qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* X, const float*
                              int32_t r, float scale, const uint32_t* keep_mask, float p,
                              uint16_t* dX, float* dA, float* dB, void* ws,
                              size_t ws_bytes, void* stream);
+
+/* ---- 8-bit blocks --------------------------------------------------------------
+ * Activations and frozen weights in 8 bits. A finetuning step keeps the
+ * input of every linear for dA; held in 8-bit blocks it takes half the
+ * memory of bf16, and the same copy is the left operand of the 8-bit
+ * weight's product below.
+ *
+ * A matrix [M x K] is stored in two buffers:
+ *   codes   uint8 [M][qlora_act8_row_bytes(K)]        K rounded up to 128;
+ *           8-bit floating-point codes, 0 past column K
+ *   scales  uint8 [M][qlora_act8_scale_row_bytes(K)]  ceil(K/128) rounded up
+ *           to a multiple of 4; the byte e + 127 of the scale 2^e of each run
+ *           of 128 columns of a row, 0 past the last block
+ * The code formats are the OCP 8-bit floats, E4M3 (QLORA_ACT8_E4M3, largest
+ * value 448) and E5M2 (QLORA_ACT8_E5M2, 57344). Per block, over its finite
+ * values:
+ *   e    = the least integer >= -110 with max|x| <= top 2^e (top the largest value)
+ *   code = the nearest code of x 2^-e, ties to even
+ *   dec  = value(code) 2^e
+ * x 2^-e is exact, so the codes are defined bit for bit, and dec is an exact
+ * bf16 value (e >= -110 keeps it normal). Nothing finite saturates. A NaN
+ * becomes a NaN code; an infinity becomes an infinity in E5M2 and a NaN in
+ * E4M3, which has none. A scale byte lies in [17, 247].
+ *
+ * A weight W [N x K] has one scale per 128 x 128 block:
+ *   codes    uint8 [N][qlora_act8_row_bytes(K)], E4M3
+ *   scales   uint8 [ceil(N/128)][qlora_act8_scale_row_bytes(K)]
+ * and, for the input gradient, the same codes in the other order:
+ *   codes_t  uint8 [K][qlora_act8_row_bytes(N)]
+ *   scales_t uint8 [ceil(K/128)][qlora_act8_scale_row_bytes(N)]
+ *
+ * Every codes pointer is 16-byte and every scales pointer 4-byte aligned.
+ * Row counts are at most 2^30, K at most 2^21, M ceil(K/128) at most 2^30. */
+int64_t qlora_act8_row_bytes(int64_t K);       /* -1 if K < 0 */
+int64_t qlora_act8_scale_row_bytes(int64_t K); /* -1 if K < 0 */
+
+/* qlora_act8_quantize — the 8-bit blocks of bf16 X [M x K], rows ldx >= K
+ * elements apart (any 2-byte alignment; 16-byte aligned rows read faster).
+ * qlora_act8_dequantize — their values as bf16, rows ldx >= K apart.
+ * Errors: INVALID_ARG (null pointer, M or K not positive, ldx < K, fmt not
+ * one of the two); UNSUPPORTED (a size or alignment outside the above). */
+int qlora_act8_quantize(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, int32_t fmt,
+                        uint8_t* codes, uint8_t* scales, void* stream);
+int qlora_act8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K,
+                          int32_t fmt, uint16_t* X, int64_t ldx, void* stream);
+
+/* qlora_swiglu_act8_fwd — the activation of a gated MLP with its 8-bit
+ * checkpoints in the same pass: with s(g) = 1 / (1 + exp(-g)),
+ *   H = bf16( G s(G) U ),   h_* = 8-bit blocks of H (what
+ * qlora_act8_quantize gives for it: the down projection's input),
+ * g_*, u_* = 8-bit blocks of G and U (what the backward reads).
+ *   G, U  device bf16 [M x F], rows ldg, ldu >= F elements apart (the two
+ *         halves of one [M x 2F] buffer, for example)
+ *   H     device bf16 [M x F], rows ldh >= F apart, or NULL
+ *   h_*, g_*, u_*  device; each pair may be NULL. At least one output.
+ * Arithmetic in float32. H may alias G or U row for row (same leading
+ * dimension and base).
+ * qlora_swiglu_act8_bwd — the gradients from the 8-bit g and u:
+ *   dG = bf16( dH u s(g) (1 + g (1 - s(g))) ),   dU = bf16( dH g s(g) ).
+ * dG or dU may alias dH in the same way.
+ * Errors: INVALID_ARG (null required pointer, half a pair, no output, M or F
+ * not positive, a leading dimension below F, unknown fmt); UNSUPPORTED (a
+ * size or alignment outside the above). */
+int qlora_swiglu_act8_fwd(const uint16_t* G, int64_t ldg, const uint16_t* U, int64_t ldu,
+                          int64_t M, int64_t F, int32_t fmt, uint16_t* H, int64_t ldh,
+                          uint8_t* h_codes, uint8_t* h_scales, uint8_t* g_codes,
+                          uint8_t* g_scales, uint8_t* u_codes, uint8_t* u_scales, void* stream);
+int qlora_swiglu_act8_bwd(const uint16_t* dH, int64_t lddh, const uint8_t* g_codes,
+                          const uint8_t* g_scales, const uint8_t* u_codes,
+                          const uint8_t* u_scales, int64_t M, int64_t F, int32_t fmt,
+                          uint16_t* dG, int64_t lddg, uint16_t* dU, int64_t lddu, void* stream);
+
+/* qlora_fp8_weight_quantize — a frozen weight in 128 x 128 blocks (E4M3) from
+ * bf16 W [N x K]; the transposed pair may be NULL (forward only). N and K at
+ * most 2^21, fewer than 2^18 blocks.
+ * Errors: INVALID_ARG (null W, codes or scales, half of the transposed pair,
+ * N or K not positive); UNSUPPORTED (a size or alignment outside the above). */
+int qlora_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, uint8_t* codes,
+                              uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, void* stream);
+
+/* Workspace of the three linear calls below: at least
+ *   qlora_act8_workspace_bytes(M, N, K, r)
+ * bytes of device memory, 256-byte aligned, as for the NF4 linear calls.
+ * r = 0 is the workspace of a call without an adapter. 0 for a shape the
+ * calls reject: those of the NF4 linear calls (for r = 0 N and K need not be
+ * multiples of 64 and the limits hold for them rounded up to 128), and
+ * ceil(M/64) ceil(r/64) at or above 2^16. */
+size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
+
+/* qlora_linear_bwd_act8 — qlora_linear_bwd (and, with a keep mask,
+ * qlora_linear_bwd_dropout) from the input's 8-bit blocks: X is dec(x_*)
+ * throughout, in dA and in T where it is recomputed.
+ *   x_codes, x_scales, fmt  8-bit blocks of X [M x K]
+ *   T          the forward's T_out, or NULL to recompute it from dec(x_*)
+ *   keep_mask  device uint32 [M x K/32] or NULL (no dropout; p is ignored)
+ *   codes, absmax_q, absmax_s2, store_type  as qlora_linear_bwd_ex; read for
+ *              dX only, and may be NULL when dX is
+ * dA and dB are accurate to float32: the float32 factors s G and s T enter
+ * the matrix products as three bf16 terms. dX is qlora_linear_bwd's: s G enters
+ * it as bf16.
+ * Errors: as qlora_linear_bwd_ex and qlora_linear_bwd_dropout; INVALID_ARG
+ * also for an unknown fmt or null x_codes / x_scales. */
+int qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* x_codes, const uint8_t* x_scales,
+                          int32_t fmt, const float* T, const uint8_t* codes,
+                          const uint8_t* absmax_q, const float* absmax_s2, const uint16_t* A,
+                          const uint16_t* B, int64_t M, int64_t N, int64_t K, int32_t r,
+                          float scale, const uint32_t* keep_mask, float p, uint16_t* dX,
+                          float* dA, float* dB, void* ws, size_t ws_bytes, int32_t store_type,
+                          void* stream);
+
+/* qlora_fp8_linear_fwd — a frozen linear layer with its weight in 8-bit
+ * blocks:
+ *   Y = bf16( dec(x) dec(w)^T + scale * T B ),   T = dec(x) A (float32)
+ * Products accumulate in float32; s T enters the second product as bf16.
+ * r = 0 with A, B and T_out NULL is the plain product, for any M, N, K >= 1;
+ * with an adapter N and K are multiples of 64 and r is in [1, 256].
+ *   Y      device bf16 [M x N];  T_out  device float [M x r] or NULL
+ * Errors: INVALID_ARG (null pointer, A, B or T_out given with r = 0, sizes
+ * not positive, unknown fmt); UNSUPPORTED (as qlora_linear_fwd; for r = 0
+ * the same limits on the sizes rounded up to 128); WORKSPACE. */
+int qlora_fp8_linear_fwd(const uint8_t* x_codes, const uint8_t* x_scales, int32_t fmt,
+                         const uint8_t* w_codes, const uint8_t* w_scales, const uint16_t* A,
+                         const uint16_t* B, int64_t M, int64_t N, int64_t K, int32_t r,
+                         float scale, uint16_t* Y, float* T_out, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* qlora_fp8_linear_bwd — its backward pass; the frozen weight gets no
+ * gradient:
+ *   G  = dY B^T
+ *   dX = bf16( dec(q(dY)) dec(w) + scale * G A^T ), q(dY) the 8-bit blocks of
+ *        dY in dy_fmt (formed in the workspace); NULL dX skips it
+ *   dA = scale * dec(x)^T G,   dB = scale * T^T dY   (float32, from bf16 dY)
+ *   T  the forward's T_out, or NULL to recompute it
+ * The transposed weight buffers are read, for dX only. With r = 0 only dX is
+ * formed: A, B, T, dA and dB are NULL, the x buffers are not read and may be.
+ * Errors: as qlora_fp8_linear_fwd. */
+int qlora_fp8_linear_bwd(const uint16_t* dY, int32_t dy_fmt, const uint8_t* x_codes,
+                         const uint8_t* x_scales, int32_t fmt, const float* T,
+                         const uint8_t* w_codes_t, const uint8_t* w_scales_t, const uint16_t* A,
+                         const uint16_t* B, int64_t M, int64_t N, int64_t K, int32_t r,
+                         float scale, uint16_t* dX, float* dA, float* dB, void* ws,
+                         size_t ws_bytes, void* stream);
 
 /* qlora_gemv_wait_limit — how long, in microseconds, the row-tile
  * workgroups of a small-M forward (M <= 16) wait for the workgroups of the

@@ -1,0 +1,316 @@
+"""The 8-bit weight's linear layer and the NF4 backward from an 8-bit input
+on the GPU, against float64 products of the oracle's decoded matrices.
+
+Bounds, elementwise and derived: a float32 sum of n products taken in pieces
+of 64 is off by at most (n / 64 + 64) 2^-24 times the sum of magnitudes; the
+8-bit matrix instruction cuts each product at 2^-13 of the largest in its
+group of eight before it adds in float32, 7 2^-13 of the group's sum of
+magnitudes at most (the products next to the largest), and about 1e-5 of it
+on random data, so the norm of the error is held to bf16's own rounding; a
+factor rounded to bf16 (8 significant bits) adds 2^-8 of its term; a bf16 result 2^-8 of itself."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import act8
+from tests.gpu_util import device, host_f32
+
+pytestmark = pytest.mark.gpu
+
+E24 = 2.0 ** -24
+
+
+def _steps(n):
+    return (n / 64 + 64) * E24
+
+
+def _steps8(n):
+    return _steps(n) + 7 * 2.0 ** -13
+
+
+def _norm(got, want, label):
+    """bf16 rounding alone is 2^-8 / sqrt(3) = 2.26e-3 of the norm at most."""
+    e = np.linalg.norm(got - want) / max(np.linalg.norm(want), 1e-300)
+    assert e <= 2.5e-3, f"{label}: norm of the error {e:.2e}"
+
+
+@pytest.fixture(scope="module")
+def q():
+    device()
+    import bit_quantized_finetuning_quantize_amd as q
+    return q
+
+
+def _f64(t):
+    return host_f32(t).astype(np.float64)
+
+
+def _check(got, want, tol, label):
+    bad = ~(np.abs(got - want) <= tol)
+    worst = float(np.max(np.abs(got - want) / np.maximum(tol, 1e-300)))
+    print(f"[parity] {label}: {worst:.3f} of the bound", flush=True)
+    assert not bad.any(), f"{label}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}"
+
+
+def _dec(codes, scales, K, fmt, rows=1):
+    return act8.dequantize(codes.cpu().numpy(), scales.cpu().numpy(), K, fmt, rows)
+
+
+class Case:
+    def __init__(self, q, M, N, K, r, fmt=0, seed=0, dy=1e-3):
+        dev = device()
+        g = torch.Generator(device=dev)
+        g.manual_seed(seed + M * 7 + N * 3 + K)
+        rnd = lambda *s: torch.randn(s, generator=g, device=dev)  # noqa: E731
+        x = rnd(M, K)
+        x[:, ::97] *= 30
+        self.x8 = q.qlora_act8_quantize(x.to(torch.bfloat16), fmt)
+        self.W = (rnd(N, K) * 0.02).to(torch.bfloat16)
+        self.A = (rnd(K, r) * 0.05).to(torch.bfloat16) if r else None
+        self.B = (rnd(r, N) * 0.05).to(torch.bfloat16) if r else None
+        self.dY = (rnd(M, N) * dy).to(torch.bfloat16)
+        self.s = 2.0
+        self.X = _dec(self.x8.codes, self.x8.scales, K, fmt)
+        if r:
+            self.a, self.b = _f64(self.A), _f64(self.B)
+        self.dy = _f64(self.dY)
+
+
+def _fwd_check(c, W, Y, T, N, K, r):
+    w = _dec(W.codes, W.scales, K, 0, 128)
+    X = c.X
+    want = X @ w.T
+    tol = _steps8(K) * (np.abs(X) @ np.abs(w).T)
+    if r:
+        t = X @ c.a
+        ttol = _steps(K) * (np.abs(X) @ np.abs(c.a))
+        _check(_f64(T), t, ttol, "T")
+        want = want + c.s * (t @ c.b)
+        tol = tol + c.s * ((2.0 ** -8 * np.abs(t) + 2 * ttol) @ np.abs(c.b)) \
+            + _steps(r) * c.s * (np.abs(t) @ np.abs(c.b))
+    _check(_f64(Y), want, tol + 2.0 ** -8 * 1.01 * np.abs(want) + 1e-38, "Y")
+    _norm(_f64(Y), want, "Y")
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 4096, 4096), (2, 17, 129), (16, 256, 384),
+                                   (5, 1000, 1544), (17, 130, 640), (33, 64, 4096), (64, 300, 127),
+                                   (129, 257, 1025), (333, 1001, 1544), (300, 520, 2176)])
+def test_plain_product(q, M, N, K, fmt):
+    print(f"[case] fp8 product M={M} N={N} K={K} fmt={fmt}", flush=True)
+    c = Case(q, M, N, K, 0, fmt)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    Y, T = q.qlora_fp8_linear_fwd(c.x8, W)
+    assert T is None
+    _fwd_check(c, W, Y, T, N, K, 0)
+    # the input gradient: dY in either format against the transposed weight
+    for dfmt in (0, 1):
+        dX, dA, dB = q.qlora_fp8_linear_bwd(c.dY, None, None, W, fmt=dfmt)
+        assert dA is None and dB is None
+        w = _dec(W.codes_t, W.scales_t, N, 0, 128)
+        d = act8.dequantize(*act8.quantize(c.dy, dfmt), N, dfmt)
+        want = d @ w.T
+        _check(_f64(dX), want, _steps8(N) * (np.abs(d) @ np.abs(w).T) + 2.0 ** -8 * 1.01 * np.abs(want)
+               + 1e-38, f"dX fmt {dfmt}")
+        _norm(_f64(dX), want, "dX")
+
+
+def _grad_check(c, D, T, dA, dB, M, N, r, f=1.0):
+    G = c.dy @ c.b.T
+    gabs = np.abs(c.dy) @ np.abs(c.b).T
+    tol = c.s * (_steps(M) + _steps(N) + 4 * E24) * (np.abs(D).T @ gabs)
+    _check(_f64(dA), c.s * (D.T @ G), tol, "dA")
+    t = _f64(T)
+    _check(_f64(dB), c.s * (t.T @ c.dy), c.s * (_steps(M) + 4 * E24) * (np.abs(t).T @ np.abs(c.dy)),
+           "dB")
+    return G, gabs
+
+
+def _low(c, G, gabs, N, r):
+    """The adapter's term of dX and its bound."""
+    low = c.s * (G @ c.a.T)
+    tol = c.s * ((2.0 ** -8 * np.abs(G) + _steps(N) * gabs) @ np.abs(c.a).T) \
+        + _steps(r) * c.s * (np.abs(G) @ np.abs(c.a).T)
+    return low, tol
+
+
+SHAPES = [(1, 64, 64, 1), (1, 512, 4096, 16), (16, 256, 256, 8), (7, 192, 320, 3), (65, 128, 64, 64),
+          (100, 1344, 576, 100), (257, 512, 1024, 64), (300, 320, 192, 256)]
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("M,N,K,r", SHAPES)
+def test_fp8_linear(q, M, N, K, r, fmt):
+    print(f"[case] fp8 linear M={M} N={N} K={K} r={r} fmt={fmt}", flush=True)
+    c = Case(q, M, N, K, r, fmt)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    Y, T = q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s)
+    _fwd_check(c, W, Y, T, N, K, r)
+    Y2, none = q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s, want_T=False)
+    assert none is None and torch.equal(Y, Y2)
+    dX, dA, dB = q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, c.A, c.B, c.s, fmt=fmt)
+    G, gabs = _grad_check(c, c.X, T, dA, dB, M, N, r)
+    w = _dec(W.codes_t, W.scales_t, N, 0, 128)
+    d = act8.dequantize(*act8.quantize(c.dy, fmt), N, fmt)
+    low, ltol = _low(c, G, gabs, N, r)
+    want = d @ w.T + low
+    _check(_f64(dX), want, _steps8(N) * (np.abs(d) @ np.abs(w).T) + ltol
+           + 2.0 ** -8 * 1.01 * np.abs(want), "dX")
+    # T recomputed, dX left out, and a rerun: the same bits
+    r1 = q.qlora_fp8_linear_bwd(c.dY, c.x8, None, W, c.A, c.B, c.s, fmt=fmt)
+    r2 = q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, c.A, c.B, c.s, want_dX=False)
+    assert torch.equal(r1[0], dX) and torch.equal(r1[1], dA) and torch.equal(r1[2], dB)
+    assert r2[0] is None and torch.equal(r2[1], dA) and torch.equal(r2[2], dB)
+
+
+@pytest.mark.parametrize("store_type", [0, 3])
+@pytest.mark.parametrize("drop", [0.0, 0.1])
+@pytest.mark.parametrize("M,N,K,r", SHAPES[:7])
+def test_nf4_backward(q, M, N, K, r, drop, store_type):
+    print(f"[case] nf4 bwd act8 M={M} N={N} K={K} r={r} drop={drop} store={store_type}", flush=True)
+    fmt = (M + r) % 2
+    c = Case(q, M, N, K, r, fmt)
+    st = q.qlora_nf4_quantize(c.W, store_type=store_type)
+    keep, kw, f, D = 1.0, {}, 1.0, c.X
+    if drop:
+        mask = q.qlora_dropout_mask(M, K, drop, seed=5, device=device())
+        kw = dict(keep_mask=mask, p=drop)
+        keep = oracle.unpack_keep(mask.cpu().numpy().view(np.uint32), K).astype(np.float64)
+        f = oracle.keep_scale(drop)
+        D = c.X * keep * f
+    T = torch.from_numpy((D @ c.a).astype(np.float32)).to(device())
+    dX, dA, dB = q.qlora_linear_bwd_act8(c.dY, c.x8, T, st, c.A, c.B, c.s, **kw)
+    G, gabs = _grad_check(c, D, T, dA, dB, M, N, r)
+    w = _f64(q.qlora_nf4_dequantize_bf16(st)).reshape(N, K)
+    low, ltol = _low(c, G, gabs, N, r)
+    want = c.dy @ w + low * keep * f
+    _check(_f64(dX), want, _steps(N) * (np.abs(c.dy) @ np.abs(w)) + ltol * f
+           + 2.0 ** -8 * 1.01 * np.abs(want), "dX")
+    # the bf16 call on the decoded input: the same products up to the order
+    # in which G is summed, which can move bf16(s G) and bf16(dX) by one ulp
+    X = q.qlora_act8_dequantize(c.x8)
+    ref = None
+    if not drop:
+        ref = q.qlora_linear_bwd(c.dY, X, T, st, c.A, c.B, c.s)
+    elif store_type == 0:
+        ref = q.qlora_linear_bwd_dropout(c.dY, X, T, st, c.A, c.B, c.s, mask, drop)
+    if ref is not None:
+        _check(_f64(dX), _f64(ref[0]), 2 * ltol * f + 2.0 ** -7 * np.abs(want)
+               + 2 * _steps(N) * (np.abs(c.dy) @ np.abs(w)), "dX against the bf16 call")
+    none, a2, b2 = q.qlora_linear_bwd_act8(c.dY, c.x8, T, st, c.A, c.B, c.s, want_dX=False, **kw)
+    assert none is None and torch.equal(a2, dA) and torch.equal(b2, dB)
+    # T recomputed from the 8-bit input
+    _, a3, b3 = q.qlora_linear_bwd_act8(c.dY, c.x8, None, st, c.A, c.B, c.s, **kw)
+    assert torch.equal(a3, dA)
+    tol = c.s * (_steps(M) + _steps(K) + 4 * E24) * ((np.abs(D) @ np.abs(c.a)).T @ np.abs(c.dy))
+    _check(_f64(b3), c.s * ((D @ c.a).T @ c.dy), tol, "dB, T recomputed")
+
+
+def test_gradients_by_differences(q):
+    """dA, dB and dX of the 8-bit layer against differences of its forward's
+    loss <dY, Y>, evaluated in float64 on the decoded matrices: the loss is
+    bilinear in (A, B), so a central difference has no truncation error."""
+    M, N, K, r = 24, 128, 192, 8
+    c = Case(q, M, N, K, r)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    _, T = q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s)
+    dX, dA, dB = q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, c.A, c.B, c.s)
+    w = _dec(W.codes, W.scales, K, 0, 128)
+    loss = lambda X, a, b: float((c.dy * (X @ w.T + c.s * (X @ a) @ b)).sum())  # noqa: E731
+    rng = np.random.default_rng(0)
+    for _ in range(4):
+        da, db, dx = rng.standard_normal((K, r)), rng.standard_normal((r, N)), rng.standard_normal((M, K))
+        na = loss(c.X, c.a + da, c.b) - loss(c.X, c.a - da, c.b)
+        nb = loss(c.X, c.a, c.b + db) - loss(c.X, c.a, c.b - db)
+        nx = loss(c.X + dx, c.a, c.b) - loss(c.X - dx, c.a, c.b)
+        ga, gb, gx = 2 * (_f64(dA) * da).sum(), 2 * (_f64(dB) * db).sum(), 2 * (_f64(dX) * dx).sum()
+        # dA, dB: float32 accuracy of sums of about 1500 signed terms
+        assert abs(ga - na) < 1e-5 * np.abs(_f64(dA) * da).sum()
+        assert abs(gb - nb) < 1e-5 * np.abs(_f64(dB) * db).sum()
+        # dX: E4M3 rounding of dY (2^-4 of an element at most) over N random signs
+        assert abs(gx - nx) < 2.0 ** -4 * np.sqrt((_f64(dX) ** 2).sum() * 4) * 4
+
+
+def test_non_finite_stay_in_their_row(q):
+    """A NaN in one input row or one upstream row reaches that row of Y and dX alone."""
+    M, N, K, r = 40, 192, 256, 16
+    dev = device()
+    c = Case(q, M, N, K, r)
+    x = q.qlora_act8_dequantize(c.x8)
+    x[3, 200] = float("nan")
+    x8 = q.qlora_act8_quantize(x)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    Y, T = q.qlora_fp8_linear_fwd(x8, W, c.A, c.B, c.s)
+    y = _f64(Y)
+    assert np.isnan(y[3]).all() and np.isfinite(np.delete(y, 3, 0)).all()
+    dY = c.dY.clone()
+    dY[5, 7] = float("nan")
+    dX, dA, dB = q.qlora_fp8_linear_bwd(dY, c.x8, None, W, c.A, c.B, c.s)
+    d = _f64(dX)
+    assert np.isnan(d[5]).all() and np.isfinite(np.delete(d, 5, 0)).all()
+    b = _f64(dB)
+    assert np.isnan(b[:, 7]).all() and np.isfinite(np.delete(b, 7, 1)).all()
+
+
+def test_large_workspace_serves_smaller_and_streams(q):
+    """One workspace serves any smaller call, and work goes to the caller's stream."""
+    dev = device()
+    big = q.act8_workspace(512, 1024, 1024, 64, dev)
+    s = torch.cuda.Stream()
+    for M, N, K, r in [(16, 256, 256, 8), (300, 320, 192, 64), (512, 1024, 1024, 64), (1, 64, 64, 1)]:
+        assert q.qlora_act8_workspace_bytes(M, N, K, r) <= big.numel()
+        c = Case(q, M, N, K, r)
+        W = q.qlora_fp8_weight_quantize(c.W)
+        Y, T = q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s)
+        ref = q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, c.A, c.B, c.s)
+        big.fill_(0xFF)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            Y2, T2 = q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s, ws=big)
+            got = q.qlora_fp8_linear_bwd(c.dY, c.x8, T2, W, c.A, c.B, c.s, ws=big)
+        s.synchronize()
+        assert torch.equal(Y, Y2) and torch.equal(T, T2)
+        for a, b in zip(ref, got):
+            assert torch.equal(a, b)
+
+
+def test_refusals(q):
+    dev = device()
+    c = Case(q, 16, 128, 192, 8)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    only = q.qlora_fp8_weight_quantize(c.W, transposed=False)
+    st = q.qlora_nf4_quantize(c.W)
+    T = torch.zeros(16, 8, device=dev)
+    bad = [
+        lambda: q.qlora_fp8_linear_fwd(c.x8, W, c.A, None, 1.0),
+        lambda: q.qlora_fp8_linear_fwd(c.x8, W, c.A.t(), c.B, 1.0),
+        lambda: q.qlora_fp8_linear_fwd(c.x8, W, c.A[:64], c.B, 1.0),
+        lambda: q.qlora_fp8_linear_fwd(c.x8, W, c.A.float(), c.B, 1.0),
+        lambda: q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, 1.0, Y=torch.empty(16, 64, dtype=torch.bfloat16, device=dev)),
+        lambda: q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, 1.0, ws=torch.empty(16, dtype=torch.uint8, device=dev)),
+        lambda: q.qlora_fp8_linear_fwd(q.Act8(c.x8.codes, c.x8.scales, (16, 192), 3), W),
+        lambda: q.qlora_fp8_linear_fwd(q.Act8(c.x8.codes[:8], c.x8.scales, (16, 192)), W),
+        lambda: q.qlora_fp8_linear_bwd(c.dY, c.x8, T, only, c.A, c.B, 1.0),
+        lambda: q.qlora_fp8_linear_bwd(c.dY, c.x8, T[:4], W, c.A, c.B, 1.0),
+        lambda: q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, None, None, 1.0),
+        lambda: q.qlora_fp8_linear_bwd(c.dY[:8], c.x8, T, W, c.A, c.B, 1.0),
+        lambda: q.qlora_linear_bwd_act8(c.dY, c.x8, T, st, None, None, 1.0),
+        lambda: q.qlora_linear_bwd_act8(c.dY.float(), c.x8, T, st, c.A, c.B, 1.0),
+        lambda: q.qlora_linear_bwd_act8(c.dY, c.x8, T, st, c.A, c.B, 1.0,
+                                        keep_mask=torch.zeros(16, 6, dtype=torch.int32, device=dev), p=1.5),
+        lambda: q.qlora_linear_bwd_act8(c.dY, c.x8, T, st, c.A, c.B, 1.0,
+                                        keep_mask=torch.zeros(16, 5, dtype=torch.int32, device=dev), p=0.1),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(q.QloraError):
+            f()
+            print("not refused:", i)
+    # an adapter needs whole 64-wide rows, the plain product does not
+    d = Case(q, 16, 100, 100, 0)
+    w = q.qlora_fp8_weight_quantize(d.W)
+    A = torch.zeros(100, 8, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(q.QloraError):
+        q.qlora_fp8_linear_fwd(d.x8, w, A, A.t().contiguous(), 1.0)
+    q.qlora_fp8_linear_fwd(d.x8, w)
