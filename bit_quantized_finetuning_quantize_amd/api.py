@@ -34,11 +34,13 @@ def _check(status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The caller's stream on the current device, as an address. The raw
+    accessors take 0.2 us where building a Stream object takes 3."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 _HIP = None
@@ -69,7 +71,7 @@ def _state_ptr(t, name):
 
 
 def _need(t, dtype, name):
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise QloraError(f"{name} must be a contiguous {dtype} tensor on the GPU")
 
 
@@ -430,20 +432,22 @@ def empty_act8(M, K, device, fmt=ACT8_E4M3):
 
 def _rows(t, shape, name):
     """Leading dimension of a bf16 matrix of `shape` on the GPU whose rows are contiguous."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or tuple(t.shape) != tuple(shape):
-        raise QloraError(f"{name} must be a bfloat16 tensor of shape {tuple(shape)} on the GPU")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_cuda:
+        raise QloraError(f"{name} must be a bfloat16 tensor of shape {shape} on the GPU")
+    M, K = shape
+    ld, step = t.stride()
+    if K > 1 and step != 1:
         raise QloraError(f"{name} must have contiguous rows")
-    ld = t.stride(0)
-    if t.shape[0] == 1:  # one row: the stride has no meaning
-        return max(ld, t.shape[1])
-    if ld < t.shape[1]:
+    if M == 1:  # one row: the stride has no meaning
+        return max(ld, K)
+    if ld < K:
         raise QloraError(f"{name} must not have overlapping rows")
     return ld
 
 
 def _bytes(t, shape, name):
-    if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+    if (t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous()
+            or not t.is_cuda):
         raise QloraError(f"{name} must be a contiguous uint8 tensor of shape {shape} on the GPU")
 
 
@@ -559,7 +563,7 @@ def _adapter(A, B, N, K):
     _need(A, torch.bfloat16, "A")
     _need(B, torch.bfloat16, "B")
     r = A.shape[1] if A.dim() == 2 else -1
-    if tuple(A.shape) != (K, r) or tuple(B.shape) != (r, N):
+    if A.shape != (K, r) or B.shape != (r, N):
         raise QloraError("A must be [K x r] and B [r x N]")
     return r
 
@@ -568,7 +572,7 @@ def _out(t, shape, dtype, device, name):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, dtype, name)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise QloraError(f"{name} must have shape {shape}")
     return t
 
@@ -576,7 +580,7 @@ def _out(t, shape, dtype, device, name):
 def _given(t, shape, dtype, name):
     if t is not None:
         _need(t, dtype, name)
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise QloraError(f"{name} must have shape {shape}")
 
 

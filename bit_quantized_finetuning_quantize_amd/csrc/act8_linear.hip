@@ -109,11 +109,16 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
 hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A, const uint16_t* B,
                           int64_t M, int64_t N, int64_t K, int r, float scale, uint16_t* Y,
                           float* T_out, void* ws, hipStream_t stream) {
-  if (!r) return launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, stream);
   const Ws8 l = ws8_layout(M, N, K, r);
   const Ptrs w = carve(ws, l);
+  const bool few = fp8_few(M, N);
+  if (!r)
+    return few ? launch_fp8_few(x, fmt, w8, M, N, K, nullptr, 0, nullptr, 0, scale, Y, nullptr, stream)
+               : launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, stream);
   int splits = 0;
   QLORA_TRY(launch_rows_act8(x, fmt, M, K, nullptr, A, r, w.part, &splits, stream));
+  if (few)
+    return launch_fp8_few(x, fmt, w8, M, N, K, w.part, splits, B, r, scale, Y, T_out, stream);
   const LowrankOut t{w.part, splits, lowrank_cols(r), 1.0f, T_out, w.u, nullptr};
   QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{B, true, N, w.v}, M, r, scale, stream));
   return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, stream);

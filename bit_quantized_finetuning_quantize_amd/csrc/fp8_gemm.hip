@@ -20,6 +20,7 @@ namespace qlora {
 namespace fp8 {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) float lds_f32;
 
 struct Fp8Gemm {
   const uint8_t *x, *xs, *w, *ws;
@@ -28,7 +29,8 @@ struct Fp8Gemm {
   const uint16_t *U, *V;  // bf16 [M x r64], [N x r64], or null
   int r64;
   uint16_t* Y;         // [M x N]
-  int nM, nN;
+  int nM, nN, group;   // tiles, and row tiles per group of the walk
+  int full, cut;       // 256 x 256 tiles done whole; parts of each other one
 };
 
 // 128-byte LDS rows, the 16-byte piece c of row r at position c ^ swz(r).
@@ -38,71 +40,123 @@ using gemm::make_rsrc;
 using gemm::tile_off;
 using gemm::wait_vmcnt;
 
-template <int kSel, int kXFmt>
+template <int kXFmt>
 __device__ __forceinline__ floatx16 mma(i32x8 w, i32x8 x, floatx16 c, uint32_t sw, uint32_t sx) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, kXFmt, kSel, (int)sw, kSel,
-                                                         (int)sx);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, kXFmt, 0, (int)sw, 0, (int)sx);
 }
 
-// Tile of TN weight rows by TM activation rows; each wave WN x WM of it.
-template <int TN, int TM, int WN, int WM, int kXFmt>
-__global__ void __launch_bounds__((TN / WN) * (TM / WM) * 64) fp8_gemm_kernel(Fp8Gemm p) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone
-  constexpr int kWaves = (TN / WN) * (TM / WM);
+// Tiles are walked in groups of `group` row tiles, column tile outermost in
+// the group, so that neighbours in the walk share operands.
+__device__ __forceinline__ void tile_at(const Fp8Gemm& p, int t, int& tm, int& tn) {
+  const int per = p.group * p.nN;
+  const int g = t / per, in = t - g * per;
+  const int rows = min(p.group, p.nM - g * p.group);
+  tm = g * p.group + in % rows;
+  tn = in / rows;
+}
+// Workgroup id runs on XCD id % 8: each XCD takes a consecutive run of the
+// walk (runs differ by one tile at most), whose operands then meet in its L2.
+__device__ __forceinline__ int xcd_order(int id, int count) {
+  const int x = id & 7;
+  return x * (count >> 3) + min(x, count & 7) + (id >> 3);
+}
+
+// Issue order: kN times one product and, beside it, kV loads and kD LDS reads.
+template <int kN, int kV, int kD>
+__device__ __forceinline__ void pace() {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x020, kV, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, kD, 0);
+  }
+}
+// Tile of TN weight rows by TM activation rows, 2 x 2 waves, each a
+// (TN / 2) x (TM / 2) part of it in 32 x 32 accumulators.
+//
+// A step is one block of 128 along K, in two halves of 64. The fragments of
+// the next half are read from LDS while the matrix cores work on the present
+// one, so two sets of fragments take turns. The operand tiles sit in a ring of
+// LDS stages. In the middle of a step every wave has read all of the step's
+// stage (its second half's fragments are in registers) and the loads of the
+// next step have landed: one barrier there frees the stage for the step
+// kStages ahead and lets the fragments of the next step be read under the second
+// half's products. No load or LDS latency is then waited for inside the loop.
+//
+// With kGroups > 1 the workgroup has that many sets of 2 x 2 waves, each with
+// a ring of its own, that take a run of the steps each; the sums of the other
+// sets are added to the first's in order at the end. For grids that leave
+// compute units idle: a step's latency then covers kGroups blocks along K.
+template <int TN, int TM, int kStages, int kGroups, int kXFmt>
+__device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t m0, uint32_t lds_all) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the kernels' stubs alone
+  constexpr int WN = TN / 2, WM = TM / 2;
   constexpr int BN = WN / 32, BM = WM / 32;
   constexpr int kStage = (TN + TM) * 128;
-  constexpr int kLoadW = TN / 8 / kWaves, kLoadX = TM / 8 / kWaves;
-  static_assert(kLoadW * kWaves * 8 == TN && kLoadX * kWaves * 8 == TM, "whole loads per wave");
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
-
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave % (TN / WN), wm = wave / (TN / WN);
+  constexpr int kLoadW = TN / 32, kLoadX = TM / 32;  // per wave and step
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = wave_all & 3, group = wave_all >> 2;
+  const uint32_t lds0 = lds_all + (uint32_t)(group * kStages * kStage);
+  const int wn = wave & 1, wm = wave >> 1;
   const int r = lane & 31, half = lane >> 5;
-  const int tm = blockIdx.x % p.nM, tn = blockIdx.x / p.nM;
-  const int64_t n0 = (int64_t)tn * TN, m0 = (int64_t)tm * TM;
 
   // operand moves: 8 rows of 128 bytes per instruction
+  // this set's steps: [first, first + KB), whole scale dwords; every set
+  // walks KB steps, and those past the end of K read zeros
+  const int KB = kGroups == 1 ? p.KB : ((p.KB + kGroups - 1) / kGroups + 3) / 4 * 4;
+  const int first = group * KB, valid = p.KB - first;
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + n0 * p.ldc, (p.N - n0) * p.ldc);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + m0 * p.ldc, (p.M - m0) * p.ldc);
-  int vw[kLoadW], vx[kLoadX];
+  // the swizzle of rows 16 apart is the same: one lane offset serves every
+  // second instruction
+  const int row0 = wave * (kLoadW * 8) + (lane >> 3), row1 = wave * (kLoadX * 8) + (lane >> 3);
+  int vw[2], vx[2];
 #pragma unroll
-  for (int i = 0; i < kLoadW; ++i) {
-    const int row = (wave * kLoadW + i) * 8 + (lane >> 3);
-    vw[i] = (int)(row * p.ldc) + (((lane & 7) ^ gemm::swz(row)) << 4);
+  for (int i = 0; i < 2; ++i) {
+    vw[i] = (int)((row0 + i * 8) * p.ldc) + (((lane & 7) ^ gemm::swz(row0 + i * 8)) << 4);
+    vx[i] = (int)((row1 + i * 8) * p.ldc) + (((lane & 7) ^ gemm::swz(row1 + i * 8)) << 4);
   }
-#pragma unroll
-  for (int i = 0; i < kLoadX; ++i) {
-    const int row = (wave * kLoadX + i) * 8 + (lane >> 3);
-    vx[i] = (int)(row * p.ldc) + (((lane & 7) ^ gemm::swz(row)) << 4);
-  }
-  auto issue = [&](int kb, int st) {
-    const uint32_t a = lds0 + (uint32_t)(st * kStage);
-#pragma unroll
-    for (int i = 0; i < kLoadW; ++i)
+  const int step16 = (int)(16 * p.ldc);
+  // move i of a step: weight rows first, then activation rows
+  auto at_step = [&](int kb) {
+    if constexpr (kGroups == 1) return min(kb, KB - 1) * 128;
+    else return min(kb, KB - 1) < valid ? (first + min(kb, KB - 1)) * 128 : 0x7f000000;
+  };
+  auto move = [&](int off, uint32_t st, int i) {
+    if (i < kLoadW)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rw, (lds_void*)(uintptr_t)(a + (uint32_t)((wave * kLoadW + i) * 1024)), 16, vw[i],
-          kb * 128, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kLoadX; ++i)
+          rw, (lds_void*)(uintptr_t)(st + (uint32_t)((wave * kLoadW + i) * 1024)), 16, vw[i & 1],
+          off + (i >> 1) * step16, 0, 0);
+    else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rx, (lds_void*)(uintptr_t)(a + (uint32_t)(TN * 128 + (wave * kLoadX + i) * 1024)), 16,
-          vx[i], kb * 128, 0, 0);
+          rx, (lds_void*)(uintptr_t)(st + (uint32_t)(TN * 128 + (wave * kLoadX + i - kLoadW) * 1024)),
+          16, vx[(i - kLoadW) & 1], off + ((i - kLoadW) >> 1) * step16, 0, 0);
+  };
+  auto issue = [&](int kb, uint32_t st) {
+    const int off = at_step(kb);
+#pragma unroll
+    for (int i = 0; i < kLoadW + kLoadX; ++i) move(off, st, i);
   };
 
-  // scale bytes: four blocks per dword
-  const int64_t NBl = (p.N + 127) / 128;
-  const __amdgpu_buffer_rsrc_t rsw = make_rsrc(p.ws, NBl * p.sb);
+  // scale bytes, a dword for four steps; the low byte is the present step's
+  const __amdgpu_buffer_rsrc_t rsw = make_rsrc(p.ws, (p.N + 127) / 128 * p.sb);
   const __amdgpu_buffer_rsrc_t rsx = make_rsrc(p.xs + m0 * p.sb, (p.M - m0) * p.sb);
-  int osw[BN], osx[BM];
+  struct Scales { uint32_t w, x[BM]; };
+  auto scales = [&](int kb) {
+    Scales s;
+    s.w = __builtin_amdgcn_raw_buffer_load_b32(rsw, (int)((n0 + wn * WN) / 128) * p.sb, first + kb, 0);
 #pragma unroll
-  for (int i = 0; i < BN; ++i) osw[i] = (int)((n0 + wn * WN + i * 32) / 128) * p.sb;
-#pragma unroll
-  for (int j = 0; j < BM; ++j) osx[j] = (wm * WM + j * 32 + r) * p.sb;
-  uint32_t sw[BN], sx[BM];
+    for (int j = 0; j < BM; ++j)
+      s.x[j] = __builtin_amdgcn_raw_buffer_load_b32(rsx, (wm * WM + j * 32 + r) * p.sb, first + kb, 0);
+    return s;
+  };
 
-  issue(0, 0);
+  // Every load of the loop and of this prologue is issued whatever KB is:
+  // past the end the last step is moved again, into a stage that is not read.
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) issue(k, lds0 + (uint32_t)(k * kStage));
+  Scales s = scales(0);
 
   floatx16 acc[BN][BM];
 #pragma unroll
@@ -113,66 +167,133 @@ __global__ void __launch_bounds__((TN / WN) * (TM / WM) * 64) fp8_gemm_kernel(Fp
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
   // the low-rank term first, straight from memory
-  if (p.U) {
-    const __amdgpu_buffer_rsrc_t ru =
-        make_rsrc(p.U + m0 * p.r64, (p.M - m0) * (int64_t)p.r64 * 2);
-    const __amdgpu_buffer_rsrc_t rv =
-        make_rsrc(p.V + n0 * p.r64, (p.N - n0) * (int64_t)p.r64 * 2);
-    for (int j0 = 0; j0 < p.r64; j0 += 16) {
-      bf16x8 a[BN], b[BM];
+  if (p.U && group == 0) {
+    const __amdgpu_buffer_rsrc_t ru = make_rsrc(p.U + m0 * p.r64, (p.M - m0) * (int64_t)p.r64 * 2);
+    const __amdgpu_buffer_rsrc_t rv = make_rsrc(p.V + n0 * p.r64, (p.N - n0) * (int64_t)p.r64 * 2);
+    for (int j0 = 0; j0 < p.r64; j0 += 64) {  // 64 columns' loads in flight together
+      bf16x8 a[4][BN], b[4][BM];
 #pragma unroll
-      for (int i = 0; i < BN; ++i)
-        a[i] = as_bf16x8(__builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       rv, ((wn * WN + i * 32 + r) * p.r64 + half * 8) * 2, j0 * 2, 0)));
+      for (int q = 0; q < 4; ++q) {
 #pragma unroll
-      for (int j = 0; j < BM; ++j)
-        b[j] = as_bf16x8(__builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       ru, ((wm * WM + j * 32 + r) * p.r64 + half * 8) * 2, j0 * 2, 0)));
-#pragma unroll
-      for (int i = 0; i < BN; ++i)
+        for (int i = 0; i < BN; ++i)
+          a[q][i] = as_bf16x8(__builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         rv, ((wn * WN + i * 32 + r) * p.r64 + half * 8) * 2, (j0 + q * 16) * 2, 0)));
 #pragma unroll
         for (int j = 0; j < BM; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+          b[q][j] = as_bf16x8(__builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         ru, ((wm * WM + j * 32 + r) * p.r64 + half * 8) * 2, (j0 + q * 16) * 2, 0)));
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < BN; ++i)
+#pragma unroll
+          for (int j = 0; j < BM; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[q][i], b[q][j], acc[i][j], 0, 0, 0);
     }
   }
 
-  auto frag = [&](uint32_t base, int row, int h) {
-    // pieces 4 h + 2 half and the next one
-    const u32x4 a = *(const lds_u32x4*)(uintptr_t)(base + (uint32_t)tile_off(row, 4 * h + 2 * half));
-    const u32x4 b = *(const lds_u32x4*)(uintptr_t)(base + (uint32_t)tile_off(row, 4 * h + 2 * half + 1));
-    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-  };
-  auto block = [&](int kb, auto sel) {
-    constexpr int kSel = decltype(sel)::value;
-    wait_vmcnt<0>();
-    gemm::stage_barrier();
-    if (kb + 1 < p.KB) issue(kb + 1, (kb + 1) & 1);
-    const uint32_t aw = lds0 + (uint32_t)((kb & 1) * kStage), ax = aw + TN * 128;
+  // LDS offsets of a fragment's two 16-byte pieces, 4 h + 2 half and the
+  // next, in row r of the wave's part; rows 32 apart share the swizzle
+  uint32_t ow[2][2], ox[2][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i32x8 fw[BN], fx[BM];
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < BN; ++i) fw[i] = frag(aw, wn * WN + i * 32 + r, h);
-#pragma unroll
-      for (int j = 0; j < BM; ++j) fx[j] = frag(ax, wm * WM + j * 32 + r, h);
-#pragma unroll
-      for (int i = 0; i < BN; ++i)
-#pragma unroll
-        for (int j = 0; j < BM; ++j)
-          acc[i][j] = mma<kSel, kXFmt>(fw[i], fx[j], acc[i][j], sw[i], sx[j]);
+    for (int c = 0; c < 2; ++c) {
+      ow[h][c] = lds0 + (uint32_t)tile_off(wn * WN + r, 4 * h + 2 * half + c);
+      ox[h][c] = lds0 + (uint32_t)(TN * 128 + tile_off(wm * WM + r, 4 * h + 2 * half + c));
     }
+  // Fragments in the order the products use them: weight block 0, the
+  // activation blocks, the other weight blocks. Two pieces each.
+  struct Frags { u32x4 f[BN + BM][2]; };
+  auto read1 = [&](Frags& f, uint32_t st, int h, int i, int c) {
+    const bool act = i >= 1 && i <= BM;
+    const int block = act ? i - 1 : i ? i - BM : 0;
+    f.f[i][c] = *(const lds_u32x4*)(uintptr_t)((act ? ox[h][c] : ow[h][c]) + st + (uint32_t)(block * 4096));
   };
-  for (int kb = 0; kb < p.KB; kb += 4) {
+  auto whole = [](const u32x4 (&f)[2]) {
+    return i32x8{(int)f[0][0], (int)f[0][1], (int)f[0][2], (int)f[0][3],
+                 (int)f[1][0], (int)f[1][1], (int)f[1][2], (int)f[1][3]};
+  };
+  auto product = [&](const Frags& f, const Scales& s) {
 #pragma unroll
-    for (int i = 0; i < BN; ++i) sw[i] = __builtin_amdgcn_raw_buffer_load_b32(rsw, osw[i], kb, 0);
+    for (int i = 0; i < BN; ++i)
 #pragma unroll
-    for (int j = 0; j < BM; ++j) sx[j] = __builtin_amdgcn_raw_buffer_load_b32(rsx, osx[j], kb, 0);
-    block(kb, std::integral_constant<int, 0>{});
-    if (kb + 1 < p.KB) block(kb + 1, std::integral_constant<int, 1>{});
-    if (kb + 2 < p.KB) block(kb + 2, std::integral_constant<int, 2>{});
-    if (kb + 3 < p.KB) block(kb + 3, std::integral_constant<int, 3>{});
+      for (int j = 0; j < BM; ++j)
+        acc[i][j] = mma<kXFmt>(whole(f.f[i ? i + BM : 0]), whole(f.f[1 + j]), acc[i][j], s.w, s.x[j]);
+  };
+  // Issue order of a half: after each product the LDS reads and the loads
+  // that fit beside it, the reads in the first half of the products so that
+  // their data is there when the next half begins.
+  constexpr int kM = BN * BM, kR = 2 * (BN + BM), kL = kLoadW + kLoadX;
+
+  uint32_t cur = 0, nxt = kStage;  // stages of steps kb and kb + 1
+  wait_vmcnt<(kStages - 1) * kL>();
+  gemm::stage_barrier();
+  Frags f0, f1;
+#pragma unroll
+  for (int i = 0; i < 2 * (BN + BM); ++i) read1(f0, 0, 0, i / 2, i % 2);
+  for (int kb4 = 0; kb4 < KB; kb4 += 4) {
+    const Scales ahead = scales(kb4 + 4);
+    const int end = min(kb4 + 4, KB);
+    for (int kb = kb4; kb < end; ++kb) {
+#pragma unroll
+      for (int i = 0; i < 2 * (BN + BM); ++i) read1(f1, cur, 1, i / 2, i % 2);
+      product(f0, s);
+      if constexpr (kM >= 4) {
+        pace<kM / 2, 0, 2 * kR / kM>();
+        pace<kM / 2, 0, 0>();
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // Step kb + 1 has landed when at most the moves of the kStages - 2 steps
+      // after it are outstanding (they complete in order; a scale load among
+      // them only makes this wait longer).
+      wait_vmcnt<(kStages - 2) * kL>();
+      gemm::stage_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      // The moves of step kb + kStages into the stage that is now free, and
+      // the reads of the next step, in turn (their order is kept: both touch
+      // LDS).
+      const int nk = at_step(kb + kStages);
+#pragma unroll
+      for (int i = 0; i < kL; ++i) {
+        move(nk, lds0 + cur, i);
+        read1(f0, nxt, 0, i / 2, i % 2);
+      }
+      static_assert(kL == kR, "one move per piece");
+      product(f1, s);
+      if constexpr (kM >= 4) pace<kM, kL / kM, kR / kM>();
+      __builtin_amdgcn_sched_barrier(0);
+      s.w >>= 8;
+#pragma unroll
+      for (int j = 0; j < BM; ++j) s.x[j] >>= 8;
+      cur = nxt;
+      nxt = nxt + kStage == kStages * kStage ? 0 : nxt + kStage;
+    }
+    s = ahead;
+  }
+  wait_vmcnt<0>();  // no direct load may outlive the workgroup's LDS
+
+  if constexpr (kGroups > 1) {
+    constexpr int kAcc = BN * BM * 16;  // floats per lane
+    const uint32_t at = lds_all + (uint32_t)(((wave * kAcc) * 64 + lane) * 4);
+    for (int g = 1; g < kGroups; ++g) {
+      __syncthreads();
+      if (group == g) {
+#pragma unroll
+        for (int e = 0; e < kAcc; ++e)
+          *(lds_f32*)(uintptr_t)(at + (uint32_t)(e * 256)) = acc[e / 16 / BM][e / 16 % BM][e % 16];
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int e = 0; e < kAcc; ++e)
+          acc[e / 16 / BM][e / 16 % BM][e % 16] += *(const lds_f32*)(uintptr_t)(at + (uint32_t)(e * 256));
+      }
+    }
+    if (group != 0) return;
   }
 
   const bool vec = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 7) == 0;
@@ -200,6 +321,158 @@ __global__ void __launch_bounds__((TN / WN) * (TM / WM) * 64) fp8_gemm_kernel(Fp
 #endif
 }
 
+__device__ __forceinline__ uint32_t lds_base() {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  return (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
+}
+
+// 256 x 256 tiles, one workgroup per compute unit: the first `full` of the
+// walk. The tiles that do not fill a last round are cut in `cut` parts (1, 2
+// or 4), a workgroup each, so that more compute units share them.
+template <int kXFmt>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+fp8_gemm_kernel(Fp8Gemm p) {
+  const uint32_t lds = lds_base();
+  const int id = blockIdx.x;
+  int tm, tn;
+  if (id < p.full) {
+    tile_at(p, xcd_order(id, p.full), tm, tn);
+    gemm_tile<256, 256, 2, 1, kXFmt>(p, (int64_t)tn * 256, (int64_t)tm * 256, lds);
+    return;
+  }
+  const int u = xcd_order(id - p.full, (int)gridDim.x - p.full);
+  tile_at(p, p.full + u / p.cut, tm, tn);
+  const int part = u % p.cut;
+  const int64_t n0 = (int64_t)tn * 256, m0 = (int64_t)tm * 256;
+  if (p.cut == 2) gemm_tile<256, 128, 3, 1, kXFmt>(p, n0, m0 + part * 128, lds);
+  else gemm_tile<128, 128, 4, 1, kXFmt>(p, n0 + (part & 1) * 128, m0 + (part >> 1) * 128, lds);
+}
+
+// One tile size; several workgroups per compute unit.
+template <int TN, int TM, int kStages, int kGroups, int kXFmt>
+__global__ void __launch_bounds__(256 * kGroups) __attribute__((amdgpu_waves_per_eu(2, kGroups > 2 ? 4 : 2)))
+fp8_gemm_small_kernel(Fp8Gemm p) {
+  int tm, tn;
+  tile_at(p, xcd_order(blockIdx.x, gridDim.x), tm, tn);
+  gemm_tile<TN, TM, kStages, kGroups, kXFmt>(p, (int64_t)tn * TN, (int64_t)tm * TM, lds_base());
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the time is that of streaming the weight once. A workgroup owns
+// 16 RN weight rows and 16 tokens over the whole of K, its eight waves a
+// run of blocks each; both operands go from memory straight to registers
+// (v_mfma_scale_f32_16x16x128_f8f6f4 takes a whole block), four blocks' loads
+// in flight together, and the waves' sums meet in LDS in a fixed order. The
+// adapter's term is added there in float32, from the split partials of T.
+struct Fp8Few {
+  Fp8Gemm g;
+  const float* part;   // [splits][M][ldp] partials of T, or null
+  int splits, ldp, r;
+  float scale;
+  const uint16_t* B;   // [r x N]
+  float* T_out;        // [M x r] or null
+};
+
+constexpr int kFewWaves = 8;
+
+template <int RN, int kXFmt>
+__global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const Fp8Gemm& p = q.g;
+  constexpr int kM = 16, kN = 16 * RN, kJ = 64;
+  __shared__ floatx4 s_acc[kFewWaves][RN][64];
+  __shared__ float s_t[kM][kJ + 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * kN, m0 = (int64_t)blockIdx.y * kM;
+
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + n0 * p.ldc, (p.N - n0) * p.ldc);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + m0 * p.ldc, (p.M - m0) * p.ldc);
+  const __amdgpu_buffer_rsrc_t rsw = make_rsrc(p.ws + n0 / 128 * p.sb, p.sb);  // the tile is in one block row
+  const __amdgpu_buffer_rsrc_t rsx = make_rsrc(p.xs + m0 * p.sb, (p.M - m0) * p.sb);
+  floatx4 acc[RN];
+#pragma unroll
+  for (int a = 0; a < RN; ++a) acc[a] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int per = (p.KB + kFewWaves - 1) / kFewWaves;
+  const int begin = wave * per, end = min(p.KB, begin + per);
+  constexpr int kU = 4;
+  for (int kb = begin; kb < end; kb += kU) {
+    u32x4 w[kU][RN][2], x[kU][2];
+    uint32_t sw[kU], sx[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      // past the wave's run every offset is out of range: zeros
+      const int off = kb + u < end ? (kb + u) * 128 : 0x7f000000;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int a = 0; a < RN; ++a)
+          w[u][a][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              rw, (int)((a * 16 + i) * p.ldc) + g * 16 + c * 64, off, 0));
+        x[u][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+            rx, (int)(i * p.ldc) + g * 16 + c * 64, off, 0));
+      }
+      sw[u] = __builtin_amdgcn_raw_buffer_load_b8(rsw, 0, kb + u, 0);
+      sx[u] = __builtin_amdgcn_raw_buffer_load_b8(rsx, i * p.sb, kb + u, 0);
+    }
+    // every load is on its way before the first product waits
+    __builtin_amdgcn_sched_barrier(0);
+    auto whole = [](const u32x4 (&f)[2]) {
+      return i32x8{(int)f[0][0], (int)f[0][1], (int)f[0][2], (int)f[0][3],
+                   (int)f[1][0], (int)f[1][1], (int)f[1][2], (int)f[1][3]};
+    };
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int a = 0; a < RN; ++a)
+        acc[a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            whole(w[u][a]), whole(x[u]), acc[a], 0, kXFmt, 0, (int)sw[u], 0, (int)sx[u]);
+  }
+#pragma unroll
+  for (int a = 0; a < RN; ++a) s_acc[wave][a][lane] = acc[a];
+
+  // one output per thread: n = n0 + tid % kN, m = m0 + tid / kN
+  static_assert(kM * kN <= kFewWaves * 64, "a thread per output");
+  const int nl = tid % kN, ml = tid / kN;
+  const int64_t n = n0 + nl, m = m0 + ml;
+  const bool mine = ml < kM && n < p.N && m < p.M;
+  float y = 0.0f;
+  if (q.part) {
+    for (int j0 = 0; j0 < q.r; j0 += kJ) {
+      const int nj = min(kJ, q.r - j0);
+      __syncthreads();
+      for (int e = tid; e < kM * kJ; e += kFewWaves * 64) {
+        const int64_t tm = m0 + e / kJ;
+        const int j = e % kJ;
+        float v = 0.0f;
+        if (tm < p.M && j < nj) {
+          for (int sp = 0; sp < q.splits; ++sp) v += q.part[((int64_t)sp * p.M + tm) * q.ldp + j0 + j];
+          if (q.T_out && blockIdx.x == 0) q.T_out[tm * q.r + j0 + j] = v;
+        }
+        s_t[e / kJ][j] = q.scale * v;
+      }
+      __syncthreads();
+      if (mine) {
+        const uint16_t* b = q.B + (int64_t)j0 * p.N + n;
+#pragma unroll 8
+        for (int j = 0; j < nj; ++j)
+          y += s_t[ml][j] * __builtin_bit_cast(float, (uint32_t)b[j * p.N] << 16);
+      }
+    }
+  }
+  __syncthreads();
+  if (!mine) return;
+  // accumulator (row 4 g + v, column i) of block a: n by row, m by column
+  const int l = ((nl & 15) >> 2) * 16 + ml;
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) v += s_acc[w][nl >> 4][l][nl & 3];
+  p.Y[m * p.N + n] = (uint16_t)(pack_bf16x2(v + y, 0.0f) & 0xffffu);
+#endif
+}
+
 }  // namespace fp8
 
 using namespace fp8;
@@ -218,20 +491,83 @@ hipError_t allow_lds(const void* kern, size_t lds, std::atomic<uint64_t>& raised
   return e;
 }
 
-template <int TN, int TM, int WN, int WM, int kXFmt>
-hipError_t run_tile(Fp8Gemm p, hipStream_t stream) {
+template <int kXFmt>
+hipError_t run_big(Fp8Gemm p, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
-  auto kern = fp8_gemm_kernel<TN, TM, WN, WM, kXFmt>;
-  constexpr size_t lds = 2 * (TN + TM) * 128;
+  auto kern = fp8_gemm_kernel<kXFmt>;
+  // 256 x 256 in two stages, 256 x 128 in three, 128 x 128 in four
+  constexpr size_t lds = 3 * (256 + 128) * 128;
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), lds, raised);
+  if (e != hipSuccess) return e;
+  p.nM = (int)((p.M + 255) / 256);
+  p.nN = (int)((p.N + 255) / 256);
+  p.group = 4;
+  const int tiles = p.nM * p.nN;
+  p.full = tiles / 256 * 256;
+  const int rest = tiles - p.full;
+  p.cut = rest <= 64 ? 4 : rest <= 128 ? 2 : 1;
+  if (p.cut == 1) p.full = tiles;
+  const int grid = p.full + (tiles - p.full) * p.cut;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), lds, stream, p);
+  return hipGetLastError();
+}
+
+template <int TN, int TM, int kStages, int kGroups, int kXFmt>
+hipError_t run_small(Fp8Gemm p, hipStream_t stream) {
+  static std::atomic<uint64_t> raised{0};
+  auto kern = fp8_gemm_small_kernel<TN, TM, kStages, kGroups, kXFmt>;
+  constexpr size_t lds = kGroups * kStages * (TN + TM) * 128;
   if (lds > 65536) {
     hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), lds, raised);
     if (e != hipSuccess) return e;
   }
   p.nM = (int)((p.M + TM - 1) / TM);
   p.nN = (int)((p.N + TN - 1) / TN);
-  hipLaunchKernelGGL(kern, dim3((unsigned)p.nM * (unsigned)p.nN),
-                     dim3((TN / WN) * (TM / WM) * 64), lds, stream, p);
+  p.group = 4;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(p.nM * p.nN)), dim3(256 * kGroups), lds, stream, p);
   return hipGetLastError();
+}
+
+template <int RN, int kXFmt>
+hipError_t run_few(const Fp8Few& q, hipStream_t stream) {
+  auto kern = fp8_few_kernel<RN, kXFmt>;
+  const dim3 grid((unsigned)((q.g.N + 16 * RN - 1) / (16 * RN)), (unsigned)((q.g.M + 15) / 16));
+  hipLaunchKernelGGL(kern, grid, dim3(kFewWaves * 64), 0, stream, q);
+  return hipGetLastError();
+}
+
+// Tile by the number of workgroups it gives. 256 x 256 moves the fewest
+// operand bytes per product and is fastest once the chip is full (8192^3:
+// 398 us; 128 x 128 in two workgroups per compute unit 497 us); smaller tiles
+// spread a small output over more compute units. From a graph of calls on
+// rotating weights (us per call, 2 to 3 of them the graph's):
+//   M x N x K            64 x 64   128 x 64   256 x 256 in parts
+//   64 x 4096 x 4096     13.8 (14.4)  16.8 (17.5)   20.8
+//   512 x 4096 x 4096    25.6 (20.7)  19.4 (20.4)   23.9
+//   300 x 11008 x 4096   47.0 (33.7)  35.5 (29.7)   33.2
+//   1000 x 512 x 512      5.4 (4.3)    6.7 (5.1)     6.9
+// with two sets of waves, in brackets with one: two sets pay from about 16
+// steps on, while every workgroup has a compute unit of its own.
+template <int kXFmt>
+hipError_t run_fmt(const Fp8Gemm& p, hipStream_t stream) {
+  const int64_t mt = (p.M + 63) / 64;
+  const int64_t t64 = mt * ((p.N + 63) / 64), t128 = mt * ((p.N + 127) / 128);
+  const bool two = p.KB >= 16;
+  if (t64 <= 256)
+    return two ? run_small<64, 64, 4, 2, kXFmt>(p, stream) : run_small<64, 64, 4, 1, kXFmt>(p, stream);
+  if (t128 <= 256 && two) return run_small<128, 64, 3, 2, kXFmt>(p, stream);
+  if (t128 < 512) return run_small<128, 64, 3, 1, kXFmt>(p, stream);
+  return run_big<kXFmt>(p, stream);
+}
+
+Fp8Gemm gemm_args(ConstAct8 x, ConstAct8 w, int64_t M, int64_t N, int64_t K, uint16_t* Y) {
+  Fp8Gemm p{};
+  p.x = x.codes; p.xs = x.scales; p.w = w.codes; p.ws = w.scales;
+  p.M = M; p.N = N; p.ldc = act8_row_bytes(K);
+  p.KB = (int)(p.ldc / kAct8Block);
+  p.sb = (int)act8_scale_row_bytes(K);
+  p.Y = Y;
+  return p;
 }
 
 }  // namespace
@@ -239,14 +575,22 @@ hipError_t run_tile(Fp8Gemm p, hipStream_t stream) {
 hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
                            const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
                            hipStream_t stream) {
-  Fp8Gemm p{};
-  p.x = x.codes; p.xs = x.scales; p.w = w.codes; p.ws = w.scales;
-  p.M = M; p.N = N; p.ldc = act8_row_bytes(K);
-  p.KB = (int)(p.ldc / kAct8Block);
-  p.sb = (int)act8_scale_row_bytes(K);
-  p.U = U; p.V = V; p.r64 = r64; p.Y = Y;
-  if (xfmt) return run_tile<128, 128, 64, 64, 1>(p, stream);
-  return run_tile<128, 128, 64, 64, 0>(p, stream);
+  Fp8Gemm p = gemm_args(x, w, M, N, K, Y);
+  p.U = U; p.V = V; p.r64 = r64;
+  return xfmt ? run_fmt<1>(p, stream) : run_fmt<0>(p, stream);
+}
+
+bool fp8_few(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 15) / 16) <= 512; }
+
+hipError_t launch_fp8_few(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
+                          const float* part, int splits, const uint16_t* B, int r, float scale,
+                          uint16_t* Y, float* T_out, hipStream_t stream) {
+  const Fp8Few q{gemm_args(x, w, M, N, K, Y), part, splits, lowrank_cols(r), r, scale, B, T_out};
+  // 16 weight rows per workgroup while that leaves one per compute unit, else
+  // 32 (32 x 4096 x 4096: 11.6 us against 13.8)
+  if ((M + 15) / 16 * ((N + 15) / 16) <= 256)
+    return xfmt ? run_few<1, 1>(q, stream) : run_few<1, 0>(q, stream);
+  return xfmt ? run_few<2, 1>(q, stream) : run_few<2, 0>(q, stream);
 }
 
 }  // namespace qlora

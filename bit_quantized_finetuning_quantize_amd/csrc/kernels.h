@@ -135,6 +135,14 @@ hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_
                            const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
                            hipStream_t stream);
 
+// The same product where its output is small (fp8_few), the adapter's term
+// from split partials of T (launch_rows_act8; null without an adapter);
+// writes T_out.
+bool fp8_few(int64_t M, int64_t N);
+hipError_t launch_fp8_few(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
+                          const float* part, int splits, const uint16_t* B, int r, float scale,
+                          uint16_t* Y, float* T_out, hipStream_t stream);
+
 // The adapter's products beside an 8-bit input (lowrank8.hip).
 // Columns of a low-rank partial or term matrix: r rounded up to 16, 32 or a
 // multiple of 64.
