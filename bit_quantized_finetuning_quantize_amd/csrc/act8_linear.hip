@@ -6,7 +6,7 @@
 //             T (float32), bf16(s T), B^T padded       one launch
 //             Y = dec(X8) dec(W8)^T + (s T) B          8-bit product
 //   backward  G = dY B^T, split along N                row product
-//             bf16(s G); s G and s T in three terms    one launch
+//             bf16(s G); float32 s G and s T          one launch
 //             dX                                       NF4 contraction, or dY to
 //                                                      8 bits and the 8-bit product
 //             dA and dB                                column products, one launch
@@ -27,7 +27,7 @@ namespace {
 
 struct Ws8 {
   int64_t r64;
-  size_t v, u, g3, t3, part, dy8, dys, total;
+  size_t v, u, g, t, part, dy8, dys, total;
 };
 
 // Byte offsets in the workspace, 256-aligned. Each part grows with every
@@ -41,8 +41,8 @@ Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
   auto take = [&](int64_t bytes) { size_t o = off; off += ((size_t)bytes + 255) / 256 * 256; return o; };
   w.v = take(std::max(N, K) * w.r64 * 2);   // B^T or A, padded
   w.u = take(Mp * w.r64 * 2);               // bf16(s T) or bf16(s G)
-  w.g3 = take(3 * w.r64 * Mp * 2);
-  w.t3 = take(3 * w.r64 * Mp * 2);
+  w.g = take(w.r64 * Mp * 4);               // s G and s T for dA and dB
+  w.t = take(w.r64 * Mp * 4);
   // splits * M * columns: 256 tiles of 64 x 64 at most, or one split
   w.part = take(r ? std::max<int64_t>(256 * 64 * 64, Mp * w.r64) * 4 : 0);
   w.dy8 = take(M * act8_row_bytes(N));
@@ -52,14 +52,15 @@ Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 struct Ptrs {
-  uint16_t *v, *u, *g3, *t3;
-  float* part;
+  uint16_t *v, *u;
+  float *g, *t, *part;
   uint8_t *dy8, *dys;
 };
 Ptrs carve(void* ws_, const Ws8& w) {
   char* ws = reinterpret_cast<char*>(ws_);
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
-  return Ptrs{at(w.v), at(w.u), at(w.g3), at(w.t3), reinterpret_cast<float*>(ws + w.part),
+  auto atf = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  return Ptrs{at(w.v), at(w.u), atf(w.g), atf(w.t), atf(w.part),
               reinterpret_cast<uint8_t*>(ws + w.dy8), reinterpret_cast<uint8_t*>(ws + w.dys)};
 }
 
@@ -69,7 +70,7 @@ bool in_place(const uint16_t* A, int r) {
 }
 
 // The adapter's part of a backward pass before dX: bf16(s G) in u, A padded
-// in v (unless it serves as it is), s G and s T in three terms.
+// in v (unless it serves as it is), float32 s G and s T for dA and dB.
 hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, const uint16_t* A,
                      const uint16_t* B, int64_t M, int64_t N, int64_t K, int r, float scale,
                      const Ptrs& w, const Dropout& dr, hipStream_t stream) {
@@ -78,12 +79,12 @@ hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, c
   int splits = 0;
   if (!T) {  // recomputed from the 8-bit input
     QLORA_TRY(launch_rows_act8(x, fmt, M, K, dr.mask, A, r, w.part, &splits, stream));
-    const LowrankOut t{w.part, splits, ldp, f, nullptr, nullptr, w.t3};
+    const LowrankOut t{w.part, splits, ldp, f, nullptr, nullptr, w.t};
     QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{}, M, r, scale, stream));
   }
   QLORA_TRY(launch_rows_bf16(dY, M, N, B, r, w.part, &splits, stream));
-  const LowrankOut o[2] = {{w.part, splits, ldp, f, nullptr, w.u, w.g3},
-                           {T, 1, r, 1.0f, nullptr, nullptr, w.t3}};
+  const LowrankOut o[2] = {{w.part, splits, ldp, f, nullptr, w.u, w.g},
+                           {T, 1, r, 1.0f, nullptr, nullptr, w.t}};
   const LowrankPad pad = in_place(A, r) ? LowrankPad{} : LowrankPad{A, false, K, w.v};
   return launch_lowrank_out(o, T ? 2 : 1, pad, M, r, scale, stream);
 }
@@ -103,7 +104,7 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
   QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, stream));
   if (dX)
     QLORA_TRY(launch_input_grad(dY, W, w.u, in_place(A, r) ? A : w.v, M, N, K, l.r64, dX, stream, dr));
-  return launch_columns(x, fmt, dr.mask, dY, w.g3, w.t3, M, N, K, r, dA, dB, stream);
+  return launch_columns(x, fmt, dr.mask, dY, w.g, w.t, M, N, K, r, dA, dB, stream);
 }
 
 hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A, const uint16_t* B,
@@ -137,7 +138,7 @@ hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, c
                               r ? (in_place(A, r) ? A : w.v) : nullptr, (int)l.r64, dX, stream));
   }
   if (!r) return hipSuccess;
-  return launch_columns(x, fmt, nullptr, dY, w.g3, w.t3, M, N, K, r, dA, dB, stream);
+  return launch_columns(x, fmt, nullptr, dY, w.g, w.t, M, N, K, r, dA, dB, stream);
 }
 
 }  // namespace qlora

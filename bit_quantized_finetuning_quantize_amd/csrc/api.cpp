@@ -91,13 +91,7 @@ int check_act8(const uint8_t* codes, const uint8_t* scales) {
 // Shapes of the linear calls on 8-bit inputs; r = 0 is a call without an adapter.
 int check_fp8_shape(int64_t M, int64_t N, int64_t K, int32_t r) {
   if (M <= 0 || N <= 0 || K <= 0) return QLORA_ERR_INVALID_ARG;
-  if (r) {
-    const int st = check_linear_shape(M, N, K, r);
-    // the three-term factors of dA and dB, [3][r][M] bf16, have 32-bit offsets
-    if (st == QLORA_OK && (M + 63) / 64 * ((r + 63) / 64) >= (int64_t)1 << 16)
-      return QLORA_ERR_UNSUPPORTED;
-    return st;
-  }
+  if (r) return check_linear_shape(M, N, K, r);
   if (N > (int64_t)1 << 21 || K > (int64_t)1 << 21 || M > (int64_t)1 << 30)
     return QLORA_ERR_UNSUPPORTED;
   const int64_t np = (N + 127) / 128 * 128, kp = (K + 127) / 128 * 128;

@@ -448,7 +448,9 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
         const int j = e % kJ;
         float v = 0.0f;
         if (tm < p.M && j < nj) {
-          for (int sp = 0; sp < q.splits; ++sp) v += q.part[((int64_t)sp * p.M + tm) * q.ldp + j0 + j];
+          const float* at = q.part + tm * q.ldp + j0 + j;
+#pragma unroll 8
+          for (int sp = 0; sp < q.splits; ++sp) v += at[(int64_t)sp * p.M * q.ldp];
           if (q.T_out && blockIdx.x == 0) q.T_out[tm * q.r + j0 + j] = v;
         }
         s_t[e / kJ][j] = q.scale * v;

@@ -155,8 +155,8 @@ hipError_t launch_rows_act8(ConstAct8 x, int fmt, int64_t M, int64_t K, const ui
 hipError_t launch_rows_bf16(const uint16_t* S, int64_t M, int64_t C, const uint16_t* B, int r,
                             float* part, int* splits, hipStream_t stream);
 // V = f * (sum of partials, rows ldp apart), as float32 [M x r], as bf16(s V)
-// [Mp x r64], and as three bf16 terms of s V [3][lowrank_cols(r)][Mp]; each
-// output may be null. Up to two of them and one padded copy per launch:
+// [Mp x r64], and as s V in the order launch_columns reads it (Mp x
+// lowrank_cols(r) floats); each output may be null. Up to two of them and one padded copy per launch:
 // dst [rows x r64] from src [rows x r], or from the columns of src [r x rows].
 struct LowrankOut {
   const float* part;
@@ -165,7 +165,7 @@ struct LowrankOut {
   float f;
   float* out32;
   uint16_t* u;
-  uint16_t* v3;
+  float* vf;
 };
 struct LowrankPad {
   const uint16_t* src = nullptr;
@@ -175,9 +175,9 @@ struct LowrankPad {
 };
 hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_t M, int r, float s,
                               hipStream_t stream);
-// dA = D(dec x)^T g, dB = t^T dY from the three-term g and t.
+// dA = D(dec x)^T g, dB = t^T dY, g and t as launch_lowrank_out's vf.
 hipError_t launch_columns(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY,
-                          const uint16_t* g3, const uint16_t* t3, int64_t M, int64_t N, int64_t K,
+                          const float* g, const float* t, int64_t M, int64_t N, int64_t K,
                           int r, float* dA, float* dB, hipStream_t stream);
 
 // Workspace of the three calls below (r may be 0 for the 8-bit weight's).

@@ -15,9 +15,11 @@
 // ds_read_b64_tr_b16 (16 lanes read a 4 x 16 piece by rows and receive it by
 // columns), with no barrier.
 //
-// dA and dB are float32: V enters the column product as three bf16 terms
-// whose sum is the float32 value to 24 bits, so the products of bf16 values
-// carry float32 accuracy. The results of the waves of a workgroup, which
+// dA and dB are float32: V stays float32 in memory and enters the column
+// product as three bf16 terms whose sum is the value to 24 bits, so the
+// products of bf16 values carry float32 accuracy. The terms are formed in
+// registers: V passes once per 64 columns of S and is most of the cache
+// traffic, 4 bytes an element so instead of 6. The results of the waves of a workgroup, which
 // take turns along the contraction, are added in a fixed order.
 #include "act8.h"
 #include "gemm.h"
@@ -55,6 +57,14 @@ struct Stream {
   const uint32_t* mask;   // dropout keep bits [rows][cols / 32], or null
 };
 
+// Place of element (m, j) in the fragment order of V: blocks of 32 rows; in a
+// block by 16 columns; there as the matrix instruction takes it, lane
+// (m / 8 % 4) * 16 + j % 16 with eight consecutive m, so that one fragment is
+// 2 KiB of consecutive memory.
+__device__ __forceinline__ int64_t frag_index(int64_t m, int64_t j, int64_t rp) {
+  return (((m >> 5) * (rp >> 4) + (j >> 4)) * 64 + ((m >> 3) & 3) * 16 + (j & 15)) * 8 + (m & 7);
+}
+
 // The eight transposed elements of a fragment from a row-major tile: lane l
 // receives column (l & 15) + c0 and rows r0 .. r0 + 7 of its own 16-lane
 // group's row base.
@@ -67,28 +77,43 @@ __device__ __forceinline__ bf16x8 tr_frag(uint32_t tile, int row0, int c0, int l
   return as_bf16x8(u32x4{l2[0], l2[1], h2[0], h2[1]});
 }
 
-// Sum of the waves' accumulators in a fixed order (a tree), left in wave 0's
-// registers. `buf` holds kWaves / 2 accumulators. Every wave takes part.
-template <int NF>
-__device__ __forceinline__ void reduce_waves(floatx4 (&acc)[NF], uint32_t buf, int wave, int lane) {
+// The waves' accumulators of one 64 x 16 NJ tile (block f * NJ + jt holds rows
+// f * 16 + 4 g + e, column jt * 16 + i) added in a fixed order: wave w takes
+// wave w + 4's, and the four sums go to LDS as [sum][column][kRowPitch rows],
+// where tile_sum adds them. Every thread of the workgroup takes part.
+constexpr int kRowPitch = 68;  // floats; 16 columns' 16-byte pieces on distinct banks
+constexpr int tile_bytes(int NJ) { return 4 * 16 * NJ * kRowPitch * 4; }
+
+template <int NJ>
+__device__ __forceinline__ void reduce_waves(floatx4 (&acc)[4 * NJ], uint32_t buf, int wave, int lane) {
+  const uint32_t mine = buf + (uint32_t)((((wave & 3) * 16 * NJ + (lane & 15)) * kRowPitch + (lane >> 4) * 4) * 4);
+  __syncthreads();
 #pragma unroll
-  for (int n = kWaves / 2; n >= 1; n >>= 1) {
-    __syncthreads();
-    if (wave >= n && wave < 2 * n) {
+  for (int pass = 0; pass < 2; ++pass) {
+    if ((pass == 0) == (wave >= 4)) {
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
-        *(lds_floatx4*)(uintptr_t)(buf + (uint32_t)((((wave - n) * NF + f) * 64 + lane) * 16)) = acc[f];
+      for (int b = 0; b < 4 * NJ; ++b)
+        *(lds_floatx4*)(uintptr_t)(mine + (uint32_t)(((b % NJ) * 16 * kRowPitch + (b / NJ) * 16) * 4)) = acc[b];
     }
     __syncthreads();
-    if (wave < n) {
+    if (pass == 0 && wave < 4) {
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const floatx4 o = *(const lds_floatx4*)(uintptr_t)(buf + (uint32_t)(((wave * NF + f) * 64 + lane) * 16));
+      for (int b = 0; b < 4 * NJ; ++b) {
+        const floatx4 o =
+            *(const lds_floatx4*)(uintptr_t)(mine + (uint32_t)(((b % NJ) * 16 * kRowPitch + (b / NJ) * 16) * 4));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[f][e] += o[e];
+        for (int e = 0; e < 4; ++e) acc[b][e] += o[e];
       }
     }
   }
+}
+template <int NJ>
+__device__ __forceinline__ float tile_sum(uint32_t buf, int row, int col) {
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    v += *(const lds_f32*)(uintptr_t)(buf + (uint32_t)(((w * 16 * NJ + col) * kRowPitch + row) * 4));
+  return v;
 }
 
 // ---------------------------------------------------------------------------
@@ -113,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone
   constexpr int NF = 4 * NJ;
   constexpr int kTile = 64 * kPitch;
-  constexpr int kRed = kWaves / 2 * NF * 1024;
+  constexpr int kRed = tile_bytes(NJ);
   __shared__ __attribute__((aligned(16))) uint8_t smem[kTrans && kWaves * kTile > kRed ? kWaves * kTile : kRed];
   const uint32_t lds = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
   const int lane = threadIdx.x & 63;
@@ -135,42 +160,68 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
 #pragma unroll
   for (int f = 0; f < NF; ++f) acc[f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const int end = min(p.steps, (split + 1) * p.per);
-  for (int st = split * p.per + wave; st < end; st += kWaves) {
-    u32x4 x[4][2];  // bf16 pairs: two matrix steps of 8 elements, four row blocks
+  // One step's loads: S (codes, scales and keep bits, or values) and W. The
+  // next step's are issued before the present one is worked on.
+  struct Regs {
+    u32x4 s[4][kSrc == kBf16 ? 2 : 1];
+    uint32_t sc[4], keep[4];
+    u32x4 w[2 * NJ];
+  };
+  auto load = [&](int st) {
+    Regs q;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const int row = f * 16 + i;
       if constexpr (kSrc == kBf16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          x[f][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          q.s[f][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
               rs, (int)(row * p.s.ld) + g * 32 + h * 16, st * 128, 0));
       } else {
-        const u32x4 c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+        q.s[f][0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
             rs, (int)(row * p.s.ld) + g * 16, st * 64, 0));
-        const float sc = act8_scale(__builtin_amdgcn_raw_buffer_load_b8(rsc, (int)(row * p.s.sld), st >> 1, 0));
-        x[f][0] = act8_decode8<kSrc>(u32x2{c[0], c[1]}, sc);
-        x[f][1] = act8_decode8<kSrc>(u32x2{c[2], c[3]}, sc);
-        if constexpr (kMask) {
-          const uint32_t bits = __builtin_amdgcn_raw_buffer_load_b32(
-              rm, (int)(row * mld * 4) + (g >> 1) * 4, st * 8, 0) >> ((g & 1) * 16);
-          x[f][0] &= keep_mask8(bits);
-          x[f][1] &= keep_mask8(bits >> 8);
-        }
+        q.sc[f] = __builtin_amdgcn_raw_buffer_load_b8(rsc, (int)(row * p.s.sld), st >> 1, 0);
+        if constexpr (kMask)
+          q.keep[f] = __builtin_amdgcn_raw_buffer_load_b32(rm, (int)(row * mld * 4) + (g >> 1) * 4, st * 8, 0);
       }
     }
-    bf16x8 w[NJ][2];
     if constexpr (kTrans) {
-      // rows st * 64 .. + 63 of A, columns j0 .. j0 + 16 NJ - 1, by way of LDS
+      // rows st * 64 .. + 63 of A, columns j0 .. j0 + 16 NJ - 1
       if (p.wvec) {
 #pragma unroll
-        for (int q = 0; q < 2 * NJ; ++q) {
-          const int id = q * 64 + lane, row = id / (2 * NJ), ch = id % (2 * NJ);
+        for (int e = 0; e < 2 * NJ; ++e) {
+          const int id = e * 64 + lane, row = id / (2 * NJ), ch = id % (2 * NJ);
           const bool ok = j0 + ch * 8 < p.r;  // r is a multiple of 8 here
-          const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          q.w[e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
               rw, ok ? (row * p.r + j0 + ch * 8) * 2 : 0x7ffffff0, st * 64 * p.r * 2, 0));
-          *(lds_u32x4*)(uintptr_t)(wt + (uint32_t)(row * kPitch + ch * 16)) = v;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int jt = 0; jt < NJ; ++jt) {
+        const int j = j0 + jt * 16 + i;
+        const int off = j < p.r ? (int)(j * p.s.cols * 2) + g * 32 : 0x7ffffff0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          q.w[jt * 2 + h] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, off + h * 16, st * 128, 0));
+      }
+    }
+    return q;
+  };
+  const int end = min(p.steps, (split + 1) * p.per);
+  const int begin = split * p.per + wave;
+  Regs now = load(begin);
+  for (int st = begin; st < end; st += kWaves) {
+    const Regs q = now;
+    if (st + kWaves < end) now = load(st + kWaves);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kTrans) {  // A's rows to LDS, back by columns
+      if (p.wvec) {
+#pragma unroll
+        for (int e = 0; e < 2 * NJ; ++e) {
+          const int id = e * 64 + lane, row = id / (2 * NJ), ch = id % (2 * NJ);
+          *(lds_u32x4*)(uintptr_t)(wt + (uint32_t)(row * kPitch + ch * 16)) = q.w[e];
         }
       } else {
         for (int e = lane; e < 64 * 16 * NJ; e += 64) {
@@ -180,42 +231,38 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
           *(gemm::lds_u16*)(uintptr_t)(wt + (uint32_t)(row * kPitch + j * 2)) = v;
         }
       }
-#pragma unroll
-      for (int jt = 0; jt < NJ; ++jt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) w[jt][h] = tr_frag(wt, 16 * g + 8 * h, jt * 16, lane);
-    } else {
-#pragma unroll
-      for (int jt = 0; jt < NJ; ++jt) {
-        const int j = j0 + jt * 16 + i;
-        const int off = j < p.r ? (int)(j * p.s.cols * 2) + g * 32 : 0x7ffffff0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          w[jt][h] = as_bf16x8(__builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, off + h * 16, st * 128, 0)));
-      }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      bf16x8 w[NJ];
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
+      for (int jt = 0; jt < NJ; ++jt) {
+        if constexpr (kTrans) w[jt] = tr_frag(wt, 16 * g + 8 * h, jt * 16, lane);
+        else w[jt] = as_bf16x8(q.w[jt * 2 + h]);
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        u32x4 x;
+        if constexpr (kSrc == kBf16) {
+          x = q.s[f][h];
+        } else {
+          x = act8_decode8<kSrc>(u32x2{q.s[f][0][2 * h], q.s[f][0][2 * h + 1]}, act8_scale((int)q.sc[f]));
+          if constexpr (kMask) x &= keep_mask8(q.keep[f] >> ((g & 1) * 16 + 8 * h));
+        }
 #pragma unroll
         for (int jt = 0; jt < NJ; ++jt)
-          acc[f * NJ + jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[f][h]), w[jt][h],
+          acc[f * NJ + jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x), w[jt],
                                                                      acc[f * NJ + jt], 0, 0, 0);
-  }
-  reduce_waves<NF>(acc, lds, wave, lane);
-  if (wave != 0) return;
-#pragma unroll
-  for (int f = 0; f < 4; ++f)
-#pragma unroll
-    for (int jt = 0; jt < NJ; ++jt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t m = m0 + f * 16 + g * 4 + e;
-        if (m < p.s.rows)
-          p.part[((int64_t)split * p.s.rows + m) * p.ldp + j0 + jt * 16 + i] = acc[f * NJ + jt][e];
       }
+    }
+  }
+  reduce_waves<NJ>(acc, lds, wave, lane);
+#pragma unroll
+  for (int q = 0; q < 2 * NJ; ++q) {
+    const int o = q * kThreads + threadIdx.x, j = o % (16 * NJ), ml = o / (16 * NJ);
+    const float v = tile_sum<NJ>(lds, ml, j);
+    if (m0 + ml < p.s.rows) p.part[((int64_t)split * p.s.rows + m0 + ml) * p.ldp + j0 + j] = v;
+  }
 #endif
 }
 
@@ -224,8 +271,9 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
 // written as any of
 //   out32  float32 V [M x r]
 //   u      bf16(s V), [Mp x r64], 0 past M and r
-//   v3     three bf16 terms of s V, transposed: [3][rp][Mp], 0 past M and r
-// 64 x 64 tiles, through LDS for the transposed form.
+//   vf     s V in float32 in the order a column product reads it
+//          (frag_index), 0 past M and r
+// 16 x 64 tiles, through LDS for the last form.
 struct OutJob {
   const float* part;  // null: no job
   int splits;
@@ -233,7 +281,7 @@ struct OutJob {
   float f;
   float* out32;
   uint16_t* u;
-  uint16_t* v3;
+  float* vf;
 };
 // Padded copies of adapter operands: dst [rows x r64] from A [rows x r]
 // (row-major), or from the columns of B [r x rows].
@@ -245,66 +293,78 @@ struct PadJob {
 };
 
 constexpr int kOutThreads = 256;
+constexpr int kOutRows = 16;  // rows of M per workgroup
 
 __device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, int64_t M, int64_t Mp,
                                          int r, int64_t r64, int64_t rp, float s, float (&tile)[64][65]) {
   const int t = threadIdx.x;
-#pragma unroll 4
-  for (int q = 0; q < 16; ++q) {
-    const int jl = t & 63, ml = (t >> 6) + 4 * q;
-    const int64_t m = mt * 64 + ml;
-    const int j = jc * 64 + jl;
-    float v = 0.0f;
-    if (m < M && j < r) {
-      for (int sp = 0; sp < jb.splits; ++sp) v += jb.part[((int64_t)sp * M + m) * jb.ldp + j];
-      v *= jb.f;
-      if (jb.out32) jb.out32[m * r + j] = v;
-    }
-    v *= s;
-    if (jb.u) jb.u[m * r64 + j] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
-    tile[ml][jl] = v;
-  }
-  if (!jb.v3) return;
-  __syncthreads();
-#pragma unroll 4
-  for (int q = 0; q < 16; ++q) {
-    const int ml = t & 63, jl = (t >> 6) + 4 * q;
-    const int64_t j = jc * 64 + jl;
-    if (j >= rp) continue;
-    float rest = tile[ml][jl];
+  float v[4];
+  const int jl = t & 63, j = jc * 64 + jl;
+  const int64_t m0 = mt * kOutRows + (t >> 6);
+  // loads inside the product's rows and columns, so that none is conditional
+  // and all of a few splits are in flight together
+  const float* at[4];
 #pragma unroll
-    for (int c = 0; c < kTerms; ++c) {
-      const uint32_t b = pack_bf16x2(rest, 0.0f) & 0xffffu;
-      jb.v3[(c * rp + j) * Mp + mt * 64 + ml] = (uint16_t)b;
-      // exact; nothing is left of an infinity or NaN, which the first term carries
-      const float top = __builtin_bit_cast(float, b << 16);
-      rest = __builtin_isfinite(top) ? rest - top : 0.0f;
-    }
+  for (int q = 0; q < 4; ++q) {
+    v[q] = 0.0f;
+    at[q] = jb.part + min(m0 + 4 * q, M - 1) * jb.ldp + min(j, r - 1);
   }
+  const int64_t stride = M * jb.ldp;
+#pragma unroll 8
+  for (int sp = 0; sp < jb.splits; ++sp)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] += at[q][sp * stride];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (m0 + 4 * q >= M || j >= r) v[q] = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t m = m0 + 4 * q;
+    v[q] *= jb.f;
+    if (jb.out32 && m < M && j < r) jb.out32[m * r + j] = v[q];
+    v[q] *= s;
+    if (jb.u) jb.u[m * r64 + j] = (uint16_t)(pack_bf16x2(v[q], 0.0f) & 0xffffu);
+    tile[(t >> 6) + 4 * q][jl] = v[q];
+  }
+  if (!jb.vf) return;
+  __syncthreads();
+  // four consecutive m of one j per thread
+  const int ja = t >> 2, ml = (t & 3) * 4;
+  if (jc * 64 + ja >= rp) return;
+  floatx4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = tile[ml + e][ja];
+  *reinterpret_cast<floatx4*>(jb.vf + frag_index(mt * kOutRows + ml, jc * 64 + ja, rp)) = o;
 }
 
 __device__ __forceinline__ void pad_tile(const PadJob& jb, int64_t rt, int jc, int r, int64_t r64,
                                          float (&tile)[64][65]) {
   const int t = threadIdx.x;
+  uint32_t v[16];
   if (!jb.columns) {
-#pragma unroll 4
+#pragma unroll
     for (int q = 0; q < 16; ++q) {
       const int64_t row = rt * 64 + (t >> 6) + 4 * q;
       const int j = jc * 64 + (t & 63);
-      if (row < jb.rows) jb.dst[row * r64 + j] = j < r ? jb.src[row * r + j] : (uint16_t)0;
+      v[q] = row < jb.rows && j < r ? jb.src[row * r + j] : 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int64_t row = rt * 64 + (t >> 6) + 4 * q;
+      if (row < jb.rows) jb.dst[row * r64 + jc * 64 + (t & 63)] = (uint16_t)v[q];
     }
     return;
   }
-#pragma unroll 4
+#pragma unroll
   for (int q = 0; q < 16; ++q) {  // read along the rows of B
     const int64_t row = rt * 64 + (t & 63);
-    const int jl = (t >> 6) + 4 * q, j = jc * 64 + jl;
-    uint32_t v = 0;
-    if (row < jb.rows && j < r) v = jb.src[(int64_t)j * jb.rows + row];
-    tile[t & 63][jl] = __builtin_bit_cast(float, v);
+    const int j = jc * 64 + (t >> 6) + 4 * q;
+    v[q] = row < jb.rows && j < r ? jb.src[(int64_t)j * jb.rows + row] : 0u;
   }
+#pragma unroll
+  for (int q = 0; q < 16; ++q) tile[t & 63][(t >> 6) + 4 * q] = __builtin_bit_cast(float, v[q]);
   __syncthreads();
-#pragma unroll 4
+#pragma unroll
   for (int q = 0; q < 16; ++q) {
     const int rl = (t >> 6) + 4 * q;
     const int64_t row = rt * 64 + rl;
@@ -320,7 +380,7 @@ struct OutArgs {
   int r;
   int64_t r64, rp;
   float s;
-  int mtiles, blocks0, blocks1;  // row tiles of M; blocks of the two out jobs
+  int blocks0, blocks1;  // workgroups of the two out jobs
 };
 
 __global__ void __launch_bounds__(kOutThreads) lowrank_out_kernel(OutArgs p) {
@@ -339,20 +399,35 @@ __global__ void __launch_bounds__(kOutThreads) lowrank_out_kernel(OutArgs p) {
 // waves take 32 rows of S at a time in turn.
 struct ColProd {
   Stream s;
-  const uint16_t* v3;  // [3][rp][Mp]
+  const float* v;      // V in fragment order
   float* out;          // element (c, j) at c * oc + j * oj
   int64_t oc, oj;
 };
 struct ColPair {
   ColProd a, b;   // a: 8-bit S, b: bf16 S
   int ta;         // column tiles of a
-  int64_t Mp;
   int r, rp;
 };
 
+// Eight floats as three bf16 terms each: every remainder is exact, so the
+// terms' sum is the float to 24 bits. An infinity's remainder is a NaN.
+__device__ __forceinline__ void split3(const floatx4 (&v)[2], u32x4 (&term)[kTerms]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float a = v[e >> 1][(e & 1) * 2], b = v[e >> 1][(e & 1) * 2 + 1];
+#pragma unroll
+    for (int c = 0; c < kTerms; ++c) {
+      const uint32_t w = pack_bf16x2(a, b);
+      term[c][e] = w;
+      a -= __builtin_bit_cast(float, w << 16);
+      b -= __builtin_bit_cast(float, w & 0xffff0000u);
+    }
+  }
+}
+
 template <int kSrc, bool kMask, int NJ>
-__device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0, int64_t Mp, int r,
-                                               int rp, uint32_t lds, int wave, int lane) {
+__device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0, int r, int rp,
+                                                uint32_t lds, int wave, int lane) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int NF = 4 * NJ;
   const int i = lane & 15, g = lane >> 4;
@@ -363,39 +438,66 @@ __device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0,
   const __amdgpu_buffer_rsrc_t rsc = make_rsrc(p.s.scales + (c0 >> 7), p.s.rows * p.s.sld - (c0 >> 7));
   const int64_t mld = p.s.cols / 32;
   const __amdgpu_buffer_rsrc_t rm = make_rsrc(p.s.mask + (c0 >> 5), p.s.rows * mld * 4 - (c0 >> 5) * 4);
-  const __amdgpu_buffer_rsrc_t rv = make_rsrc(p.v3, (int64_t)kTerms * rp * Mp * 2);
-  int ov[NJ];
-#pragma unroll
-  for (int jt = 0; jt < NJ; ++jt) ov[jt] = (int)(((int64_t)(j0 + jt * 16 + i) * Mp + g * 8) * 2);
-  const int term = (int)((int64_t)rp * Mp * 2);
+  // fragments of one block of 32 rows: rp / 16 of 2 KiB
+  const float* vb = p.v + (int64_t)(j0 >> 4) * 512 + lane * 8;
+  const int64_t vblock = (int64_t)rp * 32;
 
   floatx4 acc[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) acc[f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  constexpr int kS = kSrc == kBf16 ? 4 : 2;
+  struct Regs {
+    u32x4 s[kS];
+    uint32_t sc[2], keep[2];
+    floatx4 v[NJ][2];
+  };
   const int steps = (int)((p.s.rows + 31) / 32);
-  for (int st = wave; st < steps; st += kWaves) {
+  // One step's loads: 32 rows of S by 64 columns, and V's fragments. The next
+  // step's are issued before the present one is worked on.
+  auto load = [&](int st) {
+    Regs q;
     if constexpr (kSrc == kBf16) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = q * 8 + (lane >> 3), ch = lane & 7;
-        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            rs, (int)((st * 32 + row) * p.s.ld) + ch * 16, 0, 0));
-        *(lds_u32x4*)(uintptr_t)(tile + (uint32_t)(row * kPitch + ch * 16)) = v;
-      }
+      for (int e = 0; e < 4; ++e)
+        q.s[e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+            rs, (int)((st * 32 + e * 8 + (lane >> 3)) * p.s.ld) + (lane & 7) * 16, 0, 0));
     } else {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int row = q * 16 + (lane >> 2), ch = lane & 3;
-        const int64_t m = (int64_t)st * 32 + row;
-        const u32x4 c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+      for (int e = 0; e < 2; ++e) {
+        const int m = st * 32 + e * 16 + (lane >> 2), ch = lane & 3;
+        q.s[e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
             rs, (int)(m * p.s.ld) + ch * 16, 0, 0));
-        const float sc = act8_scale(__builtin_amdgcn_raw_buffer_load_b8(rsc, (int)(m * p.s.sld), 0, 0));
-        u32x4 lo = act8_decode8<kSrc>(u32x2{c[0], c[1]}, sc);
-        u32x4 hi = act8_decode8<kSrc>(u32x2{c[2], c[3]}, sc);
+        q.sc[e] = __builtin_amdgcn_raw_buffer_load_b8(rsc, (int)(m * p.s.sld), 0, 0);
+        if constexpr (kMask)
+          q.keep[e] = __builtin_amdgcn_raw_buffer_load_b32(rm, (int)(m * mld * 4) + (ch >> 1) * 4, 0, 0);
+      }
+    }
+    const float* v = vb + min(st, steps - 1) * vblock;  // a wave without a step loads one it does not use
+#pragma unroll
+    for (int jt = 0; jt < NJ; ++jt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) q.v[jt][h] = *reinterpret_cast<const floatx4*>(v + jt * 512 + h * 4);
+    return q;
+  };
+  Regs now = load(wave);
+  for (int st = wave; st < steps; st += kWaves) {
+    const Regs q = now;
+    if (st + kWaves < steps) now = load(st + kWaves);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kSrc == kBf16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *(lds_u32x4*)(uintptr_t)(tile + (uint32_t)((e * 8 + (lane >> 3)) * kPitch + (lane & 7) * 16)) = q.s[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = e * 16 + (lane >> 2), ch = lane & 3;
+        const float sc = act8_scale((int)q.sc[e]);
+        u32x4 lo = act8_decode8<kSrc>(u32x2{q.s[e][0], q.s[e][1]}, sc);
+        u32x4 hi = act8_decode8<kSrc>(u32x2{q.s[e][2], q.s[e][3]}, sc);
         if constexpr (kMask) {
-          const uint32_t bits = __builtin_amdgcn_raw_buffer_load_b32(
-              rm, (int)(m * mld * 4) + (ch >> 1) * 4, 0, 0) >> ((ch & 1) * 16);
+          const uint32_t bits = q.keep[e] >> ((ch & 1) * 16);
           lo &= keep_mask8(bits);
           hi &= keep_mask8(bits >> 8);
         }
@@ -403,48 +505,43 @@ __device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0,
         *(lds_u32x4*)(uintptr_t)(tile + (uint32_t)(row * kPitch + ch * 32 + 16)) = hi;
       }
     }
-    bf16x8 v[kTerms][NJ];
+    bf16x8 x[4];
 #pragma unroll
-    for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-      for (int jt = 0; jt < NJ; ++jt)
-        v[t][jt] = as_bf16x8(__builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rv, ov[jt] + t * term, st * 64, 0)));
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const bf16x8 x = tr_frag(tile, 8 * g, f * 16, lane);
-#pragma unroll
-      for (int jt = 0; jt < NJ; ++jt)
-#pragma unroll
-        for (int t = kTerms - 1; t >= 0; --t)
-          acc[f * NJ + jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, v[t][jt], acc[f * NJ + jt], 0, 0, 0);
-    }
-  }
-  reduce_waves<NF>(acc, lds, wave, lane);
-  if (wave != 0) return;
-#pragma unroll
-  for (int f = 0; f < 4; ++f)
+    for (int f = 0; f < 4; ++f) x[f] = tr_frag(tile, 8 * g, f * 16, lane);
 #pragma unroll
     for (int jt = 0; jt < NJ; ++jt) {
-      const int j = j0 + jt * 16 + i;
-      if (j >= r) continue;
+      u32x4 term[kTerms];
+      split3(q.v[jt], term);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        p.out[(c0 + f * 16 + g * 4 + e) * p.oc + j * p.oj] = acc[f * NJ + jt][e];
+      for (int c = kTerms - 1; c >= 0; --c)  // smallest terms first
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          acc[f * NJ + jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[f], as_bf16x8(term[c]),
+                                                                     acc[f * NJ + jt], 0, 0, 0);
     }
+  }
+  reduce_waves<NJ>(acc, lds, wave, lane);
+  // dA's rows run along j, dB's along the columns of S
+#pragma unroll
+  for (int q = 0; q < 2 * NJ; ++q) {
+    const int o = q * kThreads + threadIdx.x;
+    const int j = kSrc == kBf16 ? o / 64 : o % (16 * NJ), c = kSrc == kBf16 ? o % 64 : o / (16 * NJ);
+    const float v = tile_sum<NJ>(lds, c, j);
+    if (j0 + j < r) p.out[(c0 + c) * p.oc + (j0 + j) * p.oj] = v;
+  }
 #endif
 }
 
 template <int kSrc, bool kMask, int NJ>
 __global__ void __launch_bounds__(kThreads) column_products_kernel(ColPair p) {
-  constexpr int kRed = kWaves / 2 * 4 * NJ * 1024, kTiles = kWaves * 32 * kPitch;
+  constexpr int kRed = tile_bytes(NJ), kTiles = kWaves * 32 * kPitch;
   __shared__ __attribute__((aligned(16))) uint8_t smem[kTiles > kRed ? kTiles : kRed];
   const uint32_t lds = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x, j0 = blockIdx.y * 64;
-  if (b < p.ta) column_product<kSrc, kMask, NJ>(p.a, b, j0, p.Mp, p.r, p.rp, lds, wave, lane);
-  else column_product<kBf16, false, NJ>(p.b, b - p.ta, j0, p.Mp, p.r, p.rp, lds, wave, lane);
+  if (b < p.ta) column_product<kSrc, kMask, NJ>(p.a, b, j0, p.r, p.rp, lds, wave, lane);
+  else column_product<kBf16, false, NJ>(p.b, b - p.ta, j0, p.r, p.rp, lds, wave, lane);
 }
 
 }  // namespace lr8
@@ -526,12 +623,11 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
   p.r64 = ceil_div(r, 64) * 64;
   p.rp = lowrank_cols(r);
   p.s = s;
-  p.mtiles = (int)ceil_div(M, 64);
   for (int i = 0; i < n; ++i)
-    p.o[i] = OutJob{o[i].part, o[i].splits, o[i].ldp, o[i].f, o[i].out32, o[i].u, o[i].v3};
+    p.o[i] = OutJob{o[i].part, o[i].splits, o[i].ldp, o[i].f, o[i].out32, o[i].u, o[i].vf};
   p.pad = PadJob{pad.src, pad.columns, pad.rows, pad.dst};
-  p.blocks0 = p.mtiles;
-  p.blocks1 = n > 1 ? p.mtiles : 0;
+  p.blocks0 = (int)(p.Mp / kOutRows);
+  p.blocks1 = n > 1 ? p.blocks0 : 0;
   const int64_t blocks = p.blocks0 + p.blocks1 + (pad.src ? ceil_div(pad.rows, 64) : 0);
   hipLaunchKernelGGL(lowrank_out_kernel, dim3((unsigned)blocks, (unsigned)(p.r64 / 64)),
                      dim3(kOutThreads), 0, stream, p);
@@ -539,13 +635,12 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
 }
 
 hipError_t launch_columns(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY,
-                          const uint16_t* g3, const uint16_t* t3, int64_t M, int64_t N, int64_t K,
+                          const float* g, const float* t, int64_t M, int64_t N, int64_t K,
                           int r, float* dA, float* dB, hipStream_t stream) {
   ColPair p{};
-  p.a = ColProd{act8_stream(x, M, K, mask), g3, dA, (int64_t)r, 1};
-  p.b = ColProd{Stream{dY, nullptr, N * 2, 0, M, N, nullptr}, t3, dB, 1, N};
+  p.a = ColProd{act8_stream(x, M, K, mask), g, dA, (int64_t)r, 1};
+  p.b = ColProd{Stream{dY, nullptr, N * 2, 0, M, N, nullptr}, t, dB, 1, N};
   p.ta = (int)(K / 64);
-  p.Mp = ceil_div(M, 64) * 64;
   p.r = r;
   p.rp = lowrank_cols(r);
   const dim3 grid((unsigned)(K / 64 + N / 64), (unsigned)ceil_div(r, 64)), block(kThreads);

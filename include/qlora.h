@@ -557,8 +557,7 @@ int qlora_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, uint8_t* 
  * bytes of device memory, 256-byte aligned, as for the NF4 linear calls.
  * r = 0 is the workspace of a call without an adapter. 0 for a shape the
  * calls reject: those of the NF4 linear calls (for r = 0 N and K need not be
- * multiples of 64 and the limits hold for them rounded up to 128), and
- * ceil(M/64) ceil(r/64) at or above 2^16. */
+ * multiples of 64 and the limits hold for them rounded up to 128). */
 size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
 
 /* qlora_linear_bwd_act8 — qlora_linear_bwd (and, with a keep mask,

@@ -95,7 +95,7 @@ def test_linear_bwd_act8_rejects(lib):
     for kw in (dict(K=100), dict(N=100), dict(r=0), dict(r=257), dict(r=-1), dict(dY=ODD), dict(B=ODD),
                dict(A=ODD), dict(T=ODD), dict(dX=ODD), dict(dA=ODD), dict(codes=ODD), dict(x=(ODD, FAKE)),
                dict(mask=ODD, p=0.1), dict(mask=FAKE, p=0.1, r=193),
-               dict(M=1 << 20, N=1024), dict(M=1 << 22, N=64, K=64), dict(ws=ODD)):
+               dict(M=1 << 20, N=1024), dict(M=1 << 24, N=64, K=64), dict(ws=ODD)):
         assert _bwd(lib, **kw) == UNSUPPORTED, kw
     assert _bwd(lib, ws=None) == WORKSPACE
     need = lib.qlora_act8_workspace_bytes(32, 128, 128, 8)
@@ -140,7 +140,7 @@ def test_fp8_linear_bwd_rejects(lib):
 def test_workspace_query(lib):
     f = lib.qlora_act8_workspace_bytes
     assert f(16, 100, 100, 0) > 0 and f(16, 100, 100, 8) == 0 and f(0, 64, 64, 8) == 0
-    assert f(1 << 22, 64, 64, 64) == 0  # three-term factors past 32-bit offsets
+    assert f(1 << 24, 64, 64, 64) == 0  # M K = 2^30
     shapes = [(1, 64, 64, 1), (16, 256, 256, 8), (300, 320, 192, 64), (2048, 4096, 11008, 64),
               (4096, 22016, 8192, 128)]
     sizes = [f(*s) for s in shapes]
