@@ -95,10 +95,6 @@ act8_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restr
 // ---------------------------------------------------------------------------
 // SwiGLU: h = g s(g) u with s(g) = 1 / (1 + exp(-g)).
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) {
-  return __builtin_bit_cast(float, w & 0xffff0000u);
-}
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
 
 struct SwigluFwd {
@@ -248,6 +244,54 @@ fp8_weight_quantize_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K,
   }
 }
 
+// ---------------------------------------------------------------------------
+// bf16(w') of a 4-bit store, transposed: one tile of 64 weight rows by 128
+// columns per workgroup. A thread decodes 16 codes of two neighbouring rows
+// (inside one block of 64 each) and writes them to LDS as pairs; the tile is
+// stored by its columns, 128 bytes each.
+constexpr int kTPitch = 136;  // bytes of an LDS row: 64 bf16 and 8 bytes of padding
+
+__global__ void __launch_bounds__(kThreads)
+nf4_dequantize_t_kernel(Nf4Weight W, int64_t N, int64_t K, Codebook cb, uint16_t* __restrict__ out) {
+#pragma clang fp contract(off)
+  __shared__ float s_lv[16];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t[128 * kTPitch];
+  const int t = threadIdx.x;
+  if (t < 16) s_lv[t] = cb.lv[t];
+  const int64_t kt = (K + 127) / 128;
+  const int64_t n0 = blockIdx.x / kt * 64, k0 = blockIdx.x % kt * 128;
+  const int np = t >> 3, q = t & 7;
+  const int64_t k = k0 + q * 16;
+  const bool ok = k < K;  // K is a multiple of 64: a piece of 16 is inside or outside
+  u32x2 c[2];
+  float cs[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t e = (n0 + 2 * np + h) * K + (ok ? k : 0);
+    c[h] = *reinterpret_cast<const u32x2*>(W.codes + e / 2);
+    const int64_t b = e / kBlock;
+    cs[h] = !W.absmax_q ? W.absmax_s2[b]
+            : cb.dq_fp8 ? block_scale_fp8(W.absmax_q[b], W.absmax_s2[b / kGroup])
+                        : block_scale(W.absmax_q[b], W.absmax_s2[b / kGroup]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float lo = s_lv[(c[0][i >> 3] >> (4 * (i & 7))) & 15u] * cs[0];
+    const float hi = s_lv[(c[1][i >> 3] >> (4 * (i & 7))) & 15u] * cs[1];
+    *reinterpret_cast<uint32_t*>(s_t + (q * 16 + i) * kTPitch + np * 4) = pack_bf16x2(lo, hi);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int id = e * kThreads + t, row = id >> 3, ch = id & 7;
+    const u32x2 a = *reinterpret_cast<const u32x2*>(s_t + row * kTPitch + ch * 16);
+    const u32x2 b = *reinterpret_cast<const u32x2*>(s_t + row * kTPitch + ch * 16 + 8);
+    if (k0 + row < K)
+      *reinterpret_cast<u32x4*>(out + (k0 + row) * N + n0 + ch * 8) = u32x4{a[0], a[1], b[0], b[1]};
+  }
+}
+
 bool vec16(const void* p, int64_t ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0;
 }
@@ -312,6 +356,14 @@ hipError_t launch_swiglu_act8_bwd(const uint16_t* dh, int64_t lddh, ConstAct8 g8
   if (vec16(dh, lddh) && vec16(dg, lddg) && vec16(du, lddu))
     return fmt ? go(swiglu_act8_bwd_kernel<1, true>) : go(swiglu_act8_bwd_kernel<0, true>);
   return fmt ? go(swiglu_act8_bwd_kernel<1, false>) : go(swiglu_act8_bwd_kernel<0, false>);
+}
+
+hipError_t launch_nf4_dequantize_t(Nf4Weight W, int64_t N, int64_t K, uint16_t* out,
+                                   hipStream_t stream) {
+  const int64_t tiles = N / 64 * ((K + 127) / 128);
+  hipLaunchKernelGGL(nf4_dequantize_t_kernel, dim3((unsigned)tiles), dim3(kThreads), 0, stream, W, N,
+                     K, codebook_of(W), out);
+  return hipGetLastError();
 }
 
 hipError_t launch_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, Act8 w8, Act8 w8t,

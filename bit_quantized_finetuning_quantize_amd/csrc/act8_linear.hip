@@ -25,9 +25,11 @@ namespace {
     if (e_ != hipSuccess) return e_;       \
   } while (0)
 
+bool dequantize_first(int64_t M) { return M >= (getenv("DQM") ? atoi(getenv("DQM")) : 512); }
+
 struct Ws8 {
   int64_t r64;
-  size_t v, u, g, t, part, dy8, dys, total;
+  size_t v, u, g, t, part, dy8, dys, wt, total;
 };
 
 // Byte offsets in the workspace, 256-aligned. Each part grows with every
@@ -47,6 +49,9 @@ Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
   w.part = take(r ? std::max<int64_t>(256 * 64 * 64, Mp * w.r64) * 4 : 0);
   w.dy8 = take(M * act8_row_bytes(N));
   w.dys = take(M * act8_scale_row_bytes(N));
+  // the NF4 backward's decoded weight, in the place of the 8-bit dY
+  w.wt = w.dy8;
+  if (r && dequantize_first(M)) off = std::max(off, w.wt + (size_t)(N * K * 2));
   w.total = off;
   return w;
 }
@@ -55,13 +60,14 @@ struct Ptrs {
   uint16_t *v, *u;
   float *g, *t, *part;
   uint8_t *dy8, *dys;
+  uint16_t* wt;
 };
 Ptrs carve(void* ws_, const Ws8& w) {
   char* ws = reinterpret_cast<char*>(ws_);
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
   auto atf = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   return Ptrs{at(w.v), at(w.u), atf(w.g), atf(w.t), atf(w.part),
-              reinterpret_cast<uint8_t*>(ws + w.dy8), reinterpret_cast<uint8_t*>(ws + w.dys)};
+              reinterpret_cast<uint8_t*>(ws + w.dy8), reinterpret_cast<uint8_t*>(ws + w.dys), at(w.wt)};
 }
 
 // The adapter's rows serve as they are when they are whole 64-column tiles.
@@ -102,7 +108,11 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
   const Ws8 l = ws8_layout(M, N, K, r);
   const Ptrs w = carve(ws, l);
   QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, stream));
-  if (dX)
+  if (dX && dequantize_first(M)) {
+    QLORA_TRY(launch_nf4_dequantize_t(W, N, K, w.wt, stream));
+    QLORA_TRY(launch_bf16_gemm(dY, w.wt, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dr.mask, dX,
+                               stream));
+  } else if (dX)
     QLORA_TRY(launch_input_grad(dY, W, w.u, in_place(A, r) ? A : w.v, M, N, K, l.r64, dX, stream, dr));
   return launch_columns(x, fmt, dr.mask, dY, w.g, w.t, M, N, K, r, dA, dB, stream);
 }

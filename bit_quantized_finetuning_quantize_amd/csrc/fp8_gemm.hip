@@ -29,6 +29,8 @@ struct Fp8Gemm {
   const uint16_t *U, *V;  // bf16 [M x r64], [N x r64], or null
   int r64;
   uint16_t* Y;         // [M x N]
+  const uint32_t* keep;   // bf16 only: mask [M][N / 32] over the U V term, or null
+  bool stream;         // Y is stored past the caches
   int nM, nN, group;   // tiles, and row tiles per group of the walk
   int full, cut;       // 256 x 256 tiles done whole; parts of each other one
 };
@@ -41,9 +43,24 @@ using gemm::make_rsrc;
 using gemm::tile_off;
 using gemm::wait_vmcnt;
 
-template <int kXFmt>
-__device__ __forceinline__ floatx16 mma(i32x8 w, i32x8 x, floatx16 c, uint32_t sw, uint32_t sx) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, kXFmt, 0, (int)sw, 0, (int)sx);
+// Format of the operands: weights E4M3 and activations E4M3 or E5M2, or both
+// bf16 (then a step of 128 bytes is 64 elements, without scales).
+enum Fmt { kE4M3 = 0, kE5M2 = 1, kBf16 = 2 };
+
+// Product of two 32-row fragments of 64 bytes per row.
+template <int kFmt>
+__device__ __forceinline__ floatx16 mma(const u32x4 (&w)[2], const u32x4 (&x)[2], floatx16 c,
+                                        uint32_t sw, uint32_t sx) {
+  if constexpr (kFmt == kBf16) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w[0]), as_bf16x8(x[0]), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w[1]), as_bf16x8(x[1]), c, 0, 0, 0);
+  } else {
+    auto whole = [](const u32x4 (&f)[2]) {
+      return i32x8{(int)f[0][0], (int)f[0][1], (int)f[0][2], (int)f[0][3],
+                   (int)f[1][0], (int)f[1][1], (int)f[1][2], (int)f[1][3]};
+    };
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(whole(w), whole(x), c, 0, kFmt, 0, (int)sw, 0, (int)sx);
+  }
 }
 
 // Tiles are walked in groups of `group` row tiles, column tile outermost in
@@ -62,12 +79,13 @@ __device__ __forceinline__ int xcd_order(int id, int count) {
   return x * (count >> 3) + min(x, count & 7) + (id >> 3);
 }
 
-// Issue order: kN times one product and, beside it, kV loads and kD LDS reads.
-template <int kN, int kV, int kD>
+// Issue order: kN times one product (kP matrix instructions) and, beside it, kV
+// loads and kD LDS reads.
+template <int kN, int kP, int kV, int kD>
 __device__ __forceinline__ void pace() {
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, kP, 0);
     __builtin_amdgcn_sched_group_barrier(0x020, kV, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, kD, 0);
   }
@@ -94,7 +112,7 @@ constexpr int lds_bytes(int TN, int TM, int stages, int groups) {
 // a ring of its own, that take a run of the steps each; the sums of the other
 // sets are added to the first's in order at the end. For grids that leave
 // compute units idle: a step's latency then covers kGroups blocks along K.
-template <int TN, int TM, int kStages, int kGroups, int kXFmt>
+template <int TN, int TM, int kStages, int kGroups, int kFmt>
 __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t m0, uint32_t lds_all) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the kernels' stubs alone
   constexpr int WN = TN / 2, WM = TM / 2;
@@ -150,7 +168,8 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   const __amdgpu_buffer_rsrc_t rsx = make_rsrc(p.xs + m0 * p.sb, (p.M - m0) * p.sb);
   struct Scales { uint32_t w, x[BM]; };
   auto scales = [&](int kb) {
-    Scales s;
+    Scales s{};
+    if constexpr (kFmt == kBf16) return s;
     s.w = __builtin_amdgcn_raw_buffer_load_b32(rsw, (int)((n0 + wn * WN) / 128) * p.sb, first + kb, 0);
 #pragma unroll
     for (int j = 0; j < BM; ++j)
@@ -199,6 +218,23 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
           for (int j = 0; j < BM; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[q][i], b[q][j], acc[i][j], 0, 0, 0);
     }
+    if constexpr (kFmt == kBf16) {
+      if (p.keep) {  // dropped elements of the term become 0
+        const int64_t mld = p.N / 32;
+        const __amdgpu_buffer_rsrc_t rk = make_rsrc(p.keep + m0 * mld, (p.M - m0) * mld * 4);
+#pragma unroll
+        for (int j = 0; j < BM; ++j)
+#pragma unroll
+          for (int i = 0; i < BN; ++i) {
+            const int word = (int)(n0 / 32) + wn * (WN / 32) + i;
+            const uint32_t bits = __builtin_amdgcn_raw_buffer_load_b32(
+                rk, (int)((wm * WM + j * 32 + r) * mld * 4), word * 4, 0) >> (half * 4);
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              if (!((bits >> ((v >> 2) * 8 + (v & 3))) & 1u)) acc[i][j][v] = 0.0f;
+          }
+      }
+    }
   }
 
   // LDS offsets of a fragment's two 16-byte pieces, 4 h + 2 half and the
@@ -219,21 +255,18 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
     const int block = act ? i - 1 : i ? i - BM : 0;
     f.f[i][c] = *(const lds_u32x4*)(uintptr_t)((act ? ox[h][c] : ow[h][c]) + st + (uint32_t)(block * 4096));
   };
-  auto whole = [](const u32x4 (&f)[2]) {
-    return i32x8{(int)f[0][0], (int)f[0][1], (int)f[0][2], (int)f[0][3],
-                 (int)f[1][0], (int)f[1][1], (int)f[1][2], (int)f[1][3]};
-  };
   auto product = [&](const Frags& f, const Scales& s) {
 #pragma unroll
     for (int i = 0; i < BN; ++i)
 #pragma unroll
       for (int j = 0; j < BM; ++j)
-        acc[i][j] = mma<kXFmt>(whole(f.f[i ? i + BM : 0]), whole(f.f[1 + j]), acc[i][j], s.w, s.x[j]);
+        acc[i][j] = mma<kFmt>(f.f[i ? i + BM : 0], f.f[1 + j], acc[i][j], s.w, s.x[j]);
   };
   // Issue order of a half: after each product the LDS reads and the loads
   // that fit beside it, the reads in the first half of the products so that
   // their data is there when the next half begins.
   constexpr int kM = BN * BM, kR = 2 * (BN + BM), kL = kLoadW + kLoadX;
+  constexpr int kP = kFmt == kBf16 ? 2 : 1;
 
   uint32_t cur = 0, nxt = kStage;  // stages of steps kb and kb + 1
   wait_vmcnt<(kStages - 1) * kL>();
@@ -249,8 +282,8 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
       for (int i = 0; i < 2 * (BN + BM); ++i) read1(f1, cur, 1, i / 2, i % 2);
       product(f0, s);
       if constexpr (kM >= 4) {
-        pace<kM / 2, 0, 2 * kR / kM>();
-        pace<kM / 2, 0, 0>();
+        pace<kM / 2, kP, 0, 2 * kR / kM>();
+        pace<kM / 2, kP, 0, 0>();
       }
       __builtin_amdgcn_sched_barrier(0);
       // Step kb + 1 has landed when at most the moves of the kStages - 2 steps
@@ -270,7 +303,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
       }
       static_assert(kL == kR, "one move per piece");
       product(f1, s);
-      if constexpr (kM >= 4) pace<kM, kL / kM, kR / kM>();
+      if constexpr (kM >= 4) pace<kM, kP, kL / kM, kR / kM>();
       __builtin_amdgcn_sched_barrier(0);
       s.w >>= 8;
 #pragma unroll
@@ -330,7 +363,8 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
     if (m >= p.M) continue;
     uint16_t* y = p.Y + m * p.N + n;
     if (vec && n < p.N) {
-      *reinterpret_cast<u32x4*>(y) = d;
+      if (p.stream) __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(y));
+      else *reinterpret_cast<u32x4*>(y) = d;
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -580,6 +614,14 @@ hipError_t run_fmt(const Fp8Gemm& p, hipStream_t stream) {
   return run_big<kXFmt>(p, stream);
 }
 
+// Y past the caches when it and the operands together outgrow the 256 MiB
+// last-level cache: it would push out the operands, which every round of tiles
+// reads again (4096 x 22016 x 8192: 514 us against 552; 8192 x 8192 x 1024,
+// which fits, 73 us against 68).
+bool streams_out(int64_t M, int64_t N, int64_t row_bytes) {
+  return 2 * M * N + (M + N) * row_bytes > ((int64_t)256 << 20);
+}
+
 Fp8Gemm gemm_args(ConstAct8 x, ConstAct8 w, int64_t M, int64_t N, int64_t K, uint16_t* Y) {
   Fp8Gemm p{};
   p.x = x.codes; p.xs = x.scales; p.w = w.codes; p.ws = w.scales;
@@ -587,6 +629,7 @@ Fp8Gemm gemm_args(ConstAct8 x, ConstAct8 w, int64_t M, int64_t N, int64_t K, uin
   p.KB = (int)(p.ldc / kAct8Block);
   p.sb = (int)act8_scale_row_bytes(K);
   p.Y = Y;
+  p.stream = streams_out(M, N, p.ldc);
   return p;
 }
 
@@ -598,6 +641,19 @@ hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_
   Fp8Gemm p = gemm_args(x, w, M, N, K, Y);
   p.U = U; p.V = V; p.r64 = r64;
   return xfmt ? run_fmt<1>(p, stream) : run_fmt<0>(p, stream);
+}
+
+hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
+                            const uint16_t* U, const uint16_t* V, int r64, const uint32_t* keep,
+                            uint16_t* Y, hipStream_t stream) {
+  Fp8Gemm p{};
+  p.x = reinterpret_cast<const uint8_t*>(x);
+  p.w = reinterpret_cast<const uint8_t*>(w);
+  p.M = M; p.N = N; p.ldc = K * 2;
+  p.KB = (int)(K / 64);
+  p.U = U; p.V = V; p.r64 = r64; p.keep = keep; p.Y = Y;
+  p.stream = streams_out(M, N, p.ldc);
+  return run_big<kBf16>(p, stream);
 }
 
 bool fp8_few(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 15) / 16) <= 512; }

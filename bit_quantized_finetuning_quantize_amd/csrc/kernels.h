@@ -135,6 +135,14 @@ hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_
                            const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
                            hipStream_t stream);
 
+// The same for bf16 x [M x K] and w [N x K], K a multiple of 64, with a keep
+// mask [M][N / 32] over the U V^T term (or null).
+hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
+                            const uint16_t* U, const uint16_t* V, int r64, const uint32_t* keep,
+                            uint16_t* Y, hipStream_t stream);
+// out [K x N] = bf16(w')^T of a store of W [N x K], N and K multiples of 64.
+hipError_t launch_nf4_dequantize_t(Nf4Weight W, int64_t N, int64_t K, uint16_t* out, hipStream_t stream);
+
 // The same product where its output is small (fp8_few), the adapter's term
 // from split partials of T (launch_rows_act8; null without an adapter);
 // writes T_out.
