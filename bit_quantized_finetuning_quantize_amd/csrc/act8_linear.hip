@@ -7,8 +7,9 @@
 //             Y = dec(X8) dec(W8)^T + (s T) B          8-bit product
 //   backward  G = dY B^T, split along N                row product
 //             bf16(s G); float32 s G and s T          one launch
-//             dX                                       NF4 contraction, or dY to
-//                                                      8 bits and the 8-bit product
+//             dX                                       NF4: the weight to bf16,
+//                                                      then a bf16 product; 8-bit:
+//                                                      dY to 8 bits, its product
 //             dA and dB                                column products, one launch
 #include "act8.h"
 #include "kernels.h"
@@ -25,7 +26,12 @@ namespace {
     if (e_ != hipSuccess) return e_;       \
   } while (0)
 
-bool dequantize_first(int64_t M) { return M >= (getenv("DQM") ? atoi(getenv("DQM")) : 512); }
+// dX of the NF4 layer: the weight decoded to bf16 once, transposed, and a bf16
+// product on it, or the contraction that decodes tiles on their way in (whole
+// backward, r = 64: 47 us against 80 at 64 x 4096 x 4096, 218 against 228 at
+// 2048 x 11008 x 4096, 506 against 616 at 4096 x 8192 x 8192). Below 2^18
+// weights the one launch less counts (16 x 256 x 256: 27 us against 33).
+bool dequantize_first(int64_t N, int64_t K) { return N * K >= (int64_t)1 << 18; }
 
 struct Ws8 {
   int64_t r64;
@@ -51,7 +57,7 @@ Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
   w.dys = take(M * act8_scale_row_bytes(N));
   // the NF4 backward's decoded weight, in the place of the 8-bit dY
   w.wt = w.dy8;
-  if (r && dequantize_first(M)) off = std::max(off, w.wt + (size_t)(N * K * 2));
+  if (r && dequantize_first(N, K)) off = std::max(off, w.wt + (size_t)(N * K * 2));
   w.total = off;
   return w;
 }
@@ -108,7 +114,7 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
   const Ws8 l = ws8_layout(M, N, K, r);
   const Ptrs w = carve(ws, l);
   QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, stream));
-  if (dX && dequantize_first(M)) {
+  if (dX && dequantize_first(N, K)) {
     QLORA_TRY(launch_nf4_dequantize_t(W, N, K, w.wt, stream));
     QLORA_TRY(launch_bf16_gemm(dY, w.wt, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dr.mask, dX,
                                stream));

@@ -353,24 +353,29 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
       for (int v = 0; v < 16; v += 4)
         *(lds_u32x2*)(uintptr_t)(ob + (uint32_t)((j * 32 + r) * kOutPitch + (i * 32 + (v >> 2) * 8 + half * 4) * 2)) =
             u32x2{pack_bf16x2(acc[i][j][v], acc[i][j][v + 1]), pack_bf16x2(acc[i][j][v + 2], acc[i][j][v + 3])};
-  const bool vec = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 15) == 0;
   constexpr int kPieces = WN / 8;  // 16-byte pieces of a row
+  auto put = [&](auto how) {  // 0: stores of single elements, 1: of pieces, 2: of pieces past the caches
+    constexpr int kHow = decltype(how)::value;
 #pragma unroll 8
-  for (int q = 0; q < WM * kPieces / 64; ++q) {
-    const int id = q * 64 + lane, row = id / kPieces, ch = id % kPieces;
-    const u32x4 d = *(const lds_u32x4*)(uintptr_t)(ob + (uint32_t)(row * kOutPitch + ch * 16));
-    const int64_t m = m0 + wm * WM + row, n = n0 + wn * WN + ch * 8;
-    if (m >= p.M) continue;
-    uint16_t* y = p.Y + m * p.N + n;
-    if (vec && n < p.N) {
-      if (p.stream) __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(y));
-      else *reinterpret_cast<u32x4*>(y) = d;
-    } else {
+    for (int q = 0; q < WM * kPieces / 64; ++q) {
+      const int id = q * 64 + lane, row = id / kPieces, ch = id % kPieces;
+      const u32x4 d = *(const lds_u32x4*)(uintptr_t)(ob + (uint32_t)(row * kOutPitch + ch * 16));
+      const int64_t m = m0 + wm * WM + row, n = n0 + wn * WN + ch * 8;
+      if (m >= p.M) continue;
+      uint16_t* y = p.Y + m * p.N + n;
+      if constexpr (kHow == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (n + e < p.N) y[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+        for (int e = 0; e < 8; ++e)
+          if (n + e < p.N) y[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+      } else if (n < p.N) {
+        if constexpr (kHow == 2) __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(y));
+        else *reinterpret_cast<u32x4*>(y) = d;
+      }
     }
-  }
+  };
+  if (p.N % 8 != 0 || (reinterpret_cast<uintptr_t>(p.Y) & 15) != 0) put(std::integral_constant<int, 0>{});
+  else if (p.stream) put(std::integral_constant<int, 2>{});
+  else put(std::integral_constant<int, 1>{});
 #endif
 }
 
@@ -653,7 +658,7 @@ hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int
   p.KB = (int)(K / 64);
   p.U = U; p.V = V; p.r64 = r64; p.keep = keep; p.Y = Y;
   p.stream = streams_out(M, N, p.ldc);
-  return run_big<kBf16>(p, stream);
+  return run_fmt<kBf16>(p, stream);
 }
 
 bool fp8_few(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 15) / 16) <= 512; }

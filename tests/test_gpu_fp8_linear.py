@@ -97,7 +97,9 @@ def _fwd_check(c, W, Y, T, N, K, r):
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 4096, 4096), (2, 17, 129), (16, 256, 384),
                                    (5, 1000, 1544), (17, 130, 640), (33, 64, 4096), (64, 300, 127),
-                                   (129, 257, 1025), (333, 1001, 1544), (300, 520, 2176)])
+                                   (129, 257, 1025), (333, 1001, 1544), (300, 520, 2176),
+                                   # the large tiles: cut in two, in four, and after a full round
+                                   (1030, 4163, 300), (2040, 2041, 130), (4100, 4100, 140)])
 def test_plain_product(q, M, N, K, fmt):
     print(f"[case] fp8 product M={M} N={N} K={K} fmt={fmt}", flush=True)
     c = Case(q, M, N, K, 0, fmt)
@@ -137,7 +139,7 @@ def _low(c, G, gabs, N, r):
 
 
 SHAPES = [(1, 64, 64, 1), (1, 512, 4096, 16), (16, 256, 256, 8), (7, 192, 320, 3), (65, 128, 64, 64),
-          (100, 1344, 576, 100), (257, 512, 1024, 64), (300, 320, 192, 256)]
+          (100, 1344, 576, 100), (257, 512, 1024, 64), (1100, 256, 4160, 64), (300, 320, 192, 256)]
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
@@ -167,7 +169,7 @@ def test_fp8_linear(q, M, N, K, r, fmt):
 
 @pytest.mark.parametrize("store_type", [0, 3])
 @pytest.mark.parametrize("drop", [0.0, 0.1])
-@pytest.mark.parametrize("M,N,K,r", SHAPES[:7])
+@pytest.mark.parametrize("M,N,K,r", SHAPES[:8])
 def test_nf4_backward(q, M, N, K, r, drop, store_type):
     print(f"[case] nf4 bwd act8 M={M} N={N} K={K} r={r} drop={drop} store={store_type}", flush=True)
     fmt = (M + r) % 2
