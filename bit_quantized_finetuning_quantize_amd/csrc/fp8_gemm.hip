@@ -126,41 +126,46 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   const int wn = wave & 1, wm = wave >> 1;
   const int r = lane & 31, half = lane >> 5;
 
-  // operand moves: 8 rows of 128 bytes per instruction
   // this set's steps: [first, first + KB), whole scale dwords; every set
   // walks KB steps, and those past the end of K read zeros
   const int KB = kGroups == 1 ? p.KB : ((p.KB + kGroups - 1) / kGroups + 3) / 4 * 4;
   const int first = group * KB, valid = p.KB - first;
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + n0 * p.ldc, (p.N - n0) * p.ldc);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + m0 * p.ldc, (p.M - m0) * p.ldc);
-  // the swizzle of rows 16 apart is the same: one lane offset serves every
-  // second instruction
+  // The low-rank term comes first, through the same ring: a step of it is 64
+  // columns of V and U, 128 bytes of a row as in the steps along K.
+  const int LR = p.U ? p.r64 / 64 : 0;
+
+  // operand moves: 8 rows of 128 bytes per instruction. The swizzle of rows 16
+  // apart is the same: one lane offset serves every second instruction.
   const int row0 = wave * (kLoadW * 8) + (lane >> 3), row1 = wave * (kLoadX * 8) + (lane >> 3);
-  int vw[2], vx[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    vw[i] = (int)((row0 + i * 8) * p.ldc) + (((lane & 7) ^ gemm::swz(row0 + i * 8)) << 4);
-    vx[i] = (int)((row1 + i * 8) * p.ldc) + (((lane & 7) ^ gemm::swz(row1 + i * 8)) << 4);
-  }
-  const int step16 = (int)(16 * p.ldc);
-  // move i of a step: weight rows first, then activation rows
-  auto at_step = [&](int kb) {
-    return kb < min(KB, valid) ? (first + kb) * 128 : 0x7f000000;  // past the end: out of range
+  struct Source {
+    __amdgpu_buffer_rsrc_t w, x;
+    int vw[2], vx[2], step16;
   };
-  auto move = [&](int off, uint32_t st, int i) {
+  auto source = [&](const uint8_t* w, const uint8_t* x, int64_t ld) {
+    Source s;
+    s.w = make_rsrc(w + n0 * ld, (p.N - n0) * ld);
+    s.x = make_rsrc(x + m0 * ld, (p.M - m0) * ld);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s.vw[i] = (int)((row0 + i * 8) * ld) + (((lane & 7) ^ gemm::swz(row0 + i * 8)) << 4);
+      s.vx[i] = (int)((row1 + i * 8) * ld) + (((lane & 7) ^ gemm::swz(row1 + i * 8)) << 4);
+    }
+    s.step16 = (int)(16 * ld);
+    return s;
+  };
+  const Source operands = source(p.w, p.x, p.ldc);
+  // byte offset of a step in its rows; past the end out of range
+  auto at_step = [&](int kb) { return kb < min(KB, valid) ? (first + kb) * 128 : 0x7f000000; };
+  // move i of a step: weight rows first, then activation rows
+  auto move = [&](const Source& s, int off, uint32_t st, int i) {
     if (i < kLoadW)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rw, (lds_void*)(uintptr_t)(st + (uint32_t)((wave * kLoadW + i) * 1024)), 16, vw[i & 1],
-          off + (i >> 1) * step16, 0, 0);
+          s.w, (lds_void*)(uintptr_t)(st + (uint32_t)((wave * kLoadW + i) * 1024)), 16, s.vw[i & 1],
+          off + (i >> 1) * s.step16, 0, 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rx, (lds_void*)(uintptr_t)(st + (uint32_t)(TN * 128 + (wave * kLoadX + i - kLoadW) * 1024)),
-          16, vx[(i - kLoadW) & 1], off + ((i - kLoadW) >> 1) * step16, 0, 0);
-  };
-  auto issue = [&](int kb, uint32_t st) {
-    const int off = at_step(kb);
-#pragma unroll
-    for (int i = 0; i < kLoadW + kLoadX; ++i) move(off, st, i);
+          s.x, (lds_void*)(uintptr_t)(st + (uint32_t)(TN * 128 + (wave * kLoadX + i - kLoadW) * 1024)),
+          16, s.vx[(i - kLoadW) & 1], off + ((i - kLoadW) >> 1) * s.step16, 0, 0);
   };
 
   // scale bytes, a dword for four steps; the low byte is the present step's
@@ -177,8 +182,20 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
     return s;
   };
 
-  // Every load of the loop and of this prologue is issued whatever KB is: past
+  // Every load of the loops and of this prologue is issued whatever KB is: past
   // the end it reads nothing, and its stage is not used.
+  const Source lowrank = source(reinterpret_cast<const uint8_t*>(p.V), reinterpret_cast<const uint8_t*>(p.U),
+                                (int64_t)p.r64 * 2);
+  auto at_lowrank = [&](int q) { return group == 0 ? q * 128 : 0x7f000000; };
+  auto issue = [&](int q, uint32_t st) {  // step q of the low-rank steps and those along K
+    if (q < LR) {
+#pragma unroll
+      for (int i = 0; i < kLoadW + kLoadX; ++i) move(lowrank, at_lowrank(q), st, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoadW + kLoadX; ++i) move(operands, at_step(q - LR), st, i);
+    }
+  };
 #pragma unroll
   for (int k = 0; k < kStages; ++k) issue(k, lds0 + (uint32_t)(k * kStage));
   Scales s = scales(0);
@@ -190,52 +207,6 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
     for (int j = 0; j < BM; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-
-  // the low-rank term first, straight from memory
-  if (p.U && group == 0) {
-    const __amdgpu_buffer_rsrc_t ru = make_rsrc(p.U + m0 * p.r64, (p.M - m0) * (int64_t)p.r64 * 2);
-    const __amdgpu_buffer_rsrc_t rv = make_rsrc(p.V + n0 * p.r64, (p.N - n0) * (int64_t)p.r64 * 2);
-    for (int j0 = 0; j0 < p.r64; j0 += 64) {  // 64 columns' loads in flight together
-      bf16x8 a[4][BN], b[4][BM];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-#pragma unroll
-        for (int i = 0; i < BN; ++i)
-          a[q][i] = as_bf16x8(__builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         rv, ((wn * WN + i * 32 + r) * p.r64 + half * 8) * 2, (j0 + q * 16) * 2, 0)));
-#pragma unroll
-        for (int j = 0; j < BM; ++j)
-          b[q][j] = as_bf16x8(__builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         ru, ((wm * WM + j * 32 + r) * p.r64 + half * 8) * 2, (j0 + q * 16) * 2, 0)));
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < BN; ++i)
-#pragma unroll
-          for (int j = 0; j < BM; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[q][i], b[q][j], acc[i][j], 0, 0, 0);
-    }
-    if constexpr (kFmt == kBf16) {
-      if (p.keep) {  // dropped elements of the term become 0
-        const int64_t mld = p.N / 32;
-        const __amdgpu_buffer_rsrc_t rk = make_rsrc(p.keep + m0 * mld, (p.M - m0) * mld * 4);
-#pragma unroll
-        for (int j = 0; j < BM; ++j)
-#pragma unroll
-          for (int i = 0; i < BN; ++i) {
-            const int word = (int)(n0 / 32) + wn * (WN / 32) + i;
-            const uint32_t bits = __builtin_amdgcn_raw_buffer_load_b32(
-                rk, (int)((wm * WM + j * 32 + r) * mld * 4), word * 4, 0) >> (half * 4);
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-              if (!((bits >> ((v >> 2) * 8 + (v & 3))) & 1u)) acc[i][j][v] = 0.0f;
-          }
-      }
-    }
-  }
 
   // LDS offsets of a fragment's two 16-byte pieces, 4 h + 2 half and the
   // next, in row r of the wave's part; rows 32 apart share the swizzle
@@ -255,18 +226,17 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
     const int block = act ? i - 1 : i ? i - BM : 0;
     f.f[i][c] = *(const lds_u32x4*)(uintptr_t)((act ? ox[h][c] : ow[h][c]) + st + (uint32_t)(block * 4096));
   };
-  auto product = [&](const Frags& f, const Scales& s) {
+  auto product = [&](auto fmt, const Frags& f) {
 #pragma unroll
     for (int i = 0; i < BN; ++i)
 #pragma unroll
       for (int j = 0; j < BM; ++j)
-        acc[i][j] = mma<kFmt>(f.f[i ? i + BM : 0], f.f[1 + j], acc[i][j], s.w, s.x[j]);
+        acc[i][j] = mma<decltype(fmt)::value>(f.f[i ? i + BM : 0], f.f[1 + j], acc[i][j], s.w, s.x[j]);
   };
   // Issue order of a half: after each product the LDS reads and the loads
   // that fit beside it, the reads in the first half of the products so that
   // their data is there when the next half begins.
   constexpr int kM = BN * BM, kR = 2 * (BN + BM), kL = kLoadW + kLoadX;
-  constexpr int kP = kFmt == kBf16 ? 2 : 1;
 
   uint32_t cur = 0, nxt = kStage;  // stages of steps kb and kb + 1
   wait_vmcnt<(kStages - 1) * kL>();
@@ -274,42 +244,70 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   Frags f0, f1;
 #pragma unroll
   for (int i = 0; i < 2 * (BN + BM); ++i) read1(f0, 0, 0, i / 2, i % 2);
+  // One step; `from` and `off` are those of the step kStages ahead.
+  auto step = [&](auto fmt, const Source& from, int off) {
+    constexpr int kP = decltype(fmt)::value == kBf16 ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < 2 * (BN + BM); ++i) read1(f1, cur, 1, i / 2, i % 2);
+    product(fmt, f0);
+    if constexpr (kM >= 4) {
+      pace<kM / 2, kP, 0, 2 * kR / kM>();
+      pace<kM / 2, kP, 0, 0>();
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // The next step has landed when at most the moves of the kStages - 2 steps
+    // after it are outstanding (they complete in order; a scale load among
+    // them only makes this wait longer).
+    wait_vmcnt<(kStages - 2) * kL>();
+    gemm::stage_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    // The moves into the stage that is now free, and the reads of the next
+    // step, in turn (their order is kept: both touch LDS).
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      move(from, off, lds0 + cur, i);
+      read1(f0, nxt, 0, i / 2, i % 2);
+    }
+    static_assert(kL == kR, "one move per piece");
+    product(fmt, f1);
+    if constexpr (kM >= 4) pace<kM, kP, kL / kM, kR / kM>();
+    __builtin_amdgcn_sched_barrier(0);
+    cur = nxt;
+    nxt = nxt + kStage == kStages * kStage ? 0 : nxt + kStage;
+  };
+  constexpr std::integral_constant<int, kFmt> main_fmt;
+  constexpr std::integral_constant<int, kBf16> low_fmt;
+#pragma unroll 1
+  for (int q = 0; q < LR; ++q) {
+    const bool low = q + kStages < LR;
+    const Source from = low ? lowrank : operands;
+    step(low_fmt, from, low ? at_lowrank(q + kStages) : at_step(q + kStages - LR));
+  }
+  if constexpr (kFmt == kBf16) {
+    if (p.keep) {  // dropped elements of the term become 0
+      const int64_t mld = p.N / 32;
+      const __amdgpu_buffer_rsrc_t rk = make_rsrc(p.keep + m0 * mld, (p.M - m0) * mld * 4);
+#pragma unroll
+      for (int j = 0; j < BM; ++j)
+#pragma unroll
+        for (int i = 0; i < BN; ++i) {
+          const int word = (int)(n0 / 32) + wn * (WN / 32) + i;
+          const uint32_t bits = __builtin_amdgcn_raw_buffer_load_b32(
+              rk, (int)((wm * WM + j * 32 + r) * mld * 4), word * 4, 0) >> (half * 4);
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (!((bits >> ((v >> 2) * 8 + (v & 3))) & 1u)) acc[i][j][v] = 0.0f;
+        }
+    }
+  }
   for (int kb4 = 0; kb4 < KB; kb4 += 4) {
     const Scales ahead = scales(kb4 + 4);
     const int end = min(kb4 + 4, KB);
     for (int kb = kb4; kb < end; ++kb) {
-#pragma unroll
-      for (int i = 0; i < 2 * (BN + BM); ++i) read1(f1, cur, 1, i / 2, i % 2);
-      product(f0, s);
-      if constexpr (kM >= 4) {
-        pace<kM / 2, kP, 0, 2 * kR / kM>();
-        pace<kM / 2, kP, 0, 0>();
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      // Step kb + 1 has landed when at most the moves of the kStages - 2 steps
-      // after it are outstanding (they complete in order; a scale load among
-      // them only makes this wait longer).
-      wait_vmcnt<(kStages - 2) * kL>();
-      gemm::stage_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      // The moves of step kb + kStages into the stage that is now free, and
-      // the reads of the next step, in turn (their order is kept: both touch
-      // LDS).
-      const int nk = at_step(kb + kStages);
-#pragma unroll
-      for (int i = 0; i < kL; ++i) {
-        move(nk, lds0 + cur, i);
-        read1(f0, nxt, 0, i / 2, i % 2);
-      }
-      static_assert(kL == kR, "one move per piece");
-      product(f1, s);
-      if constexpr (kM >= 4) pace<kM, kP, kL / kM, kR / kM>();
-      __builtin_amdgcn_sched_barrier(0);
+      step(main_fmt, operands, at_step(kb + kStages));
       s.w >>= 8;
 #pragma unroll
       for (int j = 0; j < BM; ++j) s.x[j] >>= 8;
-      cur = nxt;
-      nxt = nxt + kStage == kStages * kStage ? 0 : nxt + kStage;
     }
     s = ahead;
   }
