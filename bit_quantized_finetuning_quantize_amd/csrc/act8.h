@@ -99,4 +99,61 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return v;
 }
 
+// Eight bf16 of a row at column c (zero past `cols`).
+template <bool kVec>
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t c, int64_t cols) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (c + 8 <= cols) {
+    if constexpr (kVec) return *reinterpret_cast<const u32x4*>(row + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = (uint32_t)row[c + 2 * i] | ((uint32_t)row[c + 2 * i + 1] << 16);
+    return v;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) v[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+  return v;
+}
+template <bool kVec>
+__device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t cols, u32x4 v) {
+  if (kVec && c + 8 <= cols) {
+    *reinterpret_cast<u32x4*>(row + c) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) row[c + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+}
+
+// Scale byte of block kb of a row; the row's last block also clears the
+// bytes up to the padded row end. Called by one lane of the block.
+__device__ __forceinline__ void put_scale(uint8_t* row, int kb, int KB, int sb, int byte) {
+  row[kb] = (uint8_t)byte;
+  if (kb == KB - 1)
+    for (int i = KB; i < sb; ++i) row[i] = 0;
+}
+
+// One block's codes from its lane's eight bf16 values.
+template <int kFmt>
+__device__ __forceinline__ void put_block(u32x4 x, uint32_t b, int kb, int KB, int sb, int64_t row,
+                                          uint8_t* codes, uint8_t* scales) {
+  const int l = threadIdx.x & 15;
+  const int byte = act8_scale_byte<kFmt>(row16_max(finite_max8(x)));
+  const u32x2 c = act8_encode8<kFmt>(x, act8_scale(byte));
+  *reinterpret_cast<u32x2*>(codes + (int64_t)b * kAct8Block + l * 8) = c;
+  if (l == 0) put_scale(scales + row * sb, kb, KB, sb, byte);
+}
+
+// Block b of the 8-bit blocks of X, in flat order b = row * KB + column block,
+// by the sixteen lanes that call with it.
+template <int kFmt, bool kVec>
+__device__ __forceinline__ void act8_quantize_block(const uint16_t* X, int64_t ldx, int64_t K, uint32_t b,
+                                                    int KB, int sb, uint8_t* codes, uint8_t* scales) {
+  const uint32_t row = b / (uint32_t)KB;
+  const int kb = (int)(b - row * (uint32_t)KB);
+  const int64_t c = (int64_t)kb * kAct8Block + (threadIdx.x & 15) * 8;
+  put_block<kFmt>(load8<kVec>(X + (int64_t)row * ldx, c, K), b, kb, KB, sb, row, codes, scales);
+}
+
 }  // namespace qlora

@@ -19,62 +19,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kGroups = kThreads / 16;  // blocks per workgroup
 
-// Eight bf16 of a row at column c (zero past `cols`).
-template <bool kVec>
-__device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t c, int64_t cols) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (c + 8 <= cols) {
-    if constexpr (kVec) return *reinterpret_cast<const u32x4*>(row + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = (uint32_t)row[c + 2 * i] | ((uint32_t)row[c + 2 * i + 1] << 16);
-    return v;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < cols) v[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
-  return v;
-}
-template <bool kVec>
-__device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t cols, u32x4 v) {
-  if (kVec && c + 8 <= cols) {
-    *reinterpret_cast<u32x4*>(row + c) = v;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < cols) row[c + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-}
-
-// Scale byte of block kb of a row; the row's last block also clears the
-// bytes up to the padded row end. Called by one lane of the block.
-__device__ __forceinline__ void put_scale(uint8_t* row, int kb, int KB, int sb, int byte) {
-  row[kb] = (uint8_t)byte;
-  if (kb == KB - 1)
-    for (int i = KB; i < sb; ++i) row[i] = 0;
-}
-
-// One block's codes from its lane's eight bf16 values.
-template <int kFmt>
-__device__ __forceinline__ void put_block(u32x4 x, uint32_t b, int kb, int KB, int sb, int64_t row,
-                                          uint8_t* codes, uint8_t* scales) {
-  const int l = threadIdx.x & 15;
-  const int byte = act8_scale_byte<kFmt>(row16_max(finite_max8(x)));
-  const u32x2 c = act8_encode8<kFmt>(x, act8_scale(byte));
-  *reinterpret_cast<u32x2*>(codes + (int64_t)b * kAct8Block + l * 8) = c;
-  if (l == 0) put_scale(scales + row * sb, kb, KB, sb, byte);
-}
-
 template <int kFmt, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 act8_quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t K, uint32_t blocks, int KB,
                      int sb, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const uint32_t b = blockIdx.x * kGroups + (threadIdx.x >> 4);
-  if (b >= blocks) return;
-  const uint32_t row = b / (uint32_t)KB;
-  const int kb = (int)(b - row * (uint32_t)KB);
-  const int64_t c = (int64_t)kb * kAct8Block + (threadIdx.x & 15) * 8;
-  put_block<kFmt>(load8<kVec>(X + (int64_t)row * ldx, c, K), b, kb, KB, sb, row, codes, scales);
+  if (b < blocks) act8_quantize_block<kFmt, kVec>(X, ldx, K, b, KB, sb, codes, scales);
 }
 
 template <int kFmt, bool kVec>
@@ -244,54 +194,6 @@ fp8_weight_quantize_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K,
   }
 }
 
-// ---------------------------------------------------------------------------
-// bf16(w') of a 4-bit store, transposed: one tile of 64 weight rows by 128
-// columns per workgroup. A thread decodes 16 codes of two neighbouring rows
-// (inside one block of 64 each) and writes them to LDS as pairs; the tile is
-// stored by its columns, 128 bytes each.
-constexpr int kTPitch = 136;  // bytes of an LDS row: 64 bf16 and 8 bytes of padding
-
-__global__ void __launch_bounds__(kThreads)
-nf4_dequantize_t_kernel(Nf4Weight W, int64_t N, int64_t K, Codebook cb, uint16_t* __restrict__ out) {
-#pragma clang fp contract(off)
-  __shared__ float s_lv[16];
-  __shared__ __attribute__((aligned(16))) uint8_t s_t[128 * kTPitch];
-  const int t = threadIdx.x;
-  if (t < 16) s_lv[t] = cb.lv[t];
-  const int64_t kt = (K + 127) / 128;
-  const int64_t n0 = blockIdx.x / kt * 64, k0 = blockIdx.x % kt * 128;
-  const int np = t >> 3, q = t & 7;
-  const int64_t k = k0 + q * 16;
-  const bool ok = k < K;  // K is a multiple of 64: a piece of 16 is inside or outside
-  u32x2 c[2];
-  float cs[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t e = (n0 + 2 * np + h) * K + (ok ? k : 0);
-    c[h] = *reinterpret_cast<const u32x2*>(W.codes + e / 2);
-    const int64_t b = e / kBlock;
-    cs[h] = !W.absmax_q ? W.absmax_s2[b]
-            : cb.dq_fp8 ? block_scale_fp8(W.absmax_q[b], W.absmax_s2[b / kGroup])
-                        : block_scale(W.absmax_q[b], W.absmax_s2[b / kGroup]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float lo = s_lv[(c[0][i >> 3] >> (4 * (i & 7))) & 15u] * cs[0];
-    const float hi = s_lv[(c[1][i >> 3] >> (4 * (i & 7))) & 15u] * cs[1];
-    *reinterpret_cast<uint32_t*>(s_t + (q * 16 + i) * kTPitch + np * 4) = pack_bf16x2(lo, hi);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int id = e * kThreads + t, row = id >> 3, ch = id & 7;
-    const u32x2 a = *reinterpret_cast<const u32x2*>(s_t + row * kTPitch + ch * 16);
-    const u32x2 b = *reinterpret_cast<const u32x2*>(s_t + row * kTPitch + ch * 16 + 8);
-    if (k0 + row < K)
-      *reinterpret_cast<u32x4*>(out + (k0 + row) * N + n0 + ch * 8) = u32x4{a[0], a[1], b[0], b[1]};
-  }
-}
-
 bool vec16(const void* p, int64_t ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0;
 }
@@ -356,14 +258,6 @@ hipError_t launch_swiglu_act8_bwd(const uint16_t* dh, int64_t lddh, ConstAct8 g8
   if (vec16(dh, lddh) && vec16(dg, lddg) && vec16(du, lddu))
     return fmt ? go(swiglu_act8_bwd_kernel<1, true>) : go(swiglu_act8_bwd_kernel<0, true>);
   return fmt ? go(swiglu_act8_bwd_kernel<1, false>) : go(swiglu_act8_bwd_kernel<0, false>);
-}
-
-hipError_t launch_nf4_dequantize_t(Nf4Weight W, int64_t N, int64_t K, uint16_t* out,
-                                   hipStream_t stream) {
-  const int64_t tiles = N / 64 * ((K + 127) / 128);
-  hipLaunchKernelGGL(nf4_dequantize_t_kernel, dim3((unsigned)tiles), dim3(kThreads), 0, stream, W, N,
-                     K, codebook_of(W), out);
-  return hipGetLastError();
 }
 
 hipError_t launch_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, Act8 w8, Act8 w8t,

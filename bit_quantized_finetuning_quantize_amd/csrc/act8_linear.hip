@@ -6,10 +6,10 @@
 //             T (float32), bf16(s T), B^T padded       one launch
 //             Y = dec(X8) dec(W8)^T + (s T) B          8-bit product
 //   backward  G = dY B^T, split along N                row product
-//             bf16(s G); float32 s G and s T          one launch
-//             dX                                       NF4: the weight to bf16,
-//                                                      then a bf16 product; 8-bit:
-//                                                      dY to 8 bits, its product
+//             bf16(s G); float32 s G and s T; beside   one launch
+//             them the weight to bf16 (NF4) or dY to
+//             8 bits (8-bit weight)
+//             dX                                       bf16 or 8-bit product
 //             dA and dB                                column products, one launch
 #include "act8.h"
 #include "kernels.h"
@@ -85,7 +85,7 @@ bool in_place(const uint16_t* A, int r) {
 // in v (unless it serves as it is), float32 s G and s T for dA and dB.
 hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, const uint16_t* A,
                      const uint16_t* B, int64_t M, int64_t N, int64_t K, int r, float scale,
-                     const Ptrs& w, const Dropout& dr, hipStream_t stream) {
+                     const Ptrs& w, const Dropout& dr, const LowrankBeside& beside, hipStream_t stream) {
   const float f = dr.mask ? dr.keep_scale : 1.0f;
   const int ldp = lowrank_cols(r);
   int splits = 0;
@@ -98,7 +98,7 @@ hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, c
   const LowrankOut o[2] = {{w.part, splits, ldp, f, nullptr, w.u, w.g},
                            {T, 1, r, 1.0f, nullptr, nullptr, w.t}};
   const LowrankPad pad = in_place(A, r) ? LowrankPad{} : LowrankPad{A, false, K, w.v};
-  return launch_lowrank_out(o, T ? 2 : 1, pad, M, r, scale, stream);
+  return launch_lowrank_out(o, T ? 2 : 1, pad, M, r, scale, stream, beside);
 }
 
 }  // namespace
@@ -113,9 +113,11 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
                            hipStream_t stream, Dropout dr) {
   const Ws8 l = ws8_layout(M, N, K, r);
   const Ptrs w = carve(ws, l);
-  QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, stream));
-  if (dX && dequantize_first(N, K)) {
-    QLORA_TRY(launch_nf4_dequantize_t(W, N, K, w.wt, stream));
+  const bool decode = dX && dequantize_first(N, K);
+  LowrankBeside beside;
+  if (decode) beside.W = W, beside.N = N, beside.K = K, beside.w = w.wt;
+  QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, beside, stream));
+  if (decode) {
     QLORA_TRY(launch_bf16_gemm(dY, w.wt, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dr.mask, dX,
                                stream));
   } else if (dX)
@@ -147,9 +149,14 @@ hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, c
                           void* ws, hipStream_t stream) {
   const Ws8 l = ws8_layout(M, N, K, r);
   const Ptrs w = carve(ws, l);
-  if (r) QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, Dropout{}, stream));
-  if (dX) {
+  if (r) {
+    LowrankBeside beside;
+    if (dX) beside.s = dY, beside.C = N, beside.fmt = dyfmt, beside.codes = w.dy8, beside.scales = w.dys;
+    QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, Dropout{}, beside, stream));
+  } else {
     QLORA_TRY(launch_act8_quantize(dY, M, N, N, dyfmt, w.dy8, w.dys, stream));
+  }
+  if (dX) {
     QLORA_TRY(launch_fp8_gemm(ConstAct8{w.dy8, w.dys}, dyfmt, w8t, M, K, N, r ? w.u : nullptr,
                               r ? (in_place(A, r) ? A : w.v) : nullptr, (int)l.r64, dX, stream));
   }

@@ -143,8 +143,10 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   };
   auto source = [&](const uint8_t* w, const uint8_t* x, int64_t ld) {
     Source s;
-    s.w = make_rsrc(w + n0 * ld, (p.N - n0) * ld);
-    s.x = make_rsrc(x + m0 * ld, (p.M - m0) * ld);
+    // the tile's rows alone (2 GiB at most), so that a step past the end of
+    // K is out of range however large the matrices are
+    s.w = make_rsrc(w + n0 * ld, min(p.N - n0, (int64_t)TN) * ld);
+    s.x = make_rsrc(x + m0 * ld, min(p.M - m0, (int64_t)TM) * ld);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       s.vw[i] = (int)((row0 + i * 8) * ld) + (((lane & 7) ^ gemm::swz(row0 + i * 8)) << 4);
@@ -443,8 +445,8 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
   const int i = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * kN, m0 = (int64_t)blockIdx.y * kM;
 
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + n0 * p.ldc, (p.N - n0) * p.ldc);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + m0 * p.ldc, (p.M - m0) * p.ldc);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + n0 * p.ldc, min(p.N - n0, (int64_t)kN) * p.ldc);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + m0 * p.ldc, min(p.M - m0, (int64_t)kM) * p.ldc);
   const __amdgpu_buffer_rsrc_t rsw = make_rsrc(p.ws + n0 / 128 * p.sb, p.sb);  // the tile is in one block row
   const __amdgpu_buffer_rsrc_t rsx = make_rsrc(p.xs + m0 * p.sb, (p.M - m0) * p.sb);
   floatx4 acc[RN];

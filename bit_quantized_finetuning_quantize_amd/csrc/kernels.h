@@ -140,8 +140,6 @@ hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_
 hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
                             const uint16_t* U, const uint16_t* V, int r64, const uint32_t* keep,
                             uint16_t* Y, hipStream_t stream);
-// out [K x N] = bf16(w')^T of a store of W [N x K], N and K multiples of 64.
-hipError_t launch_nf4_dequantize_t(Nf4Weight W, int64_t N, int64_t K, uint16_t* out, hipStream_t stream);
 
 // The same product where its output is small (fp8_few), the adapter's term
 // from split partials of T (launch_rows_act8; null without an adapter);
@@ -181,8 +179,20 @@ struct LowrankPad {
   int64_t rows = 0;
   uint16_t* dst = nullptr;
 };
+// Beside them in the same launch, none or one of:
+//   codes, scales  8-bit blocks in fmt of bf16 s [M x C], 16-byte aligned, C a multiple of 8
+//   w [K x N]      bf16(w')^T of a store of W [N x K], N and K multiples of 64
+struct LowrankBeside {
+  const uint16_t* s = nullptr;
+  int64_t C = 0;
+  int fmt = 0;
+  uint8_t *codes = nullptr, *scales = nullptr;
+  Nf4Weight W{};
+  int64_t N = 0, K = 0;
+  uint16_t* w = nullptr;
+};
 hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_t M, int r, float s,
-                              hipStream_t stream);
+                              hipStream_t stream, const LowrankBeside& beside = LowrankBeside{});
 // dA = D(dec x)^T g, dB = t^T dY, g and t as launch_lowrank_out's vf.
 hipError_t launch_columns(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY,
                           const float* g, const float* t, int64_t M, int64_t N, int64_t K,

@@ -160,8 +160,9 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
 #pragma unroll
   for (int f = 0; f < NF; ++f) acc[f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // One step's loads: S (codes, scales and keep bits, or values) and W. The
-  // next step's are issued before the present one is worked on.
+  // One step's loads, all on their way before the first is waited for: S
+  // (codes, scales and keep bits, or values) and W. The other waves cover the
+  // wait; the next step's loads a step early took more registers and time.
   struct Regs {
     u32x4 s[4][kSrc == kBf16 ? 2 : 1];
     uint32_t sc[4], keep[4];
@@ -211,10 +212,8 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
   };
   const int end = min(p.steps, (split + 1) * p.per);
   const int begin = split * p.per + wave;
-  Regs now = load(begin);
   for (int st = begin; st < end; st += kWaves) {
-    const Regs q = now;
-    if (st + kWaves < end) now = load(st + kWaves);
+    const Regs q = load(st);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kTrans) {  // A's rows to LDS, back by columns
       if (p.wvec) {
@@ -255,6 +254,7 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
                                                                      acc[f * NJ + jt], 0, 0, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
   reduce_waves<NJ>(acc, lds, wave, lane);
 #pragma unroll
@@ -296,13 +296,13 @@ constexpr int kOutThreads = 256;
 constexpr int kOutRows = 16;  // rows of M per workgroup
 
 __device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, int64_t M, int64_t Mp,
-                                         int r, int64_t r64, int64_t rp, float s, float (&tile)[64][65]) {
+                                         int r, int64_t r64, int64_t rp, float s, float (*tile)[65]) {
   const int t = threadIdx.x;
   float v[4];
   const int jl = t & 63, j = jc * 64 + jl;
   const int64_t m0 = mt * kOutRows + (t >> 6);
-  // loads inside the product's rows and columns, so that none is conditional
-  // and all of a few splits are in flight together
+  // loads inside the product's rows and columns, so that none is conditional;
+  // more splits at a time would take registers from the work beside
   const float* at[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -310,7 +310,7 @@ __device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, i
     at[q] = jb.part + min(m0 + 4 * q, M - 1) * jb.ldp + min(j, r - 1);
   }
   const int64_t stride = M * jb.ldp;
-#pragma unroll 8
+#pragma unroll 2
   for (int sp = 0; sp < jb.splits; ++sp)
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] += at[q][sp * stride];
@@ -338,7 +338,7 @@ __device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, i
 }
 
 __device__ __forceinline__ void pad_tile(const PadJob& jb, int64_t rt, int jc, int r, int64_t r64,
-                                         float (&tile)[64][65]) {
+                                         float (*tile)[65]) {
   const int t = threadIdx.x;
   uint32_t v[16];
   if (!jb.columns) {
@@ -373,6 +373,57 @@ __device__ __forceinline__ void pad_tile(const PadJob& jb, int64_t rt, int jc, i
   }
 }
 
+// ---------------------------------------------------------------------------
+// bf16(w') of a 4-bit store, transposed: one tile of 64 weight rows by 128
+// columns per workgroup. A thread decodes 16 codes of two neighbouring rows
+// (inside one block of 64 each) and writes them to LDS as pairs; the tile is
+// stored by its columns, 128 bytes each.
+constexpr int kTPitch = 136;  // bytes of an LDS row: 64 bf16 and 8 bytes of padding
+
+constexpr int kDecodeLds = 64 + 128 * kTPitch;
+
+__device__ __forceinline__ void nf4_decode_t(const Nf4Weight& W, int64_t N, int64_t K, const Codebook& cb,
+                                             uint16_t* __restrict__ out, unsigned tile, uint8_t* lds) {
+#pragma clang fp contract(off)
+  float* s_lv = reinterpret_cast<float*>(lds);
+  uint8_t* s_t = lds + 64;
+  const int t = threadIdx.x;
+  if (t < 16) s_lv[t] = cb.lv[t];
+  const int64_t kt = (K + 127) / 128;
+  const int64_t n0 = tile / kt * 64, k0 = tile % kt * 128;
+  const int np = t >> 3, q = t & 7;
+  const int64_t k = k0 + q * 16;
+  const bool ok = k < K;  // K is a multiple of 64: a piece of 16 is inside or outside
+  u32x2 c[2];
+  float cs[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t e = (n0 + 2 * np + h) * K + (ok ? k : 0);
+    c[h] = *reinterpret_cast<const u32x2*>(W.codes + e / 2);
+    const int64_t b = e / kBlock;
+    cs[h] = !W.absmax_q ? W.absmax_s2[b]
+            : cb.dq_fp8 ? block_scale_fp8(W.absmax_q[b], W.absmax_s2[b / kGroup])
+                        : block_scale(W.absmax_q[b], W.absmax_s2[b / kGroup]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float lo = s_lv[(c[0][i >> 3] >> (4 * (i & 7))) & 15u] * cs[0];
+    const float hi = s_lv[(c[1][i >> 3] >> (4 * (i & 7))) & 15u] * cs[1];
+    *reinterpret_cast<uint32_t*>(s_t + (q * 16 + i) * kTPitch + np * 4) = pack_bf16x2(lo, hi);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int id = e * kOutThreads + t, row = id >> 3, ch = id & 7;
+    const u32x2 a = *reinterpret_cast<const u32x2*>(s_t + row * kTPitch + ch * 16);
+    const u32x2 b = *reinterpret_cast<const u32x2*>(s_t + row * kTPitch + ch * 16 + 8);
+    if (k0 + row < K)
+      *reinterpret_cast<u32x4*>(out + (k0 + row) * N + n0 + ch * 8) = u32x4{a[0], a[1], b[0], b[1]};
+  }
+}
+
+// ---------------------------------------------------------------------------
 struct OutArgs {
   OutJob o[2];
   PadJob pad;
@@ -380,18 +431,44 @@ struct OutArgs {
   int r;
   int64_t r64, rp;
   float s;
-  int blocks0, blocks1;  // workgroups of the two out jobs
+  int cols;                      // column tiles of the jobs
+  int blocks0, blocks1, blocks;  // workgroups of the first out job, of both, of all jobs
 };
+// What the same launch does beside the jobs: an 8-bit copy of S, or a weight
+// to bf16 (decode_t). Both are what the launch after this one reads.
+struct BesideArgs {
+  const uint16_t* s;
+  int64_t C;
+  uint32_t blocks;
+  int KB, sb;
+  uint8_t *codes, *scales;
+  Nf4Weight W;
+  int64_t N, K;
+  Codebook cb;
+  uint16_t* w;
+};
+enum Beside { kNothing = 0, kQuantizeE4M3 = 1, kQuantizeE5M2 = 2, kDecode = 3 };
 
-__global__ void __launch_bounds__(kOutThreads) lowrank_out_kernel(OutArgs p) {
-  __shared__ float tile[64][65];
-  int b = blockIdx.x;
-  const int jc = blockIdx.y;
-  if (b < p.blocks0) return out_tile(p.o[0], b, jc, p.M, p.Mp, p.r, p.r64, p.rp, p.s, tile);
-  b -= p.blocks0;
-  if (b < p.blocks1) return out_tile(p.o[1], b, jc, p.M, p.Mp, p.r, p.r64, p.rp, p.s, tile);
-  b -= p.blocks1;
-  pad_tile(p.pad, b, jc, p.r, p.r64, tile);
+template <int kBeside>
+__global__ void __launch_bounds__(kOutThreads) lowrank_out_kernel(OutArgs p, BesideArgs q) {
+  constexpr int kTile = 64 * 65 * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kBeside == kDecode && kDecodeLds > kTile ? kDecodeLds : kTile];
+  auto tile = reinterpret_cast<float(*)[65]>(smem);
+  const int id = blockIdx.x;
+  if (id < p.blocks) {
+    const int b = id / p.cols, jc = id % p.cols;
+    if (b < p.blocks0) out_tile(p.o[0], b, jc, p.M, p.Mp, p.r, p.r64, p.rp, p.s, tile);
+    else if (b < p.blocks1) out_tile(p.o[1], b - p.blocks0, jc, p.M, p.Mp, p.r, p.r64, p.rp, p.s, tile);
+    else pad_tile(p.pad, b - p.blocks1, jc, p.r, p.r64, tile);
+    return;
+  }
+  if constexpr (kBeside == kDecode) {
+    nf4_decode_t(q.W, q.N, q.K, q.cb, q.w, id - p.blocks, smem);
+  } else if constexpr (kBeside != kNothing) {
+    const uint32_t b = (uint32_t)(id - p.blocks) * (kOutThreads / 16) + (threadIdx.x >> 4);
+    if (b < q.blocks)
+      act8_quantize_block<kBeside == kQuantizeE5M2, true>(q.s, q.C, q.C, b, q.KB, q.sb, q.codes, q.scales);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -453,8 +530,7 @@ __device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0,
     floatx4 v[NJ][2];
   };
   const int steps = (int)((p.s.rows + 31) / 32);
-  // One step's loads: 32 rows of S by 64 columns, and V's fragments. The next
-  // step's are issued before the present one is worked on.
+  // One step's loads: 32 rows of S by 64 columns, and V's fragments.
   auto load = [&](int st) {
     Regs q;
     if constexpr (kSrc == kBf16) {
@@ -473,17 +549,15 @@ __device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0,
           q.keep[e] = __builtin_amdgcn_raw_buffer_load_b32(rm, (int)(m * mld * 4) + (ch >> 1) * 4, 0, 0);
       }
     }
-    const float* v = vb + min(st, steps - 1) * vblock;  // a wave without a step loads one it does not use
+    const float* v = vb + st * vblock;
 #pragma unroll
     for (int jt = 0; jt < NJ; ++jt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) q.v[jt][h] = *reinterpret_cast<const floatx4*>(v + jt * 512 + h * 4);
     return q;
   };
-  Regs now = load(wave);
   for (int st = wave; st < steps; st += kWaves) {
-    const Regs q = now;
-    if (st + kWaves < steps) now = load(st + kWaves);
+    const Regs q = load(st);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kSrc == kBf16) {
 #pragma unroll
@@ -519,6 +593,7 @@ __device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0,
           acc[f * NJ + jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[f], as_bf16x8(term[c]),
                                                                      acc[f * NJ + jt], 0, 0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
   reduce_waves<NJ>(acc, lds, wave, lane);
   // dA's rows run along j, dB's along the columns of S
@@ -615,7 +690,7 @@ hipError_t launch_rows_bf16(const uint16_t* S, int64_t M, int64_t C, const uint1
 }
 
 hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_t M, int r, float s,
-                              hipStream_t stream) {
+                              hipStream_t stream, const LowrankBeside& beside) {
   OutArgs p{};
   p.M = M;
   p.Mp = ceil_div(M, 64) * 64;
@@ -626,12 +701,35 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
   for (int i = 0; i < n; ++i)
     p.o[i] = OutJob{o[i].part, o[i].splits, o[i].ldp, o[i].f, o[i].out32, o[i].u, o[i].vf};
   p.pad = PadJob{pad.src, pad.columns, pad.rows, pad.dst};
+  p.cols = (int)(p.r64 / 64);
   p.blocks0 = (int)(p.Mp / kOutRows);
-  p.blocks1 = n > 1 ? p.blocks0 : 0;
-  const int64_t blocks = p.blocks0 + p.blocks1 + (pad.src ? ceil_div(pad.rows, 64) : 0);
-  hipLaunchKernelGGL(lowrank_out_kernel, dim3((unsigned)blocks, (unsigned)(p.r64 / 64)),
-                     dim3(kOutThreads), 0, stream, p);
-  return hipGetLastError();
+  p.blocks1 = n * p.blocks0;
+  p.blocks = p.cols * (p.blocks1 + (pad.src ? (int)ceil_div(pad.rows, 64) : 0));
+  BesideArgs q{};
+  int64_t more = 0;
+  if (beside.codes) {
+    q.s = beside.s;
+    q.C = beside.C;
+    q.KB = (int)ceil_div(beside.C, kAct8Block);
+    q.sb = (int)act8_scale_row_bytes(beside.C);
+    q.blocks = (uint32_t)(M * q.KB);
+    q.codes = beside.codes;
+    q.scales = beside.scales;
+    more = ceil_div(q.blocks, kOutThreads / 16);
+  } else if (beside.w) {
+    q.W = beside.W;
+    q.N = beside.N;
+    q.K = beside.K;
+    q.cb = codebook_of(beside.W);
+    q.w = beside.w;
+    more = beside.N / 64 * ceil_div(beside.K, 128);
+  }
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)(p.blocks + more)), dim3(kOutThreads), 0, stream, p, q);
+    return hipGetLastError();
+  };
+  if (beside.codes) return beside.fmt ? go(lowrank_out_kernel<kQuantizeE5M2>) : go(lowrank_out_kernel<kQuantizeE4M3>);
+  return beside.w ? go(lowrank_out_kernel<kDecode>) : go(lowrank_out_kernel<kNothing>);
 }
 
 hipError_t launch_columns(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY,
