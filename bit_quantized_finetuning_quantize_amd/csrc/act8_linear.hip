@@ -26,13 +26,11 @@ namespace {
     if (e_ != hipSuccess) return e_;       \
   } while (0)
 
-// dX of the NF4 layer: the weight decoded to bf16 once, transposed, and a bf16
-// product on it, or the contraction that decodes tiles on their way in (whole
-// backward, r = 64: 47 us against 80 at 64 x 4096 x 4096, 218 against 228 at
-// 2048 x 11008 x 4096, 506 against 616 at 4096 x 8192 x 8192). Below 2^18
-// weights the one launch less counts (16 x 256 x 256: 27 us against 33).
-bool dequantize_first(int64_t N, int64_t K) { return N * K >= (int64_t)1 << 18; }
-
+// dX of the NF4 layer: the weight decoded to bf16 once, transposed, beside the
+// adapter's factors, and a bf16 product on it. The contraction that decodes
+// tiles on their way in decodes each of them once per row tile (whole backward,
+// r = 64: 80 us against 47 at 64 x 4096 x 4096, 616 against 506 at
+// 4096 x 8192 x 8192; dX alone 9.1 us against 3.6 at 16 x 256 x 256).
 struct Ws8 {
   int64_t r64;
   size_t v, u, g, t, part, dy8, dys, wt, total;
@@ -57,7 +55,7 @@ Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
   w.dys = take(M * act8_scale_row_bytes(N));
   // the NF4 backward's decoded weight, in the place of the 8-bit dY
   w.wt = w.dy8;
-  if (r && dequantize_first(N, K)) off = std::max(off, w.wt + (size_t)(N * K * 2));
+  if (r) off = std::max(off, w.wt + (size_t)(N * K * 2));
   w.total = off;
   return w;
 }
@@ -113,15 +111,12 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
                            hipStream_t stream, Dropout dr) {
   const Ws8 l = ws8_layout(M, N, K, r);
   const Ptrs w = carve(ws, l);
-  const bool decode = dX && dequantize_first(N, K);
   LowrankBeside beside;
-  if (decode) beside.W = W, beside.N = N, beside.K = K, beside.w = w.wt;
+  if (dX) beside.W = W, beside.N = N, beside.K = K, beside.w = w.wt;
   QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, beside, stream));
-  if (decode) {
+  if (dX)
     QLORA_TRY(launch_bf16_gemm(dY, w.wt, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dr.mask, dX,
                                stream));
-  } else if (dX)
-    QLORA_TRY(launch_input_grad(dY, W, w.u, in_place(A, r) ? A : w.v, M, N, K, l.r64, dX, stream, dr));
   return launch_columns(x, fmt, dr.mask, dY, w.g, w.t, M, N, K, r, dA, dB, stream);
 }
 

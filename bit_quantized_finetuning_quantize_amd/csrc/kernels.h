@@ -98,12 +98,6 @@ hipError_t launch_bwd(const uint16_t* dY, const uint16_t* X, const float* T,
                       hipStream_t stream, hipEvent_t ev0 = nullptr,
                       hipEvent_t ev1 = nullptr, Dropout dr = Dropout{});
 
-// dX = dY W' + sg apad^T with sg = bf16(s G) [M x r64] (zero past r) and
-// apad = A padded to [K x r64]; under dropout the second term passes the mask.
-hipError_t launch_input_grad(const uint16_t* dY, Nf4Weight W, const uint16_t* sg,
-                             const uint16_t* apad, int64_t M, int64_t N, int64_t K, int64_t r64,
-                             uint16_t* dX, hipStream_t stream, Dropout dr = Dropout{});
-
 // ---- 8-bit blocks -------------------------------------------------------------
 
 struct Act8 {

@@ -449,8 +449,9 @@ namespace {
 // tiles are dequantized and transposed into LDS, the LoRA columns
 // (s G | A^T) form the second segment.
 template <class Epi>
-hipError_t input_grad(const uint16_t* dY, Nf4Weight W, const uint16_t* sg, const uint16_t* apad,
-                      int64_t M, int64_t N, int64_t K, int64_t r64, Epi epi, hipStream_t stream) {
+hipError_t input_grad(const uint16_t* dY, Nf4Weight W, const uint16_t* apad, int64_t M,
+                      int64_t N, int64_t K, const WsLayout& w, char* ws, Epi epi,
+                      hipStream_t stream) {
   using LA1 = DirectRows<256>;
   using LB1 = Nf4Cols<128>;
   using LA2 = DirectRows<256>;
@@ -458,12 +459,12 @@ hipError_t input_grad(const uint16_t* dY, Nf4Weight W, const uint16_t* sg, const
   Contraction<256, 128, LA1, LB1, LA2, LB2, Epi> cfg{};
   cfg.a1 = LA1{dY, N, M};
   cfg.b1 = LB1{W.codes, W.absmax_q, W.absmax_s2, N, K, nf4_consts(W)};
-  cfg.a2 = LA2{sg, r64, M};
-  cfg.b2 = LB2{apad, r64, K};
+  cfg.a2 = LA2{reinterpret_cast<const uint16_t*>(ws + w.sg), w.r64, M};
+  cfg.b2 = LB2{apad, w.r64, K};
   cfg.nP = (int)ceil_div(M, 256);
   cfg.nQ = (int)ceil_div(K, 128);
   cfg.S1 = (int)ceil_div(N, 64);
-  cfg.S2 = (int)(r64 / 64);
+  cfg.S2 = (int)(w.r64 / 64);
   cfg.splits = 1;
   cfg.steps_per_split = cfg.S1 + cfg.S2;
   cfg.epi = epi;
@@ -510,15 +511,6 @@ hipError_t adapter_grads(LA xa, LA ya, int64_t M, int64_t N, int64_t K, int r, c
 
 }  // namespace
 
-hipError_t launch_input_grad(const uint16_t* dY, Nf4Weight W, const uint16_t* sg,
-                             const uint16_t* apad, int64_t M, int64_t N, int64_t K, int64_t r64,
-                             uint16_t* dX, hipStream_t stream, Dropout dr) {
-  if (dr.mask)
-    return input_grad(dY, W, sg, apad, M, N, K, r64, EpiBf16Keep{dX, K, M, K, dr.mask, K / 32},
-                      stream);
-  return input_grad(dY, W, sg, apad, M, N, K, r64, EpiBf16{dX, K, M, K}, stream);
-}
-
 hipError_t launch_bwd(const uint16_t* dY, const uint16_t* X, const float* T, Nf4Weight W,
                       const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K,
                       int r, float scale, uint16_t* dX, float* dA, float* dB, void* ws_,
@@ -554,8 +546,11 @@ hipError_t launch_bwd(const uint16_t* dY, const uint16_t* X, const float* T, Nf4
   // 3. dX = dY W' + (s G) A^T   (+ keep o ((s f G) A^T) under dropout)
   if (dX) {
     QLORA_TRY(record_if(ev0, stream));
-    QLORA_TRY(launch_input_grad(dY, W, reinterpret_cast<const uint16_t*>(ws + w.sg), apad, M, N, K,
-                                w.r64, dX, stream, dr));
+    if (dr.mask)
+      QLORA_TRY(input_grad(dY, W, apad, M, N, K, w, ws, EpiBf16Keep{dX, K, M, K, dr.mask, K / 32},
+                           stream));
+    else
+      QLORA_TRY(input_grad(dY, W, apad, M, N, K, w, ws, EpiBf16{dX, K, M, K}, stream));
     QLORA_TRY(record_if(ev1, stream));
   }
   // 4. dA = X^T (s G) (P = K) and dB^T = dY^T (s T) (P = N): Q = r64,

@@ -554,9 +554,9 @@ int qlora_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, uint8_t* 
 
 /* Workspace of the three linear calls below: at least
  *   qlora_act8_workspace_bytes(M, N, K, r)
- * bytes of device memory, 256-byte aligned, as for the NF4 linear calls (from
- * 2^18 weights on it holds a bf16 copy of one weight, 2 N K bytes, which
- * qlora_linear_bwd_act8 decodes into it in every call).
+ * bytes of device memory, 256-byte aligned, as for the NF4 linear calls. For
+ * r > 0 it has room for a bf16 copy of the weight, 2 N K bytes, which
+ * qlora_linear_bwd_act8 decodes into it in every call.
  * r = 0 is the workspace of a call without an adapter. 0 for a shape the
  * calls reject: those of the NF4 linear calls (for r = 0 N and K need not be
  * multiples of 64 and the limits hold for them rounded up to 128). */
