@@ -445,23 +445,23 @@ def _rows(t, shape, name):
     return ld
 
 
-def _bytes(t, shape, name):
+def _bytes(t, shape, name, part):
     if (t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous()
             or not t.is_cuda):
-        raise QloraError(f"{name} must be a contiguous uint8 tensor of shape {shape} on the GPU")
+        raise QloraError(f"{name}{part} must be a contiguous uint8 tensor of shape {shape} on the GPU")
 
 
 def _need_act8(a, name):
     M, K = a.shape
-    _bytes(a.codes, (M, act8_row_bytes(K)), f"{name}.codes")
-    _bytes(a.scales, (M, act8_scale_row_bytes(K)), f"{name}.scales")
+    _bytes(a.codes, (M, act8_row_bytes(K)), name, ".codes")
+    _bytes(a.scales, (M, act8_scale_row_bytes(K)), name, ".scales")
 
 
 def _need_weight(codes, scales, N, K, name):
     if codes is None or scales is None:
         raise QloraError(f"{name}: the weight does not hold this order")
-    _bytes(codes, (N, act8_row_bytes(K)), f"{name} codes")
-    _bytes(scales, ((N + 127) // 128, act8_scale_row_bytes(K)), f"{name} scales")
+    _bytes(codes, (N, act8_row_bytes(K)), name, " codes")
+    _bytes(scales, ((N + 127) // 128, act8_scale_row_bytes(K)), name, " scales")
 
 
 def qlora_act8_quantize(X, fmt=ACT8_E4M3, out=None):
@@ -554,6 +554,13 @@ def act8_workspace(M, N, K, r, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _act8_ws(ws, M, N, K, r, device):
+    if ws is None:
+        return act8_workspace(M, N, K, r, device)
+    _need(ws, torch.uint8, "ws")
+    return ws
+
+
 def _adapter(A, B, N, K):
     """Rank of an adapter, checked; 0 without one."""
     if A is None and B is None:
@@ -603,7 +610,7 @@ def qlora_linear_bwd_act8(dY, X8, T, W, A, B, scale, want_dX=True, keep_mask=Non
     dX = _out(dX, (M, K), torch.bfloat16, dev, "dX") if want_dX else None
     dA = _out(dA, (K, r), torch.float32, dev, "dA")
     dB = _out(dB, (r, N), torch.float32, dev, "dB")
-    ws = ws if ws is not None else act8_workspace(M, N, K, r, dev)
+    ws = _act8_ws(ws, M, N, K, r, dev)
     _check(LIB.qlora_linear_bwd_act8(_ptr(dY), _ptr(X8.codes), _ptr(X8.scales), X8.fmt, _ptr(T),
                                      _ptr(W.codes), _ptr(W.absmax_q), _ptr(W.absmax_s2), _ptr(A),
                                      _ptr(B), M, N, K, r, float(scale), _ptr(keep_mask), float(p),
@@ -645,7 +652,7 @@ def qlora_fp8_linear_fwd(X8, W, A=None, B=None, scale=1.0, want_T=True, Y=None, 
     dev = X8.codes.device
     Y = _out(Y, (M, N), torch.bfloat16, dev, "Y")
     T = _out(T, (M, r), torch.float32, dev, "T") if want_T and r else None
-    ws = ws if ws is not None else act8_workspace(M, N, K, r, dev)
+    ws = _act8_ws(ws, M, N, K, r, dev)
     _check(LIB.qlora_fp8_linear_fwd(_ptr(X8.codes), _ptr(X8.scales), X8.fmt, _ptr(W.codes),
                                     _ptr(W.scales), _ptr(A), _ptr(B), M, N, K, r, float(scale),
                                     _ptr(Y), _ptr(T), _ptr(ws), ws.numel(), _stream()))
@@ -679,7 +686,7 @@ def qlora_fp8_linear_bwd(dY, X8, T, W, A=None, B=None, scale=1.0, fmt=ACT8_E4M3,
     else:
         dX = None
     x = (_ptr(X8.codes), _ptr(X8.scales), X8.fmt) if r else (None, None, ACT8_E4M3)
-    ws = ws if ws is not None else act8_workspace(M, N, K, r, dev)
+    ws = _act8_ws(ws, M, N, K, r, dev)
     _check(LIB.qlora_fp8_linear_bwd(_ptr(dY), int(fmt), *x, _ptr(T), _ptr(W.codes_t),
                                     _ptr(W.scales_t), _ptr(A), _ptr(B), M, N, K, r, float(scale),
                                     _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream()))

@@ -99,6 +99,23 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return v;
 }
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// The eight transposed elements of a fragment from a row-major tile of bf16 in
+// LDS, rows kPitch bytes apart: lane l
+// receives column (l & 15) + c0 and rows r0 .. r0 + 7 of its own 16-lane
+// group's row base.
+template <int kPitch>
+__device__ __forceinline__ bf16x8 tr_frag(uint32_t tile, int row0, int c0, int lane) {
+  const int p = lane & 15;
+  const uint32_t a = tile + (uint32_t)((row0 + (p >> 2)) * kPitch + (c0 + (p & 3) * 4) * 2);
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(a + 4 * kPitch));
+  const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
+  return as_bf16x8(u32x4{l2[0], l2[1], h2[0], h2[1]});
+}
+
 // Eight bf16 of a row at column c (zero past `cols`).
 template <bool kVec>
 __device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t c, int64_t cols) {

@@ -5,6 +5,8 @@
 //   forward   T = dec(X8) A, split along K             row product
 //             T (float32), bf16(s T), B^T padded       one launch
 //             Y = dec(X8) dec(W8)^T + (s T) B          8-bit product
+//             (few tokens: T, or its partials summed,  8-bit product
+//             and s T in float32 there)
 //   backward  G = dY B^T, split along N                row product
 //             bf16(s G); float32 s G and s T; beside   one launch
 //             them the weight to bf16 (NF4) or dY to
@@ -127,12 +129,14 @@ hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A,
   const Ptrs w = carve(ws, l);
   const bool few = fp8_few(M, N);
   if (!r)
-    return few ? launch_fp8_few(x, fmt, w8, M, N, K, nullptr, 0, nullptr, 0, scale, Y, nullptr, stream)
+    return few ? launch_fp8_few(x, fmt, w8, M, N, K, nullptr, nullptr, 0, nullptr, 0, scale, Y, nullptr, stream)
                : launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, stream);
+  if (few && fp8_few_forms_t(A, M, K, r))
+    return launch_fp8_few(x, fmt, w8, M, N, K, A, nullptr, 0, B, r, scale, Y, T_out, stream);
   int splits = 0;
   QLORA_TRY(launch_rows_act8(x, fmt, M, K, nullptr, A, r, w.part, &splits, stream));
   if (few)
-    return launch_fp8_few(x, fmt, w8, M, N, K, w.part, splits, B, r, scale, Y, T_out, stream);
+    return launch_fp8_few(x, fmt, w8, M, N, K, nullptr, w.part, splits, B, r, scale, Y, T_out, stream);
   const LowrankOut t{w.part, splits, lowrank_cols(r), 1.0f, T_out, w.u, nullptr};
   QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{B, true, N, w.v}, M, r, scale, stream));
   return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, stream);

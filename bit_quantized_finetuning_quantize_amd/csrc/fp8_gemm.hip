@@ -425,21 +425,27 @@ fp8_gemm_small_kernel(Fp8Gemm p) {
 struct Fp8Few {
   Fp8Gemm g;
   const float* part;   // [splits][M][ldp] partials of T, or null
+  const uint16_t* A;   // kR: [K x kR], 16-byte aligned
+  int64_t K;
   int splits, ldp, r;
   float scale;
   const uint16_t* B;   // [r x N]
   float* T_out;        // [M x r] or null
 };
 
-constexpr int kFewWaves = 8;
-
-template <int RN, int kXFmt>
+// kR = 8 or 16: an adapter of that rank, T formed here by every workgroup, from
+// A read beside the weight (A's rows pass through a wave's own LDS tile and
+// come back by columns).
+template <int RN, int kXFmt, int kR>
 __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
 #ifdef __HIP_DEVICE_COMPILE__
   const Fp8Gemm& p = q.g;
   constexpr int kM = 16, kN = 16 * RN, kJ = 64;
   __shared__ floatx4 s_acc[kFewWaves][RN][64];
   __shared__ float s_t[kM][kJ + 1];
+  constexpr int kPitch = 40;  // bytes of a row of the wave's tile of A
+  __shared__ __attribute__((aligned(16))) uint8_t s_a[kR ? kFewWaves * 128 * kPitch : 16];
+  __shared__ floatx4 s_tacc[kR ? kFewWaves : 1][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -453,16 +459,27 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
 #pragma unroll
   for (int a = 0; a < RN; ++a) acc[a] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  constexpr int kA = kR / 4;  // 16-byte pieces per lane of 128 rows of A
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(q.A, q.K * kR * 2);
+  const uint32_t at = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)s_a) +
+                      (uint32_t)(wave * 128 * kPitch);
+  // a sum for every eighth step of 64, in the order of row_product_kernel's
+  // waves: T has the bits that a backward pass recomputes
+  floatx4 tacc[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) tacc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
   const int per = (p.KB + kFewWaves - 1) / kFewWaves;
   const int begin = wave * per, end = min(p.KB, begin + per);
   constexpr int kU = 4;
   for (int kb = begin; kb < end; kb += kU) {
-    u32x4 w[kU][RN][2], x[kU][2];
+    u32x4 w[kU][RN][2], x[kU][2], av[kU][kA ? kA : 1];
     uint32_t sw[kU], sx[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       // past the wave's run every offset is out of range: zeros
-      const int off = kb + u < end ? (kb + u) * 128 : 0x7f000000;
+      const bool in = kb + u < end;
+      const int off = in ? (kb + u) * 128 : 0x7f000000;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -474,6 +491,10 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
       }
       sw[u] = __builtin_amdgcn_raw_buffer_load_b8(rsw, 0, kb + u, 0);
       sx[u] = __builtin_amdgcn_raw_buffer_load_b8(rsx, i * p.sb, kb + u, 0);
+#pragma unroll
+      for (int e = 0; e < kA; ++e)
+        av[u][e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+            ra, (e * 64 + lane) * 16, in ? (kb + u) * (128 * kR * 2) : 0x7f000000, 0));
     }
     // every load is on its way before the first product waits
     __builtin_amdgcn_sched_barrier(0);
@@ -487,6 +508,36 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
       for (int a = 0; a < RN; ++a)
         acc[a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
             whole(w[u][a]), whole(x[u]), acc[a], 0, kXFmt, 0, (int)sw[u], 0, (int)sx[u]);
+    if constexpr (kR != 0) {
+      static_assert(kU == 4, "eight steps of 64 per turn of the loop");
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+#pragma unroll
+        for (int e = 0; e < kA; ++e) {
+          const int id = (e * 64 + lane) * 8;
+          const uint32_t to = at + (uint32_t)(id / kR * kPitch + id % kR * 2);
+          *(lds_u32x2*)(uintptr_t)to = u32x2{av[u][e][0], av[u][e][1]};
+          *(lds_u32x2*)(uintptr_t)(to + 8) = u32x2{av[u][e][2], av[u][e][3]};
+        }
+        const float s = act8_scale((int)sx[u]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // rows 64 (c / 2) + 16 g + 8 (c % 2) of the block
+          const u32x4 xd = act8_decode8<kXFmt>(
+              u32x2{x[u][c >> 1][2 * (c & 1)], x[u][c >> 1][2 * (c & 1) + 1]}, s);
+          floatx4& t = tacc[2 * u + (c >> 1)];
+          t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              as_bf16x8(xd), tr_frag<kPitch>(at, 64 * (c >> 1) + 16 * g + 8 * (c & 1), 0, lane), t, 0, 0, 0);
+        }
+      }
+    }
+  }
+  if constexpr (kR != 0) {
+    floatx4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) t[v] += tacc[c][v] + tacc[c + 4][v];
+    s_tacc[wave][lane] = t;
   }
 #pragma unroll
   for (int a = 0; a < RN; ++a) s_acc[wave][a][lane] = acc[a];
@@ -497,7 +548,24 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
   const int64_t n = n0 + nl, m = m0 + ml;
   const bool mine = ml < kM && n < p.N && m < p.M;
   float y = 0.0f;
-  if (q.part) {
+  if constexpr (kR != 0) {
+    __syncthreads();
+    if (tid < kM * kR) {
+      // T's element (row 4 g + v, column i)
+      const int tm = tid / kR, j = tid % kR;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFewWaves; ++w) v += s_tacc[w][(tm >> 2) * 16 + j][tm & 3];
+      if (q.T_out && blockIdx.x == 0 && m0 + tm < p.M) q.T_out[(m0 + tm) * kR + j] = v;
+      s_t[tm][j] = q.scale * v;
+    }
+    __syncthreads();
+    if (mine) {
+      const uint16_t* b = q.B + n;
+#pragma unroll
+      for (int j = 0; j < kR; ++j) y += s_t[ml][j] * __builtin_bit_cast(float, (uint32_t)b[j * p.N] << 16);
+    }
+  } else if (q.part) {
     for (int j0 = 0; j0 < q.r; j0 += kJ) {
       const int nj = min(kJ, q.r - j0);
       __syncthreads();
@@ -587,9 +655,9 @@ hipError_t run_small(Fp8Gemm p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int RN, int kXFmt>
+template <int RN, int kXFmt, int kR>
 hipError_t run_few(const Fp8Few& q, hipStream_t stream) {
-  auto kern = fp8_few_kernel<RN, kXFmt>;
+  auto kern = fp8_few_kernel<RN, kXFmt, kR>;
   const dim3 grid((unsigned)((q.g.N + 16 * RN - 1) / (16 * RN)), (unsigned)((q.g.M + 15) / 16));
   hipLaunchKernelGGL(kern, grid, dim3(kFewWaves * 64), 0, stream, q);
   return hipGetLastError();
@@ -663,15 +731,34 @@ hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int
 
 bool fp8_few(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 15) / 16) <= 512; }
 
+// Every workgroup reads all of A for it, beside its weight rows: worth a launch
+// up to about 128 Ki elements (us per call from a graph, formed in the kernel
+// and before it: 1 x 4096 x 4096 r = 16 9.8 and 11.4, 64 x 2048 x 2048 r = 16
+// 9.3 and 13.7, 16 x 512 x 8192 r = 16 15.6 and 17.1, 1 x 4096 x 11008 r = 16
+// 20.3 and 18.9).
+bool few_t_shape(int64_t M, int64_t K, int r) {
+  return M <= 64 && (r == 8 || r == 16) && K * r <= (int64_t)1 << 17;
+}
+bool fp8_few_forms_t(const uint16_t* A, int64_t M, int64_t K, int r) {
+  return few_t_shape(M, K, r) && (reinterpret_cast<uintptr_t>(A) & 15) == 0;
+}
+
 hipError_t launch_fp8_few(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
-                          const float* part, int splits, const uint16_t* B, int r, float scale,
-                          uint16_t* Y, float* T_out, hipStream_t stream) {
-  const Fp8Few q{gemm_args(x, w, M, N, K, Y), part, splits, lowrank_cols(r), r, scale, B, T_out};
+                          const uint16_t* A, const float* part, int splits, const uint16_t* B, int r,
+                          float scale, uint16_t* Y, float* T_out, hipStream_t stream) {
+  const Fp8Few q{gemm_args(x, w, M, N, K, Y), part, A, K, splits, lowrank_cols(r), r, scale, B, T_out};
   // 16 weight rows per workgroup while that leaves one per compute unit, else
   // 32 (32 x 4096 x 4096: 11.6 us against 13.8)
-  if ((M + 15) / 16 * ((N + 15) / 16) <= 256)
-    return xfmt ? run_few<1, 1>(q, stream) : run_few<1, 0>(q, stream);
-  return xfmt ? run_few<2, 1>(q, stream) : run_few<2, 0>(q, stream);
+  const bool narrow = (M + 15) / 16 * ((N + 15) / 16) <= 256;
+  auto go = [&](auto fmt, auto rank) {
+    constexpr int kFmt = decltype(fmt)::value, kR = decltype(rank)::value;
+    return narrow ? run_few<1, kFmt, kR>(q, stream) : run_few<2, kFmt, kR>(q, stream);
+  };
+  auto by_rank = [&](auto fmt) {
+    if (!A) return go(fmt, std::integral_constant<int, 0>{});
+    return r == 8 ? go(fmt, std::integral_constant<int, 8>{}) : go(fmt, std::integral_constant<int, 16>{});
+  };
+  return xfmt ? by_rank(std::integral_constant<int, 1>{}) : by_rank(std::integral_constant<int, 0>{});
 }
 
 }  // namespace qlora

@@ -136,12 +136,17 @@ hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int
                             uint16_t* Y, hipStream_t stream);
 
 // The same product where its output is small (fp8_few), the adapter's term
-// from split partials of T (launch_rows_act8; null without an adapter);
-// writes T_out.
+// from split partials of T (launch_rows_act8; null without an adapter) or, where
+// fp8_few_forms_t, from A (else null); writes T_out. For few_t_shape
+// launch_rows_act8 sums kFewWaves runs along K as that kernel does, so that
+// both give T the same bits.
 bool fp8_few(int64_t M, int64_t N);
+bool few_t_shape(int64_t M, int64_t K, int r);
+bool fp8_few_forms_t(const uint16_t* A, int64_t M, int64_t K, int r);
+constexpr int kFewWaves = 8;
 hipError_t launch_fp8_few(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
-                          const float* part, int splits, const uint16_t* B, int r, float scale,
-                          uint16_t* Y, float* T_out, hipStream_t stream);
+                          const uint16_t* A, const float* part, int splits, const uint16_t* B, int r,
+                          float scale, uint16_t* Y, float* T_out, hipStream_t stream);
 
 // The adapter's products beside an 8-bit input (lowrank8.hip).
 // Columns of a low-rank partial or term matrix: r rounded up to 16, 32 or a

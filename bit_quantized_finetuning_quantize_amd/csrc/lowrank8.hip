@@ -41,8 +41,6 @@ constexpr int kTerms = 3;
 constexpr int kPitch = 144;  // bytes of a transposing tile's row: 64 bf16 and 16 bytes
                              // of padding, which keeps four rows on distinct banks
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) float lds_f32;
 typedef __attribute__((address_space(3))) floatx4 lds_floatx4;
 
@@ -63,18 +61,6 @@ struct Stream {
 // 2 KiB of consecutive memory.
 __device__ __forceinline__ int64_t frag_index(int64_t m, int64_t j, int64_t rp) {
   return (((m >> 5) * (rp >> 4) + (j >> 4)) * 64 + ((m >> 3) & 3) * 16 + (j & 15)) * 8 + (m & 7);
-}
-
-// The eight transposed elements of a fragment from a row-major tile: lane l
-// receives column (l & 15) + c0 and rows r0 .. r0 + 7 of its own 16-lane
-// group's row base.
-__device__ __forceinline__ bf16x8 tr_frag(uint32_t tile, int row0, int c0, int lane) {
-  const int p = lane & 15;
-  const uint32_t a = tile + (uint32_t)((row0 + (p >> 2)) * kPitch + (c0 + (p & 3) * 4) * 2);
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(a + 4 * kPitch));
-  const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
-  return as_bf16x8(u32x4{l2[0], l2[1], h2[0], h2[1]});
 }
 
 // The waves' accumulators of one 64 x 16 NJ tile (block f * NJ + jt holds rows
@@ -236,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
       bf16x8 w[NJ];
 #pragma unroll
       for (int jt = 0; jt < NJ; ++jt) {
-        if constexpr (kTrans) w[jt] = tr_frag(wt, 16 * g + 8 * h, jt * 16, lane);
+        if constexpr (kTrans) w[jt] = tr_frag<kPitch>(wt, 16 * g + 8 * h, jt * 16, lane);
         else w[jt] = as_bf16x8(q.w[jt * 2 + h]);
       }
 #pragma unroll
@@ -581,7 +567,7 @@ __device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0,
     }
     bf16x8 x[4];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) x[f] = tr_frag(tile, 8 * g, f * 16, lane);
+    for (int f = 0; f < 4; ++f) x[f] = tr_frag<kPitch>(tile, 8 * g, f * 16, lane);
 #pragma unroll
     for (int jt = 0; jt < NJ; ++jt) {
       u32x4 term[kTerms];
@@ -653,15 +639,16 @@ hipError_t run_rows(RowProd p, int splits, hipStream_t stream) {
   });
 }
 
-RowProd row_args(Stream s, const uint16_t* w, int r, float* part, int* splits) {
+// `per`: steps of a split, or 0 for row_splits' choice.
+RowProd row_args(Stream s, const uint16_t* w, int r, int per, float* part, int* splits) {
   RowProd p{};
   p.s = s;
   p.w = w;
   p.r = r;
   p.wvec = r % 8 == 0 && (reinterpret_cast<uintptr_t>(w) & 15) == 0;
   p.steps = (int)ceil_div(s.cols, 64);
-  *splits = row_splits(s.rows, s.cols, r);
-  p.per = (int)ceil_div(p.steps, *splits);
+  *splits = per ? (int)ceil_div(p.steps, per) : row_splits(s.rows, s.cols, r);
+  p.per = per ? per : (int)ceil_div(p.steps, *splits);
   p.ldp = lowrank_cols(r);
   p.part = part;
   p.tiles = (int)ceil_div(s.rows, 64);
@@ -678,14 +665,16 @@ int lowrank_cols(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : (int)ceil_div(r, 
 
 hipError_t launch_rows_act8(ConstAct8 x, int fmt, int64_t M, int64_t K, const uint32_t* mask,
                             const uint16_t* A, int r, float* part, int* splits, hipStream_t stream) {
-  const RowProd p = row_args(act8_stream(x, M, K, mask), A, r, part, splits);
+  // where the 8-bit product for few tokens may form T itself, its order
+  const int per = few_t_shape(M, K, r) ? 2 * (int)ceil_div(act8_row_bytes(K) / kAct8Block, kFewWaves) : 0;
+  const RowProd p = row_args(act8_stream(x, M, K, mask), A, r, per, part, splits);
   if (mask) return fmt ? run_rows<kE5M2, true, true>(p, *splits, stream) : run_rows<kE4M3, true, true>(p, *splits, stream);
   return fmt ? run_rows<kE5M2, false, true>(p, *splits, stream) : run_rows<kE4M3, false, true>(p, *splits, stream);
 }
 
 hipError_t launch_rows_bf16(const uint16_t* S, int64_t M, int64_t C, const uint16_t* B, int r,
                             float* part, int* splits, hipStream_t stream) {
-  const RowProd p = row_args(Stream{S, nullptr, C * 2, 0, M, C, nullptr}, B, r, part, splits);
+  const RowProd p = row_args(Stream{S, nullptr, C * 2, 0, M, C, nullptr}, B, r, 0, part, splits);
   return run_rows<kBf16, false, false>(p, *splits, stream);
 }
 

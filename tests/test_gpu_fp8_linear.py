@@ -167,6 +167,28 @@ def test_fp8_linear(q, M, N, K, r, fmt):
     assert r2[0] is None and torch.equal(r2[1], dA) and torch.equal(r2[2], dB)
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 64, 8), (17, 448, 576, 8), (64, 1088, 192, 16), (16, 128, 8192, 16),
+                                     (3, 192, 1344, 16), (64, 64, 16384, 8), (2, 64, 16448, 8), (65, 64, 256, 16)])
+def test_few_tokens_form_t(q, M, N, K, r, fmt):
+    """T formed beside the 8-bit product: against the formula, and its bits
+    against a launch of its own (an A that 16-byte loads cannot take) and a
+    backward pass that recomputes it."""
+    print(f"[case] few tokens M={M} N={N} K={K} r={r} fmt={fmt}", flush=True)
+    c = Case(q, M, N, K, r, fmt)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    Y, T = q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s)
+    _fwd_check(c, W, Y, T, N, K, r)
+    flat = torch.empty(K * r + 1, dtype=torch.bfloat16, device=c.A.device)
+    A = flat[1:].view(K, r)
+    A.copy_(c.A)
+    Y1, T1 = q.qlora_fp8_linear_fwd(c.x8, W, A, c.B, c.s)
+    assert torch.equal(T, T1) and torch.equal(Y, Y1)
+    g0 = q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, c.A, c.B, c.s, want_dX=False)
+    g1 = q.qlora_fp8_linear_bwd(c.dY, c.x8, None, W, c.A, c.B, c.s, want_dX=False)
+    assert torch.equal(g0[1], g1[1]) and torch.equal(g0[2], g1[2])
+
+
 @pytest.mark.parametrize("store_type", [0, 3])
 @pytest.mark.parametrize("drop", [0.0, 0.1])
 @pytest.mark.parametrize("M,N,K,r", SHAPES[:8])
@@ -316,3 +338,17 @@ def test_refusals(q):
     with pytest.raises(q.QloraError):
         q.qlora_fp8_linear_fwd(d.x8, w, A, A.t().contiguous(), 1.0)
     q.qlora_fp8_linear_fwd(d.x8, w)
+
+
+def test_workspace_must_be_device_bytes(q):
+    c = Case(q, 2, 64, 64, 8, 0)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    n = q.qlora_act8_workspace_bytes(2, 64, 64, 8)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(n, dtype=torch.float32, device=c.A.device),
+               torch.empty(2 * n, dtype=torch.uint8, device=c.A.device)[::2]):
+        with pytest.raises(q.QloraError):
+            q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s, ws=ws)
+        with pytest.raises(q.QloraError):
+            q.qlora_fp8_linear_bwd(c.dY, c.x8, None, W, c.A, c.B, c.s, ws=ws)
+        with pytest.raises(q.QloraError):
+            q.qlora_linear_bwd_act8(c.dY, c.x8, None, q.qlora_nf4_quantize(c.W), c.A, c.B, c.s, ws=ws)
