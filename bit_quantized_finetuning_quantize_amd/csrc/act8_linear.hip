@@ -7,7 +7,8 @@
 //             Y = dec(X8) dec(W8)^T + (s T) B          8-bit product
 //             (few tokens: T, or its partials summed,  8-bit product
 //             and s T in float32 there)
-//   backward  G = dY B^T, split along N                row product
+//   backward  G = dY B^T, split along N (a short N:    row product
+//             in the next launch)
 //             bf16(s G); float32 s G and s T; beside   one launch
 //             them the weight to bf16 (NF4) or dY to
 //             8 bits (8-bit weight)
@@ -81,6 +82,13 @@ bool in_place(const uint16_t* A, int r) {
   return r % 64 == 0 && (reinterpret_cast<uintptr_t>(A) & 15) == 0;
 }
 
+// Whether G = dY B^T is formed where it is written out, in one launch less
+// (whole 8-bit backward from a graph, us, so and with its own launch:
+// 16 x 256 x 256 r = 8 10.3 and 12.9, 2048 x 512 x 2048 r = 64 33.0 and 37.6,
+// 257 x 1024 x 1024 r = 64 22.0 and 23.0, 16 x 2048 x 1024 r = 64 28.6 and 21.4,
+// 2048 x 1024 x 1024 r = 256 43.4 and 39.6).
+bool factor_in_place(int64_t N, int r) { return N <= 1024 && r <= 64; }
+
 // The adapter's part of a backward pass before dX: bf16(s G) in u, A padded
 // in v (unless it serves as it is), float32 s G and s T for dA and dB.
 hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, const uint16_t* A,
@@ -91,12 +99,13 @@ hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, c
   int splits = 0;
   if (!T) {  // recomputed from the 8-bit input
     QLORA_TRY(launch_rows_act8(x, fmt, M, K, dr.mask, A, r, w.part, &splits, stream));
-    const LowrankOut t{w.part, splits, ldp, f, nullptr, nullptr, w.t};
+    const LowrankOut t{w.part, nullptr, nullptr, 0, splits, ldp, f, nullptr, nullptr, w.t};
     QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{}, M, r, scale, stream));
   }
-  QLORA_TRY(launch_rows_bf16(dY, M, N, B, r, w.part, &splits, stream));
-  const LowrankOut o[2] = {{w.part, splits, ldp, f, nullptr, w.u, w.g},
-                           {T, 1, r, 1.0f, nullptr, nullptr, w.t}};
+  const bool here = factor_in_place(N, r);
+  if (!here) QLORA_TRY(launch_rows_bf16(dY, M, N, B, r, w.part, &splits, stream));
+  const LowrankOut o[2] = {{here ? nullptr : w.part, here ? dY : nullptr, B, N, splits, ldp, f, nullptr, w.u, w.g},
+                           {T, nullptr, nullptr, 0, 1, r, 1.0f, nullptr, nullptr, w.t}};
   const LowrankPad pad = in_place(A, r) ? LowrankPad{} : LowrankPad{A, false, K, w.v};
   return launch_lowrank_out(o, T ? 2 : 1, pad, M, r, scale, stream, beside);
 }
@@ -137,7 +146,7 @@ hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A,
   QLORA_TRY(launch_rows_act8(x, fmt, M, K, nullptr, A, r, w.part, &splits, stream));
   if (few)
     return launch_fp8_few(x, fmt, w8, M, N, K, nullptr, w.part, splits, B, r, scale, Y, T_out, stream);
-  const LowrankOut t{w.part, splits, lowrank_cols(r), 1.0f, T_out, w.u, nullptr};
+  const LowrankOut t{w.part, nullptr, nullptr, 0, splits, lowrank_cols(r), 1.0f, T_out, w.u, nullptr};
   QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{B, true, N, w.v}, M, r, scale, stream));
   return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, stream);
 }

@@ -416,12 +416,14 @@ fp8_gemm_small_kernel(Fp8Gemm p) {
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: the time is that of streaming the weight once. A workgroup owns
-// 16 RN weight rows and 16 tokens over the whole of K, its eight waves a
-// run of blocks each; both operands go from memory straight to registers
+// Few tokens: the time is that of a launch and of streaming the weight once
+// (1 x 4096 x 4096, 17 MB: 6.4 us; 7.8 us where it forms T for r = 16). A
+// workgroup owns 16 RN weight rows and 16 tokens over the whole of K, its eight
+// waves a run of blocks each; both operands go from memory straight to registers
 // (v_mfma_scale_f32_16x16x128_f8f6f4 takes a whole block), four blocks' loads
-// in flight together, and the waves' sums meet in LDS in a fixed order. The
-// adapter's term is added there in float32, from the split partials of T.
+// in flight together, and the waves' sums meet in LDS in a fixed order. Two sets
+// of four blocks in flight gained 2 to 5 % with 16 weight rows and spilled with
+// 32. The adapter's term is added there in float32, from the split partials of T.
 struct Fp8Few {
   Fp8Gemm g;
   const float* part;   // [splits][M][ldp] partials of T, or null
@@ -664,8 +666,9 @@ hipError_t run_few(const Fp8Few& q, hipStream_t stream) {
 }
 
 // Tile by the number of workgroups it gives. 256 x 256 moves the fewest
-// operand bytes per product and is fastest once the chip is full (8192^3:
-// 398 us; 128 x 128 in two workgroups per compute unit 497 us); smaller tiles
+// operand bytes per product and is fastest once the chip is full (8192^3 with
+// this tile 398 us when 128 x 128 in two workgroups per compute unit took 497);
+// smaller tiles
 // spread a small output over more compute units. From a graph of calls on
 // rotating weights (us per call, 2 to 3 of them the graph's):
 //   M x N x K            64 x 64   128 x 64   256 x 256 in parts

@@ -164,7 +164,9 @@ hipError_t launch_rows_bf16(const uint16_t* S, int64_t M, int64_t C, const uint1
 // lowrank_cols(r) floats); each output may be null. Up to two of them and one padded copy per launch:
 // dst [rows x r64] from src [rows x r], or from the columns of src [r x rows].
 struct LowrankOut {
-  const float* part;
+  const float* part;  // or null, with
+  const uint16_t *s, *w;  // the factors of V = S W^T: S bf16 [M x C], W [r x C], C a multiple of 64
+  int64_t C;
   int splits;
   int64_t ldp;
   float f;

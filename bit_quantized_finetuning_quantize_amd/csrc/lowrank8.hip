@@ -4,9 +4,15 @@
 // Column products P[c][j] = sum_m S[m][c] V[m][j]     dA = dec(X8)^T (s G), dB^T = dY^T (s T)
 //
 // S streams past once: codes are decoded in registers (a code times its
-// power-of-two scale is an exact bf16 value). Both are bound by reading S
-// and by the small factor's traffic through the caches; the matrix work is
-// r columns wide.
+// power-of-two scale is an exact bf16 value). The matrix work is r columns
+// wide, so both are bound by reading S and by the small factor, which every
+// workgroup reads again through the caches. Kernel times at r = 64:
+//   dY B^T, 2048 x 11008 (bf16, 45 MB)       16 to 19 us, 2.4 to 2.8 TB/s of S
+//   dec(X8) A, 4096 x 8192 (33.5 MB)         18 us, 1.9 TB/s (A is r K values,
+//                                            decoded X passes the vector units)
+//   dA and dB at K = 11008, N = 4096, 2048 rows (39 MB)   19 to 23 us
+// At 257 rows or fewer they take 3 to 5 us, mostly the launch and one round
+// trip to memory.
 //
 // v_mfma_f32_16x16x32_bf16 takes eight contraction elements per lane. A row
 // product finds them next to each other in memory (S and B rows), except for
@@ -19,8 +25,9 @@
 // product as three bf16 terms whose sum is the value to 24 bits, so the
 // products of bf16 values carry float32 accuracy. The terms are formed in
 // registers: V passes once per 64 columns of S and is most of the cache
-// traffic, 4 bytes an element so instead of 6. The results of the waves of a workgroup, which
-// take turns along the contraction, are added in a fixed order.
+// traffic, 4 bytes an element so instead of 6 (terms formed beforehand took the
+// same time and half as much memory again). The results of the waves of a
+// workgroup, which take turns along the contraction, are added in a fixed order.
 #include "act8.h"
 #include "gemm.h"
 #include "kernels.h"
@@ -103,7 +110,9 @@ __device__ __forceinline__ float tile_sum(uint32_t buf, int row, int col) {
 }
 
 // ---------------------------------------------------------------------------
-// Row products: 64 rows by 16 NJ columns per workgroup; the waves take the
+// Row products: 64 rows by 16 NJ columns per workgroup (so that S is read once
+// for r up to 64), split along the contraction into about one workgroup per
+// compute unit (512 halves: 22 us instead of 16 for dY B^T); the waves take the
 // contraction 64 elements at a time in turn. Inside such a step the lanes of
 // group g hold elements 16 g .. 16 g + 15 (one 16-byte piece of codes), which
 // make two matrix instructions of eight elements per lane.
@@ -259,9 +268,13 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
 //   u      bf16(s V), [Mp x r64], 0 past M and r
 //   vf     s V in float32 in the order a column product reads it
 //          (frag_index), 0 past M and r
-// 16 x 64 tiles, through LDS for the last form.
+// 16 x 64 tiles, through LDS for the last form. 4.5 to 5.5 us up to 4096 rows:
+// a launch and one round trip, whence the other work in the same launch (8-bit
+// blocks of dY at 2048 x 4096 beside it: 7.0 us, 5.8 in a launch of its own).
 struct OutJob {
-  const float* part;  // null: no job
+  const float* part;  // null: no job, or the product below
+  const uint16_t *sm, *w;  // the partials' place: V = S W^T formed here, S [M x C], W [r x C]
+  int64_t C;
   int splits;
   int64_t ldp;
   float f;
@@ -281,28 +294,67 @@ struct PadJob {
 constexpr int kOutThreads = 256;
 constexpr int kOutRows = 16;  // rows of M per workgroup
 
+// A tile of V = S W^T in place of summed partials, a wave per 16 columns, over
+// the whole of C: for the C at which a launch costs more than the few trips to
+// memory that one wave then makes.
+__device__ __forceinline__ void out_product(const OutJob& jb, int64_t mt, int jc, int64_t M, int r,
+                                            float (*tile)[65]) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const int t = threadIdx.x, lane = t & 63, i = lane & 15, g = lane >> 4, ja = jc * 64 + (t >> 6) * 16 + i;
+  const int64_t first = mt * kOutRows;
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(jb.sm + first * jb.C, min(M - first, (int64_t)kOutRows) * jb.C * 2);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(jb.w, r * jb.C * 2);
+  const int so = (int)(i * jb.C * 2) + g * 16, wo = ja < r ? (int)(ja * jb.C * 2) + g * 16 : 0x70000000;
+  floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int kU = 8;  // pieces of 32 elements in flight
+  for (int c = 0; c < (int)jb.C * 2; c += kU * 64) {
+    u32x4 x[kU], w[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int off = c + u * 64 < (int)jb.C * 2 ? c + u * 64 : 0x7f000000;  // past the row: zeros
+      x[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, so, off, 0));
+      w[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wo, off, 0));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[u]), as_bf16x8(w[u]), acc, 0, 0, 0);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) tile[4 * g + e][(t >> 6) * 16 + i] = acc[e];
+#endif
+}
+
 __device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, int64_t M, int64_t Mp,
                                          int r, int64_t r64, int64_t rp, float s, float (*tile)[65]) {
   const int t = threadIdx.x;
   float v[4];
   const int jl = t & 63, j = jc * 64 + jl;
   const int64_t m0 = mt * kOutRows + (t >> 6);
-  // loads inside the product's rows and columns, so that none is conditional;
-  // more splits at a time would take registers from the work beside
-  const float* at[4];
+  if (jb.sm) {
+    out_product(jb, mt, jc, M, r, tile);
+    __syncthreads();
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[q] = 0.0f;
-    at[q] = jb.part + min(m0 + 4 * q, M - 1) * jb.ldp + min(j, r - 1);
-  }
-  const int64_t stride = M * jb.ldp;
+    for (int q = 0; q < 4; ++q) v[q] = tile[(t >> 6) + 4 * q][jl];
+    __syncthreads();
+  } else {
+    // loads inside the product's rows and columns, so that none is conditional;
+    // more splits at a time would take registers from the work beside
+    const float* at[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = 0.0f;
+      at[q] = jb.part + min(m0 + 4 * q, M - 1) * jb.ldp + min(j, r - 1);
+    }
+    const int64_t stride = M * jb.ldp;
 #pragma unroll 2
-  for (int sp = 0; sp < jb.splits; ++sp)
+    for (int sp = 0; sp < jb.splits; ++sp)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] += at[q][sp * stride];
+      for (int q = 0; q < 4; ++q) v[q] += at[q][sp * stride];
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (m0 + 4 * q >= M || j >= r) v[q] = 0.0f;
+    for (int q = 0; q < 4; ++q)
+      if (m0 + 4 * q >= M || j >= r) v[q] = 0.0f;
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int64_t m = m0 + 4 * q;
@@ -363,9 +415,9 @@ __device__ __forceinline__ void pad_tile(const PadJob& jb, int64_t rt, int jc, i
 // bf16(w') of a 4-bit store, transposed: one tile of 64 weight rows by 128
 // columns per workgroup. A thread decodes 16 codes of two neighbouring rows
 // (inside one block of 64 each) and writes them to LDS as pairs; the tile is
-// stored by its columns, 128 bytes each.
+// stored by its columns, 128 bytes each. Bound by its writes: 11008 x 4096, 90 MB
+// written and 24 MB read, takes 25 us with the jobs beside it (4.6 TB/s).
 constexpr int kTPitch = 136;  // bytes of an LDS row: 64 bf16 and 8 bytes of padding
-
 constexpr int kDecodeLds = 64 + 128 * kTPitch;
 
 __device__ __forceinline__ void nf4_decode_t(const Nf4Weight& W, int64_t N, int64_t K, const Codebook& cb,
@@ -688,7 +740,7 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
   p.rp = lowrank_cols(r);
   p.s = s;
   for (int i = 0; i < n; ++i)
-    p.o[i] = OutJob{o[i].part, o[i].splits, o[i].ldp, o[i].f, o[i].out32, o[i].u, o[i].vf};
+    p.o[i] = OutJob{o[i].part, o[i].s, o[i].w, o[i].C, o[i].splits, o[i].ldp, o[i].f, o[i].out32, o[i].u, o[i].vf};
   p.pad = PadJob{pad.src, pad.columns, pad.rows, pad.dst};
   p.cols = (int)(p.r64 / 64);
   p.blocks0 = (int)(p.Mp / kOutRows);
