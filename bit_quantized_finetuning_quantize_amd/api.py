@@ -577,7 +577,7 @@ def _adapter(A, B, N, K):
 
 def _out(t, shape, dtype, device, name):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)  # 0.4 us less than of a tuple
     _need(t, dtype, name)
     if t.shape != shape:
         raise QloraError(f"{name} must have shape {shape}")

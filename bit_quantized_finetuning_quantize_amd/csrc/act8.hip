@@ -14,7 +14,7 @@
 //   dequantize  11.7 us   68 MB  5.8 TB/s
 //   SwiGLU      41.4 us  203 MB  4.9 TB/s (H and three sets of blocks)
 //   its backward  29.2 us  181 MB  6.2 TB/s
-// and a weight of 11008 x 4096 in both orders takes 38 us (180 MB, 4.7 TB/s).
+// and a weight of 11008 x 4096 in both orders takes 40 us (180 MB, 4.5 TB/s).
 // Small calls (16 x 4096) take 2.4 us, a launch's own time.
 #include "act8.h"
 #include "kernels.h"
