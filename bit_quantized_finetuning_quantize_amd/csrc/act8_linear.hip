@@ -14,8 +14,7 @@
 //             8 bits (8-bit weight)
 //             dX                                       bf16 or 8-bit product
 //             dA and dB                                column products, one launch
-#include "act8.h"
-#include "kernels.h"
+#include "lowrank8.h"
 
 #include <algorithm>
 
@@ -125,10 +124,10 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
   LowrankBeside beside;
   if (dX) beside.W = W, beside.N = N, beside.K = K, beside.w = w.wt;
   QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, beside, stream));
-  if (dX)
-    QLORA_TRY(launch_bf16_gemm(dY, w.wt, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dr.mask, dX,
-                               stream));
-  return launch_columns(x, fmt, dr.mask, dY, w.g, w.t, M, N, K, r, dA, dB, stream);
+  const lr8::ColPair cols = lr8::column_pair(x, fmt, dr.mask, dY, w.g, w.t, M, N, K, r, dA, dB);
+  return dX ? launch_bf16_gemm(dY, w.wt, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dr.mask, dX,
+                               &cols, stream)
+            : launch_columns(cols, stream);
 }
 
 hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A, const uint16_t* B,
@@ -139,7 +138,7 @@ hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A,
   const bool few = fp8_few(M, N);
   if (!r)
     return few ? launch_fp8_few(x, fmt, w8, M, N, K, nullptr, nullptr, 0, nullptr, 0, scale, Y, nullptr, stream)
-               : launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, stream);
+               : launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, nullptr, stream);
   if (few && fp8_few_forms_t(A, M, K, r))
     return launch_fp8_few(x, fmt, w8, M, N, K, A, nullptr, 0, B, r, scale, Y, T_out, stream);
   int splits = 0;
@@ -148,7 +147,7 @@ hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A,
     return launch_fp8_few(x, fmt, w8, M, N, K, nullptr, w.part, splits, B, r, scale, Y, T_out, stream);
   const LowrankOut t{w.part, nullptr, nullptr, 0, splits, lowrank_cols(r), 1.0f, T_out, w.u, nullptr};
   QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{B, true, N, w.v}, M, r, scale, stream));
-  return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, stream);
+  return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, nullptr, stream);
 }
 
 hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, const float* T,
@@ -157,19 +156,18 @@ hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, c
                           void* ws, hipStream_t stream) {
   const Ws8 l = ws8_layout(M, N, K, r);
   const Ptrs w = carve(ws, l);
-  if (r) {
-    LowrankBeside beside;
-    if (dX) beside.s = dY, beside.C = N, beside.fmt = dyfmt, beside.codes = w.dy8, beside.scales = w.dys;
-    QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, Dropout{}, beside, stream));
-  } else {
+  const ConstAct8 dy8{w.dy8, w.dys};
+  if (!r) {
     QLORA_TRY(launch_act8_quantize(dY, M, N, N, dyfmt, w.dy8, w.dys, stream));
+    return launch_fp8_gemm(dy8, dyfmt, w8t, M, K, N, nullptr, nullptr, 0, dX, nullptr, stream);
   }
-  if (dX) {
-    QLORA_TRY(launch_fp8_gemm(ConstAct8{w.dy8, w.dys}, dyfmt, w8t, M, K, N, r ? w.u : nullptr,
-                              r ? (in_place(A, r) ? A : w.v) : nullptr, (int)l.r64, dX, stream));
-  }
-  if (!r) return hipSuccess;
-  return launch_columns(x, fmt, nullptr, dY, w.g, w.t, M, N, K, r, dA, dB, stream);
+  LowrankBeside beside;
+  if (dX) beside.s = dY, beside.C = N, beside.fmt = dyfmt, beside.codes = w.dy8, beside.scales = w.dys;
+  QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, Dropout{}, beside, stream));
+  const lr8::ColPair cols = lr8::column_pair(x, fmt, nullptr, dY, w.g, w.t, M, N, K, r, dA, dB);
+  return dX ? launch_fp8_gemm(dy8, dyfmt, w8t, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dX, &cols,
+                              stream)
+            : launch_columns(cols, stream);
 }
 
 }  // namespace qlora

@@ -24,9 +24,7 @@
 // sums exchanged through memory (256 x 256 tiles instead of 256 x 128; the
 // exchange took 17 us, more than the larger tiles gained), the waves of a tile
 // splitting K (2048 x 4096 x 11008 75.2 us to 74.0).
-#include "act8.h"
-#include "gemm.h"
-#include "kernels.h"
+#include "lowrank8.h"
 
 #include <algorithm>
 #include <atomic>
@@ -422,12 +420,20 @@ fp8_gemm_kernel(Fp8Gemm p) {
   else gemm_tile<128, 128, 4, 1, kXFmt>(p, n0 + (part & 1) * 128, m0 + (part >> 1) * 128, lds);
 }
 
-// One tile size; several workgroups per compute unit.
-template <int TN, int TM, int kStages, int kGroups, int kXFmt>
-__global__ void __launch_bounds__(256 * kGroups) __attribute__((amdgpu_waves_per_eu(2, kGroups > 2 ? 4 : 2)))
-fp8_gemm_small_kernel(Fp8Gemm p) {
+// One tile size; several workgroups per compute unit. With NJ, the workgroups
+// past the tiles do the column products of a backward pass, which need nothing
+// of this product: they fill the compute units that a small one leaves idle.
+template <int TN, int TM, int kStages, int kGroups, int kXFmt, int NJ>
+__global__ void __launch_bounds__(NJ ? lr8::kThreads : 256 * kGroups)
+__attribute__((amdgpu_waves_per_eu(2, kGroups > 2 ? 4 : 2)))
+fp8_gemm_small_kernel(Fp8Gemm p, lr8::ColPair cols) {
+  const int count = p.nM * p.nN;
+  if constexpr (NJ != 0) {
+    if ((int)blockIdx.x >= count) return lr8::column_job<lr8::kAct8, NJ>(cols, blockIdx.x - count, lds_base());
+    if (kGroups == 1 && threadIdx.x >= 256) return;
+  }
   int tm, tn;
-  tile_at(p, xcd_order(blockIdx.x, gridDim.x), tm, tn);
+  tile_at(p, xcd_order(blockIdx.x, count), tm, tn);
   gemm_tile<TN, TM, kStages, kGroups, kXFmt>(p, (int64_t)tn * TN, (int64_t)tm * TM, lds_base());
 }
 
@@ -657,11 +663,11 @@ hipError_t run_big(Fp8Gemm p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int TN, int TM, int kStages, int kGroups, int kXFmt>
-hipError_t run_small(Fp8Gemm p, hipStream_t stream) {
+template <int TN, int TM, int kStages, int kGroups, int kXFmt, int NJ>
+hipError_t run_small(Fp8Gemm p, const lr8::ColPair& cols, hipStream_t stream) {
   static std::atomic<uint64_t> raised{0};
-  auto kern = fp8_gemm_small_kernel<TN, TM, kStages, kGroups, kXFmt>;
-  constexpr size_t lds = lds_bytes(TN, TM, kStages, kGroups);
+  auto kern = fp8_gemm_small_kernel<TN, TM, kStages, kGroups, kXFmt, NJ>;
+  constexpr size_t lds = std::max(lds_bytes(TN, TM, kStages, kGroups), NJ ? lr8::column_lds(NJ) : 0);
   if (lds > 65536) {
     hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), lds, raised);
     if (e != hipSuccess) return e;
@@ -669,7 +675,8 @@ hipError_t run_small(Fp8Gemm p, hipStream_t stream) {
   p.nM = (int)((p.M + TM - 1) / TM);
   p.nN = (int)((p.N + TN - 1) / TN);
   p.group = 4;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(p.nM * p.nN)), dim3(256 * kGroups), lds, stream, p);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(p.nM * p.nN + (NJ ? cols.jobs : 0))),
+                     dim3(NJ ? lr8::kThreads : 256 * kGroups), lds, stream, p, cols);
   return hipGetLastError();
 }
 
@@ -694,16 +701,31 @@ hipError_t run_few(const Fp8Few& q, hipStream_t stream) {
 //   1000 x 512 x 512      5.4 (4.3)    6.7 (5.1)     6.9
 // with two sets of waves, in brackets with one: two sets pay from about 16
 // steps on, while every workgroup has a compute unit of its own.
+//
+// `cols`: column products to do besides, or null. They share the launch of a
+// grid that leaves compute units idle, else they follow in their own (whole
+// 8-bit backward, us in a graph, so and in two launches: 16 x 256 x 256 r = 8
+// 7.8 and 10.3, 257 x 4096 x 4096 r = 8 26.9 and 30.8, 64 x 4096 x 4096 r = 64
+// 23.6 and 28.3, 512 x 4096 x 4096 r = 64 with its 256 workgroups 36.5 and 37.2).
 template <int kXFmt>
-hipError_t run_fmt(const Fp8Gemm& p, hipStream_t stream) {
+hipError_t run_fmt(const Fp8Gemm& p, const lr8::ColPair* cols, hipStream_t stream) {
   const int64_t mt = (p.M + 63) / 64;
   const int64_t t64 = mt * ((p.N + 63) / 64), t128 = mt * ((p.N + 127) / 128);
   const bool two = p.KB >= 16;
-  if (t64 <= 256)
-    return two ? run_small<64, 64, 4, 2, kXFmt>(p, stream) : run_small<64, 64, 4, 1, kXFmt>(p, stream);
-  if (t128 <= 256 && two) return run_small<128, 64, 3, 2, kXFmt>(p, stream);
-  if (t128 < 512) return run_small<128, 64, 3, 1, kXFmt>(p, stream);
-  return run_big<kXFmt>(p, stream);
+  if (t128 <= 256) {
+    auto small = [&](auto nj) {
+      constexpr int NJ = decltype(nj)::value;
+      const lr8::ColPair none{};
+      const lr8::ColPair& c = NJ ? *cols : none;
+      if (t64 <= 256)
+        return two ? run_small<64, 64, 4, 2, kXFmt, NJ>(p, c, stream) : run_small<64, 64, 4, 1, kXFmt, NJ>(p, c, stream);
+      return two ? run_small<128, 64, 3, 2, kXFmt, NJ>(p, c, stream) : run_small<128, 64, 3, 1, kXFmt, NJ>(p, c, stream);
+    };
+    return cols ? lr8::by_nj(cols->r, small) : small(std::integral_constant<int, 0>{});
+  }
+  const hipError_t e = t128 < 512 ? run_small<128, 64, 3, 1, kXFmt, 0>(p, lr8::ColPair{}, stream)
+                                  : run_big<kXFmt>(p, stream);
+  return cols && e == hipSuccess ? launch_columns(*cols, stream) : e;
 }
 
 // Y past the caches when it and the operands together outgrow the 256 MiB
@@ -729,15 +751,15 @@ Fp8Gemm gemm_args(ConstAct8 x, ConstAct8 w, int64_t M, int64_t N, int64_t K, uin
 
 hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
                            const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
-                           hipStream_t stream) {
+                           const lr8::ColPair* cols, hipStream_t stream) {
   Fp8Gemm p = gemm_args(x, w, M, N, K, Y);
   p.U = U; p.V = V; p.r64 = r64;
-  return xfmt ? run_fmt<1>(p, stream) : run_fmt<0>(p, stream);
+  return xfmt ? run_fmt<1>(p, cols, stream) : run_fmt<0>(p, cols, stream);
 }
 
 hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
                             const uint16_t* U, const uint16_t* V, int r64, const uint32_t* keep,
-                            uint16_t* Y, hipStream_t stream) {
+                            uint16_t* Y, const lr8::ColPair* cols, hipStream_t stream) {
   Fp8Gemm p{};
   p.x = reinterpret_cast<const uint8_t*>(x);
   p.w = reinterpret_cast<const uint8_t*>(w);
@@ -745,7 +767,7 @@ hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int
   p.KB = (int)(K / 64);
   p.U = U; p.V = V; p.r64 = r64; p.keep = keep; p.Y = Y;
   p.stream = streams_out(M, N, p.ldc);
-  return run_fmt<kBf16>(p, stream);
+  return run_fmt<kBf16>(p, cols, stream);
 }
 
 bool fp8_few(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 15) / 16) <= 512; }

@@ -123,17 +123,22 @@ hipError_t launch_swiglu_act8_bwd(const uint16_t* dh, int64_t lddh, ConstAct8 g8
                                   int64_t M, int64_t F, int fmt, uint16_t* dg, int64_t lddg,
                                   uint16_t* du, int64_t lddu, hipStream_t stream);
 
+namespace lr8 {
+struct ColPair;
+}
+
 // Y [M x N] = dec(x) dec(w)^T + U V^T; x [M x K], w [N x K] in 128 x 128
-// blocks (E4M3), U bf16 [M x r64] and V bf16 [N x r64] or null.
+// blocks (E4M3), U bf16 [M x r64] and V bf16 [N x r64] or null; and the column
+// products `cols` (or null).
 hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
                            const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
-                           hipStream_t stream);
+                           const lr8::ColPair* cols, hipStream_t stream);
 
 // The same for bf16 x [M x K] and w [N x K], K a multiple of 64, with a keep
 // mask [M][N / 32] over the U V^T term (or null).
 hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
                             const uint16_t* U, const uint16_t* V, int r64, const uint32_t* keep,
-                            uint16_t* Y, hipStream_t stream);
+                            uint16_t* Y, const lr8::ColPair* cols, hipStream_t stream);
 
 // The same product where its output is small (fp8_few), the adapter's term
 // from split partials of T (launch_rows_act8; null without an adapter) or, where
@@ -194,10 +199,8 @@ struct LowrankBeside {
 };
 hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_t M, int r, float s,
                               hipStream_t stream, const LowrankBeside& beside = LowrankBeside{});
-// dA = D(dec x)^T g, dB = t^T dY, g and t as launch_lowrank_out's vf.
-hipError_t launch_columns(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY,
-                          const float* g, const float* t, int64_t M, int64_t N, int64_t K,
-                          int r, float* dA, float* dB, hipStream_t stream);
+// dA = D(dec x)^T g, dB = t^T dY, g and t as launch_lowrank_out's vf (lowrank8.h).
+hipError_t launch_columns(const lr8::ColPair& p, hipStream_t stream);
 
 // Workspace of the three calls below (r may be 0 for the 8-bit weight's).
 size_t act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);

@@ -28,86 +28,13 @@
 // traffic, 4 bytes an element so instead of 6 (terms formed beforehand took the
 // same time and half as much memory again). The results of the waves of a
 // workgroup, which take turns along the contraction, are added in a fixed order.
-#include "act8.h"
-#include "gemm.h"
-#include "kernels.h"
+#include "lowrank8.h"
 
 #include <algorithm>
 
 namespace qlora {
 
 namespace lr8 {
-
-using gemm::keep_mask8;
-using gemm::lds_u32x4;
-using gemm::make_rsrc;
-
-constexpr int kWaves = 8;
-constexpr int kThreads = kWaves * 64;
-constexpr int kTerms = 3;
-constexpr int kPitch = 144;  // bytes of a transposing tile's row: 64 bf16 and 16 bytes
-                             // of padding, which keeps four rows on distinct banks
-
-typedef __attribute__((address_space(3))) float lds_f32;
-typedef __attribute__((address_space(3))) floatx4 lds_floatx4;
-
-// How S is held: 8-bit blocks in either format, or bf16.
-enum Src { kE4M3 = 0, kE5M2 = 1, kBf16 = 2 };
-
-struct Stream {
-  const void* s;          // codes or bf16 values
-  const uint8_t* scales;  // 8-bit only
-  int64_t ld, sld;        // bytes between rows of s, of scales
-  int64_t rows, cols;
-  const uint32_t* mask;   // dropout keep bits [rows][cols / 32], or null
-};
-
-// Place of element (m, j) in the fragment order of V: blocks of 32 rows; in a
-// block by 16 columns; there as the matrix instruction takes it, lane
-// (m / 8 % 4) * 16 + j % 16 with eight consecutive m, so that one fragment is
-// 2 KiB of consecutive memory.
-__device__ __forceinline__ int64_t frag_index(int64_t m, int64_t j, int64_t rp) {
-  return (((m >> 5) * (rp >> 4) + (j >> 4)) * 64 + ((m >> 3) & 3) * 16 + (j & 15)) * 8 + (m & 7);
-}
-
-// The waves' accumulators of one 64 x 16 NJ tile (block f * NJ + jt holds rows
-// f * 16 + 4 g + e, column jt * 16 + i) added in a fixed order: wave w takes
-// wave w + 4's, and the four sums go to LDS as [sum][column][kRowPitch rows],
-// where tile_sum adds them. Every thread of the workgroup takes part.
-constexpr int kRowPitch = 68;  // floats; 16 columns' 16-byte pieces on distinct banks
-constexpr int tile_bytes(int NJ) { return 4 * 16 * NJ * kRowPitch * 4; }
-
-template <int NJ>
-__device__ __forceinline__ void reduce_waves(floatx4 (&acc)[4 * NJ], uint32_t buf, int wave, int lane) {
-  const uint32_t mine = buf + (uint32_t)((((wave & 3) * 16 * NJ + (lane & 15)) * kRowPitch + (lane >> 4) * 4) * 4);
-  __syncthreads();
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    if ((pass == 0) == (wave >= 4)) {
-#pragma unroll
-      for (int b = 0; b < 4 * NJ; ++b)
-        *(lds_floatx4*)(uintptr_t)(mine + (uint32_t)(((b % NJ) * 16 * kRowPitch + (b / NJ) * 16) * 4)) = acc[b];
-    }
-    __syncthreads();
-    if (pass == 0 && wave < 4) {
-#pragma unroll
-      for (int b = 0; b < 4 * NJ; ++b) {
-        const floatx4 o =
-            *(const lds_floatx4*)(uintptr_t)(mine + (uint32_t)(((b % NJ) * 16 * kRowPitch + (b / NJ) * 16) * 4));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[b][e] += o[e];
-      }
-    }
-  }
-}
-template <int NJ>
-__device__ __forceinline__ float tile_sum(uint32_t buf, int row, int col) {
-  float v = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w)
-    v += *(const lds_f32*)(uintptr_t)(buf + (uint32_t)(((w * 16 * NJ + col) * kRowPitch + row) * 4));
-  return v;
-}
 
 // ---------------------------------------------------------------------------
 // Row products: 64 rows by 16 NJ columns per workgroup (so that S is read once
@@ -509,152 +436,10 @@ __global__ void __launch_bounds__(kOutThreads) lowrank_out_kernel(OutArgs p, Bes
   }
 }
 
-// ---------------------------------------------------------------------------
-// Column products: 64 columns of S by 16 NJ columns of V per workgroup; the
-// waves take 32 rows of S at a time in turn.
-struct ColProd {
-  Stream s;
-  const float* v;      // V in fragment order
-  float* out;          // element (c, j) at c * oc + j * oj
-  int64_t oc, oj;
-};
-struct ColPair {
-  ColProd a, b;   // a: 8-bit S, b: bf16 S
-  int ta;         // column tiles of a
-  int r, rp;
-};
-
-// Eight floats as three bf16 terms each: every remainder is exact, so the
-// terms' sum is the float to 24 bits. An infinity's remainder is a NaN.
-__device__ __forceinline__ void split3(const floatx4 (&v)[2], u32x4 (&term)[kTerms]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float a = v[e >> 1][(e & 1) * 2], b = v[e >> 1][(e & 1) * 2 + 1];
-#pragma unroll
-    for (int c = 0; c < kTerms; ++c) {
-      const uint32_t w = pack_bf16x2(a, b);
-      term[c][e] = w;
-      a -= __builtin_bit_cast(float, w << 16);
-      b -= __builtin_bit_cast(float, w & 0xffff0000u);
-    }
-  }
-}
-
-template <int kSrc, bool kMask, int NJ>
-__device__ __forceinline__ void column_product(const ColProd& p, int ct, int j0, int r, int rp,
-                                                uint32_t lds, int wave, int lane) {
-#ifdef __HIP_DEVICE_COMPILE__
-  constexpr int NF = 4 * NJ;
-  const int i = lane & 15, g = lane >> 4;
-  const int64_t c0 = (int64_t)ct * 64;
-  const uint32_t tile = lds + (uint32_t)(wave * 32 * kPitch);
-  constexpr int kBytes = kSrc == kBf16 ? 2 : 1;
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc((const uint8_t*)p.s.s + c0 * kBytes, p.s.rows * p.s.ld - c0 * kBytes);
-  const __amdgpu_buffer_rsrc_t rsc = make_rsrc(p.s.scales + (c0 >> 7), p.s.rows * p.s.sld - (c0 >> 7));
-  const int64_t mld = p.s.cols / 32;
-  const __amdgpu_buffer_rsrc_t rm = make_rsrc(p.s.mask + (c0 >> 5), p.s.rows * mld * 4 - (c0 >> 5) * 4);
-  // fragments of one block of 32 rows: rp / 16 of 2 KiB
-  const float* vb = p.v + (int64_t)(j0 >> 4) * 512 + lane * 8;
-  const int64_t vblock = (int64_t)rp * 32;
-
-  floatx4 acc[NF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f) acc[f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  constexpr int kS = kSrc == kBf16 ? 4 : 2;
-  struct Regs {
-    u32x4 s[kS];
-    uint32_t sc[2], keep[2];
-    floatx4 v[NJ][2];
-  };
-  const int steps = (int)((p.s.rows + 31) / 32);
-  // One step's loads: 32 rows of S by 64 columns, and V's fragments.
-  auto load = [&](int st) {
-    Regs q;
-    if constexpr (kSrc == kBf16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        q.s[e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            rs, (int)((st * 32 + e * 8 + (lane >> 3)) * p.s.ld) + (lane & 7) * 16, 0, 0));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int m = st * 32 + e * 16 + (lane >> 2), ch = lane & 3;
-        q.s[e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            rs, (int)(m * p.s.ld) + ch * 16, 0, 0));
-        q.sc[e] = __builtin_amdgcn_raw_buffer_load_b8(rsc, (int)(m * p.s.sld), 0, 0);
-        if constexpr (kMask)
-          q.keep[e] = __builtin_amdgcn_raw_buffer_load_b32(rm, (int)(m * mld * 4) + (ch >> 1) * 4, 0, 0);
-      }
-    }
-    const float* v = vb + st * vblock;
-#pragma unroll
-    for (int jt = 0; jt < NJ; ++jt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) q.v[jt][h] = *reinterpret_cast<const floatx4*>(v + jt * 512 + h * 4);
-    return q;
-  };
-  for (int st = wave; st < steps; st += kWaves) {
-    const Regs q = load(st);
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (kSrc == kBf16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *(lds_u32x4*)(uintptr_t)(tile + (uint32_t)((e * 8 + (lane >> 3)) * kPitch + (lane & 7) * 16)) = q.s[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = e * 16 + (lane >> 2), ch = lane & 3;
-        const float sc = act8_scale((int)q.sc[e]);
-        u32x4 lo = act8_decode8<kSrc>(u32x2{q.s[e][0], q.s[e][1]}, sc);
-        u32x4 hi = act8_decode8<kSrc>(u32x2{q.s[e][2], q.s[e][3]}, sc);
-        if constexpr (kMask) {
-          const uint32_t bits = q.keep[e] >> ((ch & 1) * 16);
-          lo &= keep_mask8(bits);
-          hi &= keep_mask8(bits >> 8);
-        }
-        *(lds_u32x4*)(uintptr_t)(tile + (uint32_t)(row * kPitch + ch * 32)) = lo;
-        *(lds_u32x4*)(uintptr_t)(tile + (uint32_t)(row * kPitch + ch * 32 + 16)) = hi;
-      }
-    }
-    bf16x8 x[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) x[f] = tr_frag<kPitch>(tile, 8 * g, f * 16, lane);
-#pragma unroll
-    for (int jt = 0; jt < NJ; ++jt) {
-      u32x4 term[kTerms];
-      split3(q.v[jt], term);
-#pragma unroll
-      for (int c = kTerms - 1; c >= 0; --c)  // smallest terms first
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-          acc[f * NJ + jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[f], as_bf16x8(term[c]),
-                                                                     acc[f * NJ + jt], 0, 0, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  reduce_waves<NJ>(acc, lds, wave, lane);
-  // dA's rows run along j, dB's along the columns of S
-#pragma unroll
-  for (int q = 0; q < 2 * NJ; ++q) {
-    const int o = q * kThreads + threadIdx.x;
-    const int j = kSrc == kBf16 ? o / 64 : o % (16 * NJ), c = kSrc == kBf16 ? o % 64 : o / (16 * NJ);
-    const float v = tile_sum<NJ>(lds, c, j);
-    if (j0 + j < r) p.out[(c0 + c) * p.oc + (j0 + j) * p.oj] = v;
-  }
-#endif
-}
-
-template <int kSrc, bool kMask, int NJ>
+template <int kSrc, int NJ>
 __global__ void __launch_bounds__(kThreads) column_products_kernel(ColPair p) {
-  constexpr int kRed = tile_bytes(NJ), kTiles = kWaves * 32 * kPitch;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kTiles > kRed ? kTiles : kRed];
-  const uint32_t lds = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.x, j0 = blockIdx.y * 64;
-  if (b < p.ta) column_product<kSrc, kMask, NJ>(p.a, b, j0, p.r, p.rp, lds, wave, lane);
-  else column_product<kBf16, false, NJ>(p.b, b - p.ta, j0, p.r, p.rp, lds, wave, lane);
+  __shared__ __attribute__((aligned(16))) uint8_t smem[column_lds(NJ)];
+  column_job<kSrc, NJ>(p, blockIdx.x, (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem));
 }
 
 }  // namespace lr8
@@ -671,14 +456,6 @@ int row_splits(int64_t M, int64_t C, int r) {
   const int64_t tiles = ceil_div(M, 64) * ceil_div(r, 64), steps = ceil_div(C, 64);
   const int64_t s = std::max<int64_t>(1, std::min(256 / tiles, steps / kWaves));
   return (int)ceil_div(steps, ceil_div(steps, s));
-}
-
-template <class F>
-hipError_t by_nj(int r, F&& f) {
-  using std::integral_constant;
-  if (r <= 16) return f(integral_constant<int, 1>{});
-  if (r <= 32) return f(integral_constant<int, 2>{});
-  return f(integral_constant<int, 4>{});
 }
 
 template <int kSrc, bool kMask, bool kTrans>
@@ -707,8 +484,8 @@ RowProd row_args(Stream s, const uint16_t* w, int r, int per, float* part, int* 
   return p;
 }
 
-Stream act8_stream(ConstAct8 x, int64_t M, int64_t K, const uint32_t* mask) {
-  return Stream{x.codes, x.scales, act8_row_bytes(K), act8_scale_row_bytes(K), M, K, mask};
+Stream act8_stream(ConstAct8 x, int fmt, int64_t M, int64_t K, const uint32_t* mask) {
+  return Stream{x.codes, x.scales, act8_row_bytes(K), act8_scale_row_bytes(K), M, K, mask, fmt};
 }
 
 }  // namespace
@@ -719,14 +496,14 @@ hipError_t launch_rows_act8(ConstAct8 x, int fmt, int64_t M, int64_t K, const ui
                             const uint16_t* A, int r, float* part, int* splits, hipStream_t stream) {
   // where the 8-bit product for few tokens may form T itself, its order
   const int per = few_t_shape(M, K, r) ? 2 * (int)ceil_div(act8_row_bytes(K) / kAct8Block, kFewWaves) : 0;
-  const RowProd p = row_args(act8_stream(x, M, K, mask), A, r, per, part, splits);
+  const RowProd p = row_args(act8_stream(x, fmt, M, K, mask), A, r, per, part, splits);
   if (mask) return fmt ? run_rows<kE5M2, true, true>(p, *splits, stream) : run_rows<kE4M3, true, true>(p, *splits, stream);
   return fmt ? run_rows<kE5M2, false, true>(p, *splits, stream) : run_rows<kE4M3, false, true>(p, *splits, stream);
 }
 
 hipError_t launch_rows_bf16(const uint16_t* S, int64_t M, int64_t C, const uint16_t* B, int r,
                             float* part, int* splits, hipStream_t stream) {
-  const RowProd p = row_args(Stream{S, nullptr, C * 2, 0, M, C, nullptr}, B, r, 0, part, splits);
+  const RowProd p = row_args(Stream{S, nullptr, C * 2, 0, M, C, nullptr, 0}, B, r, 0, part, splits);
   return run_rows<kBf16, false, false>(p, *splits, stream);
 }
 
@@ -773,24 +550,25 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
   return beside.w ? go(lowrank_out_kernel<kDecode>) : go(lowrank_out_kernel<kNothing>);
 }
 
-hipError_t launch_columns(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY,
-                          const float* g, const float* t, int64_t M, int64_t N, int64_t K,
-                          int r, float* dA, float* dB, hipStream_t stream) {
+lr8::ColPair lr8::column_pair(ConstAct8 x, int fmt, const uint32_t* mask, const uint16_t* dY, const float* g,
+                              const float* t, int64_t M, int64_t N, int64_t K, int r, float* dA, float* dB) {
   ColPair p{};
-  p.a = ColProd{act8_stream(x, M, K, mask), g, dA, (int64_t)r, 1};
-  p.b = ColProd{Stream{dY, nullptr, N * 2, 0, M, N, nullptr}, t, dB, 1, N};
+  p.a = ColProd{act8_stream(x, fmt, M, K, mask), g, dA, (int64_t)r, 1};
+  p.b = ColProd{Stream{dY, nullptr, N * 2, 0, M, N, nullptr, 0}, t, dB, 1, N};
   p.ta = (int)(K / 64);
+  p.tiles = (int)(K / 64 + N / 64);
+  p.jobs = p.tiles * (int)ceil_div(r, 64);
   p.r = r;
   p.rp = lowrank_cols(r);
-  const dim3 grid((unsigned)(K / 64 + N / 64), (unsigned)ceil_div(r, 64)), block(kThreads);
-  return by_nj(r, [&](auto nj) {
+  return p;
+}
+
+hipError_t launch_columns(const ColPair& p, hipStream_t stream) {
+  return by_nj(p.r, [&](auto nj) {
     constexpr int NJ = decltype(nj)::value;
-    auto go = [&](auto kern) {
-      hipLaunchKernelGGL(kern, grid, block, 0, stream, p);
-      return hipGetLastError();
-    };
-    if (mask) return fmt ? go(column_products_kernel<kE5M2, true, NJ>) : go(column_products_kernel<kE4M3, true, NJ>);
-    return fmt ? go(column_products_kernel<kE5M2, false, NJ>) : go(column_products_kernel<kE4M3, false, NJ>);
+    hipLaunchKernelGGL((p.a.s.fmt ? column_products_kernel<kE5M2, NJ> : column_products_kernel<kE4M3, NJ>),
+                       dim3((unsigned)p.jobs), dim3(kThreads), 0, stream, p);
+    return hipGetLastError();
   });
 }
 
