@@ -140,9 +140,9 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   const int wn = wave & 1, wm = wave >> 1;
   const int r = lane & 31, half = lane >> 5;
 
-  // this set's steps: [first, first + KB), whole scale dwords; every set
-  // walks KB steps, and those past the end of K read zeros
-  const int KB = kGroups == 1 ? p.KB : ((p.KB + kGroups - 1) / kGroups + 3) / 4 * 4;
+  // this set's steps: [first, first + KB); every set walks KB steps, and those
+  // past the end of K read zeros
+  const int KB = (p.KB + kGroups - 1) / kGroups;
   const int first = group * KB, valid = p.KB - first;
   // The low-rank term comes first, through the same ring: a step of it is 64
   // columns of V and U, 128 bytes of a row as in the steps along K.
@@ -184,17 +184,29 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
           16, s.vx[(i - kLoadW) & 1], off + ((i - kLoadW) >> 1) * s.step16, 0, 0);
   };
 
-  // scale bytes, a dword for four steps; the low byte is the present step's
+  // scale bytes, a dword for four steps; the low byte is the present step's. A
+  // set that begins inside a dword takes four steps' bytes from two of them.
   const __amdgpu_buffer_rsrc_t rsw = make_rsrc(p.ws, (p.N + 127) / 128 * p.sb);
   const __amdgpu_buffer_rsrc_t rsx = make_rsrc(p.xs + m0 * p.sb, (p.M - m0) * p.sb);
   struct Scales { uint32_t w, x[BM]; };
   auto scales = [&](int kb) {
     Scales s{};
     if constexpr (kFmt == kBf16) return s;
-    s.w = __builtin_amdgcn_raw_buffer_load_b32(rsw, (int)((n0 + wn * WN) / 128) * p.sb, first + kb, 0);
+    const int at = (kGroups == 1 ? 0 : first & ~3) + kb;
+    s.w = __builtin_amdgcn_raw_buffer_load_b32(rsw, (int)((n0 + wn * WN) / 128) * p.sb, at, 0);
 #pragma unroll
     for (int j = 0; j < BM; ++j)
-      s.x[j] = __builtin_amdgcn_raw_buffer_load_b32(rsx, (wm * WM + j * 32 + r) * p.sb, first + kb, 0);
+      s.x[j] = __builtin_amdgcn_raw_buffer_load_b32(rsx, (wm * WM + j * 32 + r) * p.sb, at, 0);
+    return s;
+  };
+  auto four = [&](const Scales& lo, const Scales& hi) {
+    Scales s = lo;
+    if constexpr (kGroups > 1) {
+      const uint32_t by = (uint32_t)(first & 3) * 8;
+      s.w = __builtin_amdgcn_alignbit(hi.w, lo.w, by);
+#pragma unroll
+      for (int j = 0; j < BM; ++j) s.x[j] = __builtin_amdgcn_alignbit(hi.x[j], lo.x[j], by);
+    }
     return s;
   };
 
@@ -214,7 +226,8 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   };
 #pragma unroll
   for (int k = 0; k < kStages; ++k) issue(k, lds0 + (uint32_t)(k * kStage));
-  Scales s = scales(0);
+  Scales s, dw0 = scales(0), dw1{};
+  if constexpr (kGroups > 1) dw1 = scales(4);
 
   floatx16 acc[BN][BM];
 #pragma unroll
@@ -317,7 +330,8 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
     }
   }
   for (int kb4 = 0; kb4 < KB; kb4 += 4) {
-    const Scales ahead = scales(kb4 + 4);
+    const Scales ahead = scales(kb4 + (kGroups > 1 ? 8 : 4));
+    s = four(dw0, dw1);
     const int end = min(kb4 + 4, KB);
     for (int kb = kb4; kb < end; ++kb) {
       step(main_fmt, operands, at_step(kb + kStages));
@@ -325,7 +339,8 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
 #pragma unroll
       for (int j = 0; j < BM; ++j) s.x[j] >>= 8;
     }
-    s = ahead;
+    dw0 = kGroups > 1 ? dw1 : ahead;
+    dw1 = ahead;
   }
   wait_vmcnt<0>();  // no direct load may outlive the workgroup's LDS
 
