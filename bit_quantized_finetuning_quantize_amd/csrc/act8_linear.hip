@@ -35,7 +35,7 @@ namespace {
 // 4096 x 8192 x 8192; dX alone 9.1 us against 3.6 at 16 x 256 x 256).
 struct Ws8 {
   int64_t r64;
-  size_t v, u, g, t, part, dy8, dys, wt, total;
+  size_t v, u, g, t, part, done, dy8, dys, wt, total;
 };
 
 // Byte offsets in the workspace, 256-aligned. Each part grows with every
@@ -53,6 +53,7 @@ Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
   w.t = take(w.r64 * Mp * 4);
   // splits * M * columns: 256 tiles of 64 x 64 at most, or one split
   w.part = take(r ? std::max<int64_t>(256 * 64 * 64, Mp * w.r64) * 4 : 0);
+  w.done = take(r ? kTileSums * 4 : 0);
   w.dy8 = take(M * act8_row_bytes(N));
   w.dys = take(M * act8_scale_row_bytes(N));
   // the NF4 backward's decoded weight, in the place of the 8-bit dY
@@ -67,13 +68,16 @@ struct Ptrs {
   float *g, *t, *part;
   uint8_t *dy8, *dys;
   uint16_t* wt;
+  TileSums sums;
 };
 Ptrs carve(void* ws_, const Ws8& w) {
   char* ws = reinterpret_cast<char*>(ws_);
   auto at = [&](size_t o) { return reinterpret_cast<uint16_t*>(ws + o); };
   auto atf = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   return Ptrs{at(w.v), at(w.u), atf(w.g), atf(w.t), atf(w.part),
-              reinterpret_cast<uint8_t*>(ws + w.dy8), reinterpret_cast<uint8_t*>(ws + w.dys), at(w.wt)};
+              reinterpret_cast<uint8_t*>(ws + w.dy8), reinterpret_cast<uint8_t*>(ws + w.dys), at(w.wt),
+              // the partials' place serves the product's tiles after them
+              TileSums{reinterpret_cast<uint32_t*>(ws + w.done), atf(w.part)}};
 }
 
 // The adapter's rows serve as they are when they are whole 64-column tiles.
@@ -99,14 +103,14 @@ hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, c
   if (!T) {  // recomputed from the 8-bit input
     QLORA_TRY(launch_rows_act8(x, fmt, M, K, dr.mask, A, r, w.part, &splits, stream));
     const LowrankOut t{w.part, nullptr, nullptr, 0, splits, ldp, f, nullptr, nullptr, w.t};
-    QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{}, M, r, scale, stream));
+    QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{}, M, r, scale, nullptr, stream));
   }
   const bool here = factor_in_place(N, r);
   if (!here) QLORA_TRY(launch_rows_bf16(dY, M, N, B, r, w.part, &splits, stream));
   const LowrankOut o[2] = {{here ? nullptr : w.part, here ? dY : nullptr, B, N, splits, ldp, f, nullptr, w.u, w.g},
                            {T, nullptr, nullptr, 0, 1, r, 1.0f, nullptr, nullptr, w.t}};
   const LowrankPad pad = in_place(A, r) ? LowrankPad{} : LowrankPad{A, false, K, w.v};
-  return launch_lowrank_out(o, T ? 2 : 1, pad, M, r, scale, stream, beside);
+  return launch_lowrank_out(o, T ? 2 : 1, pad, M, r, scale, w.sums.done, stream, beside);
 }
 
 }  // namespace
@@ -126,7 +130,7 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
   QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, dr, beside, stream));
   const lr8::ColPair cols = lr8::column_pair(x, fmt, dr.mask, dY, w.g, w.t, M, N, K, r, dA, dB);
   return dX ? launch_bf16_gemm(dY, w.wt, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dr.mask, dX,
-                               &cols, stream)
+                               w.sums, &cols, stream)
             : launch_columns(cols, stream);
 }
 
@@ -138,7 +142,7 @@ hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A,
   const bool few = fp8_few(M, N);
   if (!r)
     return few ? launch_fp8_few(x, fmt, w8, M, N, K, nullptr, nullptr, 0, nullptr, 0, scale, Y, nullptr, stream)
-               : launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, nullptr, stream);
+               : launch_fp8_gemm(x, fmt, w8, M, N, K, nullptr, nullptr, 0, Y, TileSums{}, nullptr, stream);
   if (few && fp8_few_forms_t(A, M, K, r))
     return launch_fp8_few(x, fmt, w8, M, N, K, A, nullptr, 0, B, r, scale, Y, T_out, stream);
   int splits = 0;
@@ -146,8 +150,8 @@ hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A,
   if (few)
     return launch_fp8_few(x, fmt, w8, M, N, K, nullptr, w.part, splits, B, r, scale, Y, T_out, stream);
   const LowrankOut t{w.part, nullptr, nullptr, 0, splits, lowrank_cols(r), 1.0f, T_out, w.u, nullptr};
-  QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{B, true, N, w.v}, M, r, scale, stream));
-  return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, nullptr, stream);
+  QLORA_TRY(launch_lowrank_out(&t, 1, LowrankPad{B, true, N, w.v}, M, r, scale, w.sums.done, stream));
+  return launch_fp8_gemm(x, fmt, w8, M, N, K, w.u, w.v, (int)l.r64, Y, w.sums, nullptr, stream);
 }
 
 hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, const float* T,
@@ -159,14 +163,14 @@ hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, c
   const ConstAct8 dy8{w.dy8, w.dys};
   if (!r) {
     QLORA_TRY(launch_act8_quantize(dY, M, N, N, dyfmt, w.dy8, w.dys, stream));
-    return launch_fp8_gemm(dy8, dyfmt, w8t, M, K, N, nullptr, nullptr, 0, dX, nullptr, stream);
+    return launch_fp8_gemm(dy8, dyfmt, w8t, M, K, N, nullptr, nullptr, 0, dX, TileSums{}, nullptr, stream);
   }
   LowrankBeside beside;
   if (dX) beside.s = dY, beside.C = N, beside.fmt = dyfmt, beside.codes = w.dy8, beside.scales = w.dys;
   QLORA_TRY(bwd_front(dY, x, fmt, T, A, B, M, N, K, r, scale, w, Dropout{}, beside, stream));
   const lr8::ColPair cols = lr8::column_pair(x, fmt, nullptr, dY, w.g, w.t, M, N, K, r, dA, dB);
-  return dX ? launch_fp8_gemm(dy8, dyfmt, w8t, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dX, &cols,
-                              stream)
+  return dX ? launch_fp8_gemm(dy8, dyfmt, w8t, M, K, N, w.u, in_place(A, r) ? A : w.v, (int)l.r64, dX,
+                              w.sums, &cols, stream)
             : launch_columns(cols, stream);
 }
 

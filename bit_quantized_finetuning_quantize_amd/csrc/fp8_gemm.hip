@@ -35,6 +35,7 @@ namespace fp8 {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) float lds_f32;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
 
 struct Fp8Gemm {
   const uint8_t *x, *xs, *w, *ws;
@@ -47,6 +48,11 @@ struct Fp8Gemm {
   bool stream;         // Y is stored past the caches
   int nM, nN, group;   // tiles, and row tiles per group of the walk
   int full, cut;       // 256 x 256 tiles done whole; parts of each other one
+  // Small tiles: workgroups that share a tile, a run of K each; their counts
+  // of workgroups done (0 before) and sums, 4096 floats a workgroup.
+  int splits;
+  uint32_t* done;
+  float* sums;
 };
 
 // 128-byte LDS rows, the 16-byte piece c of row r at position c ^ swz(r).
@@ -110,6 +116,54 @@ constexpr int lds_bytes(int TN, int TM, int stages, int groups) {
   return ring > out ? ring : out;
 }
 
+// The sum of a tile's splits. Every workgroup stores its sums and counts itself;
+// the last one to do so adds them all, in the order of the splits, whichever it
+// is, and is the one to go on (true). No workgroup waits for another. They may
+// sit on different XCDs, whose L2s are separate: the sc1 bit makes a store
+// write through to memory and a load pass over the L2.
+__device__ __forceinline__ bool join_splits(floatx16& acc, const Fp8Gemm& p, int tile, int split, uint32_t lds) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kSc1 = 16, kBytes = 64 * 64 * 4;
+  const __amdgpu_buffer_rsrc_t at = make_rsrc(p.sums + (int64_t)tile * p.splits * 4096, p.splits * kBytes);
+  const int v = (int)threadIdx.x * 16;  // 256 threads
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const floatx4 o{acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]};
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), at, v, split * kBytes + e * 4096, kSc1);
+  }
+  // every store of the workgroup acknowledged before it counts itself
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  lds_u32* word = (lds_u32*)(uintptr_t)lds;
+  if (threadIdx.x == 0)
+    *word = __hip_atomic_fetch_add(p.done + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const bool last = __builtin_amdgcn_readfirstlane((int)*word) == p.splits - 1;
+  __syncthreads();
+  if (!last) return false;
+  asm volatile("" ::: "memory");
+  floatx16 sum;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+  constexpr int kU = 4;  // splits in flight; past the last they read zeros
+  for (int s0 = 0; s0 < p.splits; s0 += kU) {
+    floatx4 o[kU][4];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[u][e] = __builtin_bit_cast(
+            floatx4, __builtin_amdgcn_raw_buffer_load_b128(at, v, (s0 + u) * kBytes + e * 4096, kSc1));
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i] += o[u][i >> 2][i & 3];
+  }
+  acc = sum;
+#endif
+  return true;
+}
+
 // Tile of TN weight rows by TM activation rows, 2 x 2 waves, each a
 // (TN / 2) x (TM / 2) part of it in 32 x 32 accumulators.
 //
@@ -126,8 +180,12 @@ constexpr int lds_bytes(int TN, int TM, int stages, int groups) {
 // a ring of its own, that take a run of the steps each; the sums of the other
 // sets are added to the first's in order at the end. For grids that leave
 // compute units idle: a step's latency then covers kGroups blocks along K.
-template <int TN, int TM, int kStages, int kGroups, int kFmt>
-__device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t m0, uint32_t lds_all) {
+//
+// With kJoin, `split` is this workgroup's run of K in the tile `tile` that
+// p.splits of them share: see join_splits.
+template <int TN, int TM, int kStages, int kGroups, int kFmt, bool kJoin = false>
+__device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t m0, uint32_t lds_all,
+                                          int tile = 0, int split = 0) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the kernels' stubs alone
   constexpr int WN = TN / 2, WM = TM / 2;
   constexpr int BN = WN / 32, BM = WM / 32;
@@ -142,11 +200,12 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
 
   // this set's steps: [first, first + KB); every set walks KB steps, and those
   // past the end of K read zeros
-  const int KB = (p.KB + kGroups - 1) / kGroups;
-  const int first = group * KB, valid = p.KB - first;
+  const int run = kJoin ? (p.KB + p.splits - 1) / p.splits : p.KB, start = split * run;
+  const int KB = (run + kGroups - 1) / kGroups;
+  const int first = start + group * KB, valid = min(p.KB, start + run) - first;
   // The low-rank term comes first, through the same ring: a step of it is 64
   // columns of V and U, 128 bytes of a row as in the steps along K.
-  const int LR = p.U ? p.r64 / 64 : 0;
+  const int LR = p.U && split == 0 ? p.r64 / 64 : 0;
 
   // operand moves: 8 rows of 128 bytes per instruction. The swizzle of rows 16
   // apart is the same: one lane offset serves every second instruction.
@@ -184,6 +243,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
           16, s.vx[(i - kLoadW) & 1], off + ((i - kLoadW) >> 1) * s.step16, 0, 0);
   };
 
+  constexpr bool kRuns = kGroups > 1 || kJoin;  // steps may begin anywhere
   // scale bytes, a dword for four steps; the low byte is the present step's. A
   // set that begins inside a dword takes four steps' bytes from two of them.
   const __amdgpu_buffer_rsrc_t rsw = make_rsrc(p.ws, (p.N + 127) / 128 * p.sb);
@@ -192,7 +252,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   auto scales = [&](int kb) {
     Scales s{};
     if constexpr (kFmt == kBf16) return s;
-    const int at = (kGroups == 1 ? 0 : first & ~3) + kb;
+    const int at = (kRuns ? first & ~3 : 0) + kb;
     s.w = __builtin_amdgcn_raw_buffer_load_b32(rsw, (int)((n0 + wn * WN) / 128) * p.sb, at, 0);
 #pragma unroll
     for (int j = 0; j < BM; ++j)
@@ -201,7 +261,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   };
   auto four = [&](const Scales& lo, const Scales& hi) {
     Scales s = lo;
-    if constexpr (kGroups > 1) {
+    if constexpr (kRuns) {
       const uint32_t by = (uint32_t)(first & 3) * 8;
       s.w = __builtin_amdgcn_alignbit(hi.w, lo.w, by);
 #pragma unroll
@@ -227,7 +287,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
 #pragma unroll
   for (int k = 0; k < kStages; ++k) issue(k, lds0 + (uint32_t)(k * kStage));
   Scales s, dw0 = scales(0), dw1{};
-  if constexpr (kGroups > 1) dw1 = scales(4);
+  if constexpr (kRuns) dw1 = scales(4);
 
   floatx16 acc[BN][BM];
 #pragma unroll
@@ -330,7 +390,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
     }
   }
   for (int kb4 = 0; kb4 < KB; kb4 += 4) {
-    const Scales ahead = scales(kb4 + (kGroups > 1 ? 8 : 4));
+    const Scales ahead = scales(kb4 + (kRuns ? 8 : 4));
     s = four(dw0, dw1);
     const int end = min(kb4 + 4, KB);
     for (int kb = kb4; kb < end; ++kb) {
@@ -339,7 +399,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
 #pragma unroll
       for (int j = 0; j < BM; ++j) s.x[j] >>= 8;
     }
-    dw0 = kGroups > 1 ? dw1 : ahead;
+    dw0 = kRuns ? dw1 : ahead;
     dw1 = ahead;
   }
   wait_vmcnt<0>();  // no direct load may outlive the workgroup's LDS
@@ -362,6 +422,10 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
       }
     }
     if (group != 0) return;
+  }
+  if constexpr (kJoin) {
+    static_assert(BN * BM == 1, "one accumulator");
+    if (p.splits > 1 && !join_splits(acc[0][0], p, tile, split, lds_all)) return;
   }
 
   // Output by way of LDS (the ring is done with): a lane holds four
@@ -442,14 +506,19 @@ template <int TN, int TM, int kStages, int kGroups, int kXFmt, int NJ>
 __global__ void __launch_bounds__(NJ ? lr8::kThreads : 256 * kGroups)
 __attribute__((amdgpu_waves_per_eu(2, kGroups > 2 ? 4 : 2)))
 fp8_gemm_small_kernel(Fp8Gemm p, lr8::ColPair cols) {
-  const int count = p.nM * p.nN;
+  constexpr bool kJoin = TN == 64 && TM == 64;
+  const int tiles = p.nM * p.nN, count = kJoin ? tiles * p.splits : tiles;
   if constexpr (NJ != 0) {
     if ((int)blockIdx.x >= count) return lr8::column_job<lr8::kAct8, NJ>(cols, blockIdx.x - count, lds_base());
     if (kGroups == 1 && threadIdx.x >= 256) return;
   }
-  int tm, tn;
-  tile_at(p, xcd_order(blockIdx.x, count), tm, tn);
-  gemm_tile<TN, TM, kStages, kGroups, kXFmt>(p, (int64_t)tn * TN, (int64_t)tm * TM, lds_base());
+  int tm, tn, tile = xcd_order(blockIdx.x, count), split = 0;
+  if constexpr (kJoin) {  // an XCD's workgroups share runs of K
+    split = tile / tiles;
+    tile -= split * tiles;
+  }
+  tile_at(p, tile, tm, tn);
+  gemm_tile<TN, TM, kStages, kGroups, kXFmt, kJoin>(p, (int64_t)tn * TN, (int64_t)tm * TM, lds_base(), tile, split);
 }
 
 // ---------------------------------------------------------------------------
@@ -690,7 +759,7 @@ hipError_t run_small(Fp8Gemm p, const lr8::ColPair& cols, hipStream_t stream) {
   p.nM = (int)((p.M + TM - 1) / TM);
   p.nN = (int)((p.N + TN - 1) / TN);
   p.group = 4;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(p.nM * p.nN + (NJ ? cols.jobs : 0))),
+  hipLaunchKernelGGL(kern, dim3((unsigned)(p.nM * p.nN * p.splits + (NJ ? cols.jobs : 0))),
                      dim3(NJ ? lr8::kThreads : 256 * kGroups), lds, stream, p, cols);
   return hipGetLastError();
 }
@@ -717,16 +786,25 @@ hipError_t run_few(const Fp8Few& q, hipStream_t stream) {
 // with two sets of waves, in brackets with one: two sets pay from about 16
 // steps on, while every workgroup has a compute unit of its own.
 //
+// Up to 128 tiles of 64 x 64 are shared by several workgroups where each has 24
+// steps or more (us in a graph, so and without): 64 x 4096 x 11008 r = 64 28.6
+// and 37.0, 512 x 1024 x 11008 32.5 and 37.1; with 16 steps 512 x 1024 x 4096
+// takes 22.1 instead of 20.8. Column products in the same launch keep some of
+// the compute units (backward of 32 x 11008 x 4096 30.0 us, 31.5 if they do not
+// and 35.1 without sharing).
+//
 // `cols`: column products to do besides, or null. They share the launch of a
 // grid that leaves compute units idle, else they follow in their own (whole
 // 8-bit backward, us in a graph, so and in two launches: 16 x 256 x 256 r = 8
 // 7.8 and 10.3, 257 x 4096 x 4096 r = 8 26.9 and 30.8, 64 x 4096 x 4096 r = 64
 // 23.6 and 28.3, 512 x 4096 x 4096 r = 64 with its 256 workgroups 36.5 and 37.2).
 template <int kXFmt>
-hipError_t run_fmt(const Fp8Gemm& p, const lr8::ColPair* cols, hipStream_t stream) {
+hipError_t run_fmt(Fp8Gemm p, const lr8::ColPair* cols, hipStream_t stream) {
   const int64_t mt = (p.M + 63) / 64;
   const int64_t t64 = mt * ((p.N + 63) / 64), t128 = mt * ((p.N + 127) / 128);
-  const bool two = p.KB >= 16;
+  const int64_t room = cols ? 160 : 256;  // workgroups
+  p.splits = t64 <= 128 && p.done ? (int)std::max<int64_t>(1, std::min<int64_t>(room / t64, p.KB / 24)) : 1;
+  const bool two = p.KB / p.splits >= (p.splits > 1 ? 8 : 16);
   if (t128 <= 256) {
     auto small = [&](auto nj) {
       constexpr int NJ = decltype(nj)::value;
@@ -765,22 +843,22 @@ Fp8Gemm gemm_args(ConstAct8 x, ConstAct8 w, int64_t M, int64_t N, int64_t K, uin
 }  // namespace
 
 hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
-                           const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
+                           const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y, TileSums sums,
                            const lr8::ColPair* cols, hipStream_t stream) {
   Fp8Gemm p = gemm_args(x, w, M, N, K, Y);
-  p.U = U; p.V = V; p.r64 = r64;
+  p.U = U; p.V = V; p.r64 = r64; p.done = sums.done; p.sums = sums.sums;
   return xfmt ? run_fmt<1>(p, cols, stream) : run_fmt<0>(p, cols, stream);
 }
 
 hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
                             const uint16_t* U, const uint16_t* V, int r64, const uint32_t* keep,
-                            uint16_t* Y, const lr8::ColPair* cols, hipStream_t stream) {
+                            uint16_t* Y, TileSums sums, const lr8::ColPair* cols, hipStream_t stream) {
   Fp8Gemm p{};
   p.x = reinterpret_cast<const uint8_t*>(x);
   p.w = reinterpret_cast<const uint8_t*>(w);
   p.M = M; p.N = N; p.ldc = K * 2;
   p.KB = (int)(K / 64);
-  p.U = U; p.V = V; p.r64 = r64; p.keep = keep; p.Y = Y;
+  p.U = U; p.V = V; p.r64 = r64; p.keep = keep; p.Y = Y; p.done = sums.done; p.sums = sums.sums;
   p.stream = streams_out(M, N, p.ldc);
   return run_fmt<kBf16>(p, cols, stream);
 }

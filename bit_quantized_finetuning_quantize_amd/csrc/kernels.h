@@ -127,18 +127,26 @@ namespace lr8 {
 struct ColPair;
 }
 
+// Memory for tiles that several workgroups share: kTileSums counts, 0 before,
+// and 64 * 64 floats for each of at most kTileSums workgroups; or nulls.
+constexpr int kTileSums = 256;
+struct TileSums {
+  uint32_t* done = nullptr;
+  float* sums = nullptr;
+};
+
 // Y [M x N] = dec(x) dec(w)^T + U V^T; x [M x K], w [N x K] in 128 x 128
 // blocks (E4M3), U bf16 [M x r64] and V bf16 [N x r64] or null; and the column
 // products `cols` (or null).
 hipError_t launch_fp8_gemm(ConstAct8 x, int xfmt, ConstAct8 w, int64_t M, int64_t N, int64_t K,
-                           const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y,
+                           const uint16_t* U, const uint16_t* V, int r64, uint16_t* Y, TileSums sums,
                            const lr8::ColPair* cols, hipStream_t stream);
 
 // The same for bf16 x [M x K] and w [N x K], K a multiple of 64, with a keep
 // mask [M][N / 32] over the U V^T term (or null).
 hipError_t launch_bf16_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
                             const uint16_t* U, const uint16_t* V, int r64, const uint32_t* keep,
-                            uint16_t* Y, const lr8::ColPair* cols, hipStream_t stream);
+                            uint16_t* Y, TileSums sums, const lr8::ColPair* cols, hipStream_t stream);
 
 // The same product where its output is small (fp8_few), the adapter's term
 // from split partials of T (launch_rows_act8; null without an adapter) or, where
@@ -197,8 +205,9 @@ struct LowrankBeside {
   int64_t N = 0, K = 0;
   uint16_t* w = nullptr;
 };
+// `done`: the counts of a TileSums, set to 0 (or null).
 hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_t M, int r, float s,
-                              hipStream_t stream, const LowrankBeside& beside = LowrankBeside{});
+                              uint32_t* done, hipStream_t stream, const LowrankBeside& beside = LowrankBeside{});
 // dA = D(dec x)^T g, dB = t^T dY, g and t as launch_lowrank_out's vf (lowrank8.h).
 hipError_t launch_columns(const lr8::ColPair& p, hipStream_t stream);
 

@@ -398,6 +398,7 @@ struct OutArgs {
   float s;
   int cols;                      // column tiles of the jobs
   int blocks0, blocks1, blocks;  // workgroups of the first out job, of both, of all jobs
+  uint32_t* done;                // kTileSums words to clear, or null
 };
 // What the same launch does beside the jobs: an 8-bit copy of S, or a weight
 // to bf16 (decode_t). Both are what the launch after this one reads.
@@ -420,6 +421,8 @@ __global__ void __launch_bounds__(kOutThreads) lowrank_out_kernel(OutArgs p, Bes
   __shared__ __attribute__((aligned(16))) uint8_t smem[kBeside == kDecode && kDecodeLds > kTile ? kDecodeLds : kTile];
   auto tile = reinterpret_cast<float(*)[65]>(smem);
   const int id = blockIdx.x;
+  static_assert(kTileSums == kOutThreads, "a word per thread");
+  if (id == 0 && p.done) p.done[threadIdx.x] = 0;
   if (id < p.blocks) {
     const int b = id / p.cols, jc = id % p.cols;
     if (b < p.blocks0) out_tile(p.o[0], b, jc, p.M, p.Mp, p.r, p.r64, p.rp, p.s, tile);
@@ -508,8 +511,9 @@ hipError_t launch_rows_bf16(const uint16_t* S, int64_t M, int64_t C, const uint1
 }
 
 hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_t M, int r, float s,
-                              hipStream_t stream, const LowrankBeside& beside) {
+                              uint32_t* done, hipStream_t stream, const LowrankBeside& beside) {
   OutArgs p{};
+  p.done = done;
   p.M = M;
   p.Mp = ceil_div(M, 64) * 64;
   p.r = r;

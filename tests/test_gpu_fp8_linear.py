@@ -232,6 +232,43 @@ def test_nf4_backward(q, M, N, K, r, drop, store_type):
     _check(_f64(b3), c.s * ((D @ c.a).T @ c.dy), tol, "dB, T recomputed")
 
 
+@pytest.mark.parametrize("M,N,K,r,fmt", [(100, 1280, 6400, 64, 0), (16, 12544, 64, 8, 1), (70, 6272, 128, 100, 0),
+                                         (33, 3136, 6272, 16, 1)])
+def test_shared_tiles(q, M, N, K, r, fmt):
+    """Products along a long axis, whose tiles several workgroups share: the
+    formula, and the same bits in every call, on either base."""
+    print(f"[case] shared tiles M={M} N={N} K={K} r={r} fmt={fmt}", flush=True)
+    c = Case(q, M, N, K, r, fmt)
+    W = q.qlora_fp8_weight_quantize(c.W)
+    Y, T = q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s)
+    _fwd_check(c, W, Y, T, N, K, r)
+    dX, dA, dB = q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, c.A, c.B, c.s, fmt=fmt)
+    G, gabs = _grad_check(c, c.X, T, dA, dB, M, N, r)
+    w = _dec(W.codes_t, W.scales_t, N, 0, 128)
+    d = act8.dequantize(*act8.quantize(c.dy, fmt), N, fmt)
+    low, ltol = _low(c, G, gabs, N, r)
+    want = d @ w.T + low
+    _check(_f64(dX), want, _steps8(N) * (np.abs(d) @ np.abs(w).T) + ltol
+           + 2.0 ** -8 * 1.01 * np.abs(want), "dX")
+    # the NF4 layer, with dropout
+    st = q.qlora_nf4_quantize(c.W)
+    mask = q.qlora_dropout_mask(M, K, 0.1, seed=5, device=device())
+    keep = oracle.unpack_keep(mask.cpu().numpy().view(np.uint32), K).astype(np.float64)
+    f = oracle.keep_scale(0.1)
+    kw = dict(keep_mask=mask, p=0.1)
+    nX, nA, nB = q.qlora_linear_bwd_act8(c.dY, c.x8, T, st, c.A, c.B, c.s, **kw)
+    w = _f64(q.qlora_nf4_dequantize_bf16(st)).reshape(N, K)
+    want = c.dy @ w + low * keep * f
+    _check(_f64(nX), want, _steps(N) * (np.abs(c.dy) @ np.abs(w)) + ltol * f
+           + 2.0 ** -8 * 1.01 * np.abs(want), "NF4 dX")
+    for _ in range(5):
+        assert torch.equal(q.qlora_fp8_linear_fwd(c.x8, W, c.A, c.B, c.s)[0], Y)
+        again = q.qlora_fp8_linear_bwd(c.dY, c.x8, T, W, c.A, c.B, c.s, fmt=fmt)
+        assert all(torch.equal(a, b) for a, b in zip(again, (dX, dA, dB)))
+        again = q.qlora_linear_bwd_act8(c.dY, c.x8, T, st, c.A, c.B, c.s, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(again, (nX, nA, nB)))
+
+
 def test_gradients_by_differences(q):
     """dA, dB and dX of the 8-bit layer against differences of its forward's
     loss <dY, Y>, evaluated in float64 on the decoded matrices: the loss is
