@@ -828,7 +828,7 @@ hipError_t run_fmt(Fp8Gemm p, const lr8::ColPair* cols, hipStream_t stream) {
   const int64_t t64 = mt * ((p.N + 63) / 64), t128 = mt * ((p.N + 127) / 128);
   const int64_t room = cols ? 160 : 256;  // workgroups
   p.splits = t64 <= 128 && p.done ? (int)std::max<int64_t>(1, std::min<int64_t>(room / t64, p.KB / 24)) : 1;
-  const bool two = p.KB / p.splits >= (p.splits > 1 ? 8 : 16);
+  const bool two = p.KB / p.splits >= 16;
   if (t128 <= 256) {
     auto small = [&](auto nj) {
       constexpr int NJ = decltype(nj)::value;
