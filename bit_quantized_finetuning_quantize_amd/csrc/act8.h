@@ -19,6 +19,13 @@ __host__ __device__ constexpr int64_t act8_scale_row_bytes(int64_t K) {
   return ((K + kAct8Block - 1) / kAct8Block + 3) / 4 * 4;
 }
 
+// An offset past every range that the products read through a buffer descriptor
+// (a tile of 256 rows, or an adapter matrix of 256): a load there gives zeros. A
+// tile's row offset, up to 48 rows, may come on top and leaves it in 31 bits.
+constexpr int kPastEnd = 0x70000000;
+constexpr int64_t kMaxRowBytes = (int64_t)2 << 21;  // bf16, the longest row the calls take
+static_assert(kPastEnd >= 256 * kMaxRowBytes && kPastEnd + 48 * kMaxRowBytes <= 0x7fffffff, "past every tile, 31 bits");
+
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 

@@ -230,7 +230,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   };
   const Source operands = source(p.w, p.x, p.ldc);
   // byte offset of a step in its rows; past the end out of range
-  auto at_step = [&](int kb) { return kb < min(KB, valid) ? (first + kb) * 128 : 0x7f000000; };
+  auto at_step = [&](int kb) { return kb < min(KB, valid) ? (first + kb) * 128 : kPastEnd; };
   // move i of a step: weight rows first, then activation rows
   auto move = [&](const Source& s, int off, uint32_t st, int i) {
     if (i < kLoadW)
@@ -274,7 +274,7 @@ __device__ __forceinline__ void gemm_tile(const Fp8Gemm& p, int64_t n0, int64_t 
   // the end it reads nothing, and its stage is not used.
   const Source lowrank = source(reinterpret_cast<const uint8_t*>(p.V), reinterpret_cast<const uint8_t*>(p.U),
                                 (int64_t)p.r64 * 2);
-  auto at_lowrank = [&](int q) { return group == 0 ? q * 128 : 0x7f000000; };
+  auto at_lowrank = [&](int q) { return group == 0 ? q * 128 : kPastEnd; };
   auto issue = [&](int q, uint32_t st) {  // step q of the low-rank steps and those along K
     if (q < LR) {
 #pragma unroll
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
     for (int u = 0; u < kU; ++u) {
       // past the wave's run every offset is out of range: zeros
       const bool in = kb + u < end;
-      const int off = in ? (kb + u) * 128 : 0x7f000000;
+      const int off = in ? (kb + u) * 128 : kPastEnd;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Few q) {
 #pragma unroll
       for (int e = 0; e < kA; ++e)
         av[u][e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            ra, (e * 64 + lane) * 16, in ? (kb + u) * (128 * kR * 2) : 0x7f000000, 0));
+            ra, (e * 64 + lane) * 16, in ? (kb + u) * (128 * kR * 2) : kPastEnd, 0));
     }
     // every load is on its way before the first product waits
     __builtin_amdgcn_sched_barrier(0);

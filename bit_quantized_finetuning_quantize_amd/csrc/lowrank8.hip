@@ -116,14 +116,14 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
           const int id = e * 64 + lane, row = id / (2 * NJ), ch = id % (2 * NJ);
           const bool ok = j0 + ch * 8 < p.r;  // r is a multiple of 8 here
           q.w[e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-              rw, ok ? (row * p.r + j0 + ch * 8) * 2 : 0x7ffffff0, st * 64 * p.r * 2, 0));
+              rw, ok ? (row * p.r + j0 + ch * 8) * 2 : kPastEnd, st * 64 * p.r * 2, 0));
         }
       }
     } else {
 #pragma unroll
       for (int jt = 0; jt < NJ; ++jt) {
         const int j = j0 + jt * 16 + i;
-        const int off = j < p.r ? (int)(j * p.s.cols * 2) + g * 32 : 0x7ffffff0;
+        const int off = j < p.r ? (int)(j * p.s.cols * 2) + g * 32 : kPastEnd;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           q.w[jt * 2 + h] = __builtin_bit_cast(
@@ -231,14 +231,14 @@ __device__ __forceinline__ void out_product(const OutJob& jb, int64_t mt, int jc
   const int64_t first = mt * kOutRows;
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(jb.sm + first * jb.C, min(M - first, (int64_t)kOutRows) * jb.C * 2);
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(jb.w, r * jb.C * 2);
-  const int so = (int)(i * jb.C * 2) + g * 16, wo = ja < r ? (int)(ja * jb.C * 2) + g * 16 : 0x70000000;
+  const int so = (int)(i * jb.C * 2) + g * 16, wo = ja < r ? (int)(ja * jb.C * 2) + g * 16 : kPastEnd;
   floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   constexpr int kU = 8;  // pieces of 32 elements in flight
   for (int c = 0; c < (int)jb.C * 2; c += kU * 64) {
     u32x4 x[kU], w[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int off = c + u * 64 < (int)jb.C * 2 ? c + u * 64 : 0x7f000000;  // past the row: zeros
+      const int off = c + u * 64 < (int)jb.C * 2 ? c + u * 64 : kPastEnd;  // past the row: zeros
       x[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, so, off, 0));
       w[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wo, off, 0));
     }
