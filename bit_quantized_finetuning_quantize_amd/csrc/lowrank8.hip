@@ -278,10 +278,11 @@ __device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, i
     for (int sp = 0; sp < jb.splits; ++sp)
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += at[q][sp * stride];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (m0 + 4 * q >= M || j >= r) v[q] = 0.0f;
   }
+  // 0 past M and r: what stands there is a copy, or an infinity's product with 0
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (m0 + 4 * q >= M || j >= r) v[q] = 0.0f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int64_t m = m0 + 4 * q;
