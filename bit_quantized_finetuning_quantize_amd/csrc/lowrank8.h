@@ -101,14 +101,17 @@ struct ColPair {
 };
 
 // Eight floats as three bf16 terms each: every remainder is exact, so the
-// terms' sum is the float to 24 bits. An infinity's remainder is a NaN.
+// terms' sum is the float to 24 bits. The first term is cut towards zero, since
+// rounded it would be an infinity above the largest bf16; the others are
+// rounded. An infinity's remainder is a NaN.
 __device__ __forceinline__ void split3(const floatx4 (&v)[2], u32x4 (&term)[kTerms]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float a = v[e >> 1][(e & 1) * 2], b = v[e >> 1][(e & 1) * 2 + 1];
 #pragma unroll
     for (int c = 0; c < kTerms; ++c) {
-      const uint32_t w = pack_bf16x2(a, b);
+      const uint32_t w = c ? pack_bf16x2(a, b)
+                           : __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
       term[c][e] = w;
       a -= __builtin_bit_cast(float, w << 16);
       b -= __builtin_bit_cast(float, w & 0xffff0000u);

@@ -571,8 +571,9 @@ size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
  *   codes, absmax_q, absmax_s2, store_type  as qlora_linear_bwd_ex; read for
  *              dX only, and may be NULL when dX is
  * dA and dB are accurate to float32: the float32 factors s G and s T enter
- * the matrix products as three bf16 terms. An infinity among them has no such
- * terms: the gradients that it reaches are then NaN or infinite. dX is
+ * the matrix products as three bf16 terms, exact for every finite value. An
+ * infinity has no such terms, and one in dY or dec(x_*) meets terms of either
+ * sign: the elements of dA and dB that it reaches are NaN or infinite. dX is
  * qlora_linear_bwd's: s G enters it as bf16.
  * Errors: as qlora_linear_bwd_ex and qlora_linear_bwd_dropout; INVALID_ARG
  * also for an unknown fmt or null x_codes / x_scales. */

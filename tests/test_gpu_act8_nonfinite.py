@@ -1,6 +1,6 @@
 """Infinities and NaN through the linear calls on 8-bit inputs: each reaches
 what the formula says it reaches and nothing else, in every form of the
-product."""
+product, and finite factors at the top of float32's range stay finite."""
 
 import numpy as np
 import pytest
@@ -115,3 +115,32 @@ def test_dropped_elements_do_not_spread(q, M, N, K, r, value):
         got.append(q.qlora_linear_bwd_act8(c.dY, x8, None, st, c.A, c.B, 2.0, keep_mask=mask, p=0.2))
     for a, b in zip(*got):
         assert torch.equal(a, b) and bool(torch.isfinite(a.float()).all())
+
+
+# G = 1.998 2^127 is a float32 above the largest bf16 (1.992 2^127)
+@pytest.mark.parametrize("base", ["fp8", "nf4"])
+@pytest.mark.parametrize("N,r", [(128, 8), (128, 40), (1088, 8)])
+def test_factors_above_the_largest_bf16(q, N, r, base):
+    M, K = 35, 64
+    dev = device()
+    bf = dict(dtype=torch.bfloat16, device=dev)
+    c = Positive(M, N, K, r)
+    c.dY, c.B = torch.zeros(M, N, **bf), torch.zeros(r, N, **bf)
+    c.dY[33, 0], c.dY[33, 1] = 1.9921875 * 2.0 ** 63, 1.5 * 2.0 ** 60
+    c.B[:, 0], c.B[:, 1] = 2.0 ** 64, 2.0 ** 59
+    G = (1.9921875 + 1.5 * 2.0 ** -8) * 2.0 ** 127
+    assert G < torch.finfo(torch.float32).max and np.isinf(float(torch.tensor(G, **bf)))
+    x = torch.full((M, K), 2.0 ** -10, **bf)
+    x8 = q.qlora_act8_quantize(x)
+    T = torch.zeros(M, r, device=dev)
+    T[33, :] = -G
+    c.dY[33, 2] = 2.0 ** -20
+    if base == "fp8":
+        w = q.qlora_fp8_weight_quantize(c.W)
+        _, dA, dB = q.qlora_fp8_linear_bwd(c.dY, x8, T, w, c.A, c.B, 1.0, want_dX=False)
+    else:
+        _, dA, dB = q.qlora_linear_bwd_act8(c.dY, x8, T, q.qlora_nf4_quantize(c.W), c.A, c.B, 1.0, want_dX=False)
+    # one product per element, of 24 bits: exact
+    assert np.array_equal(_f64(dA), np.full((K, r), G * 2.0 ** -10))
+    assert np.array_equal(_f64(dB)[:, 2], np.full(r, -G * 2.0 ** -20))
+    assert np.array_equal(_f64(dB)[:, 3:], np.zeros((r, N - 3)))
