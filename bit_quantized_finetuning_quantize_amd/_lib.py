@@ -74,6 +74,7 @@ SIGNATURES = {
                                        _vp, _c_i64, _vp, _c_i64, _vp]),
     "qlora_fp8_weight_quantize": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp]),
     "qlora_act8_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "qlora_fp8_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32]),
     "qlora_linear_bwd_act8": (_c_int, [_vp, _vp, _vp, _c_i32, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64,
                                        _c_i64, _c_i64, _c_i32, _c_f32, _vp, _c_f32, _vp, _vp, _vp,
                                        _vp, _c_size, _c_i32, _vp]),

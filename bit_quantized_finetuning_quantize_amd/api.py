@@ -545,18 +545,29 @@ def qlora_act8_workspace_bytes(M, N, K, r):
     return int(LIB.qlora_act8_workspace_bytes(M, N, K, r))
 
 
-def act8_workspace(M, N, K, r, device):
-    """Workspace of qlora_linear_bwd_act8 and the 8-bit weight's linear calls
-    (r = 0 without an adapter)."""
-    n = qlora_act8_workspace_bytes(M, N, K, r)
+def qlora_fp8_workspace_bytes(M, N, K, r, backward=True):
+    return int(LIB.qlora_fp8_workspace_bytes(M, N, K, r, int(backward)))
+
+
+def _ws(n, M, N, K, r, device):
     if n == 0:
         raise QloraError(f"unsupported linear shape M={M} N={N} K={K} r={r}")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _act8_ws(ws, M, N, K, r, device):
-    if ws is None:
-        return act8_workspace(M, N, K, r, device)
+def act8_workspace(M, N, K, r, device):
+    """Workspace of qlora_linear_bwd_act8, with room for its bf16 copy of the
+    weight; it serves the 8-bit weight's linear calls too (r = 0 without an adapter)."""
+    return _ws(qlora_act8_workspace_bytes(M, N, K, r), M, N, K, r, device)
+
+
+def fp8_workspace(M, N, K, r, device, backward=True):
+    """Workspace of the 8-bit weight's linear calls (r = 0 without an adapter);
+    without `backward` of the forward alone, and of a backward pass without dX."""
+    return _ws(qlora_fp8_workspace_bytes(M, N, K, r, backward), M, N, K, r, device)
+
+
+def _given_ws(ws):
     _need(ws, torch.uint8, "ws")
     return ws
 
@@ -610,7 +621,8 @@ def qlora_linear_bwd_act8(dY, X8, T, W, A, B, scale, want_dX=True, keep_mask=Non
     dX = _out(dX, (M, K), torch.bfloat16, dev, "dX") if want_dX else None
     dA = _out(dA, (K, r), torch.float32, dev, "dA")
     dB = _out(dB, (r, N), torch.float32, dev, "dB")
-    ws = _act8_ws(ws, M, N, K, r, dev)
+    ws = (_given_ws(ws) if ws is not None else act8_workspace(M, N, K, r, dev) if want_dX
+          else fp8_workspace(M, N, K, r, dev, False))
     _check(LIB.qlora_linear_bwd_act8(_ptr(dY), _ptr(X8.codes), _ptr(X8.scales), X8.fmt, _ptr(T),
                                      _ptr(W.codes), _ptr(W.absmax_q), _ptr(W.absmax_s2), _ptr(A),
                                      _ptr(B), M, N, K, r, float(scale), _ptr(keep_mask), float(p),
@@ -652,7 +664,7 @@ def qlora_fp8_linear_fwd(X8, W, A=None, B=None, scale=1.0, want_T=True, Y=None, 
     dev = X8.codes.device
     Y = _out(Y, (M, N), torch.bfloat16, dev, "Y")
     T = _out(T, (M, r), torch.float32, dev, "T") if want_T and r else None
-    ws = _act8_ws(ws, M, N, K, r, dev)
+    ws = _given_ws(ws) if ws is not None else fp8_workspace(M, N, K, r, dev, False)
     _check(LIB.qlora_fp8_linear_fwd(_ptr(X8.codes), _ptr(X8.scales), X8.fmt, _ptr(W.codes),
                                     _ptr(W.scales), _ptr(A), _ptr(B), M, N, K, r, float(scale),
                                     _ptr(Y), _ptr(T), _ptr(ws), ws.numel(), _stream()))
@@ -686,7 +698,7 @@ def qlora_fp8_linear_bwd(dY, X8, T, W, A=None, B=None, scale=1.0, fmt=ACT8_E4M3,
     else:
         dX = None
     x = (_ptr(X8.codes), _ptr(X8.scales), X8.fmt) if r else (None, None, ACT8_E4M3)
-    ws = _act8_ws(ws, M, N, K, r, dev)
+    ws = _given_ws(ws) if ws is not None else fp8_workspace(M, N, K, r, dev, want_dX)
     _check(LIB.qlora_fp8_linear_bwd(_ptr(dY), int(fmt), *x, _ptr(T), _ptr(W.codes_t),
                                     _ptr(W.scales_t), _ptr(A), _ptr(B), M, N, K, r, float(scale),
                                     _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream()))

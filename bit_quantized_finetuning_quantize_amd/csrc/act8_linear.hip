@@ -40,8 +40,9 @@ struct Ws8 {
 
 // Byte offsets in the workspace, 256-aligned. Each part grows with every
 // size (the split partials by their bound of one workgroup per compute
-// unit), so a workspace for a larger call serves a smaller one.
-Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
+// unit), so a workspace for a larger call serves a smaller one. What only
+// some calls need is last, so that the others need not bring it.
+Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r, Act8Ws what) {
   Ws8 w{};
   w.r64 = ((int64_t)r + 63) / 64 * 64;
   const int64_t Mp = (M + 63) / 64 * 64;
@@ -54,11 +55,13 @@ Ws8 ws8_layout(int64_t M, int64_t N, int64_t K, int r) {
   // splits * M * columns: 256 tiles of 64 x 64 at most, or one split
   w.part = take(r ? std::max<int64_t>(256 * 64 * 64, Mp * w.r64) * 4 : 0);
   w.done = take(r ? kTileSums * 4 : 0);
+  // the NF4 backward's decoded weight, in the place of the 8-bit dY
+  w.wt = off;
+  w.total = std::max<size_t>(off, 256);  // 0 is a rejected shape
+  if (what == Act8Ws::kFactors) return w;
   w.dy8 = take(M * act8_row_bytes(N));
   w.dys = take(M * act8_scale_row_bytes(N));
-  // the NF4 backward's decoded weight, in the place of the 8-bit dY
-  w.wt = w.dy8;
-  if (r) off = std::max(off, w.wt + (size_t)(N * K * 2));
+  if (r && what == Act8Ws::kWeight) off = std::max(off, w.wt + (size_t)(N * K * 2));
   w.total = off;
   return w;
 }
@@ -115,15 +118,15 @@ hipError_t bwd_front(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, c
 
 }  // namespace
 
-size_t act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r) {
-  return ws8_layout(M, N, K, r).total;
+size_t act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, Act8Ws what) {
+  return ws8_layout(M, N, K, r, what).total;
 }
 
 hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, Nf4Weight W,
                            const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K,
                            int r, float scale, uint16_t* dX, float* dA, float* dB, void* ws,
                            hipStream_t stream, Dropout dr) {
-  const Ws8 l = ws8_layout(M, N, K, r);
+  const Ws8 l = ws8_layout(M, N, K, r, dX ? Act8Ws::kWeight : Act8Ws::kFactors);
   const Ptrs w = carve(ws, l);
   LowrankBeside beside;
   if (dX) beside.W = W, beside.N = N, beside.K = K, beside.w = w.wt;
@@ -137,7 +140,7 @@ hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float
 hipError_t launch_fp8_fwd(ConstAct8 x, int fmt, ConstAct8 w8, const uint16_t* A, const uint16_t* B,
                           int64_t M, int64_t N, int64_t K, int r, float scale, uint16_t* Y,
                           float* T_out, void* ws, hipStream_t stream) {
-  const Ws8 l = ws8_layout(M, N, K, r);
+  const Ws8 l = ws8_layout(M, N, K, r, Act8Ws::kFactors);
   const Ptrs w = carve(ws, l);
   const bool few = fp8_few(M, N);
   if (!r)
@@ -158,7 +161,7 @@ hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, c
                           ConstAct8 w8t, const uint16_t* A, const uint16_t* B, int64_t M, int64_t N,
                           int64_t K, int r, float scale, uint16_t* dX, float* dA, float* dB,
                           void* ws, hipStream_t stream) {
-  const Ws8 l = ws8_layout(M, N, K, r);
+  const Ws8 l = ws8_layout(M, N, K, r, dX ? Act8Ws::kDy8 : Act8Ws::kFactors);
   const Ptrs w = carve(ws, l);
   const ConstAct8 dy8{w.dy8, w.dys};
   if (!r) {

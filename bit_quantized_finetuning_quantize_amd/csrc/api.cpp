@@ -503,12 +503,17 @@ int qlora_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, uint8_t* 
 
 size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
   if (check_fp8_shape(M, N, K, r) != QLORA_OK) return 0;
-  return qlora::act8_workspace_bytes(M, N, K, r);
+  return qlora::act8_workspace_bytes(M, N, K, r, qlora::Act8Ws::kWeight);
 }
 
-static int check_act8_ws(int64_t M, int64_t N, int64_t K, int32_t r, const void* ws,
+size_t qlora_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int32_t backward) {
+  if (check_fp8_shape(M, N, K, r) != QLORA_OK) return 0;
+  return qlora::act8_workspace_bytes(M, N, K, r, backward ? qlora::Act8Ws::kDy8 : qlora::Act8Ws::kFactors);
+}
+
+static int check_act8_ws(int64_t M, int64_t N, int64_t K, int32_t r, qlora::Act8Ws what, const void* ws,
                          size_t ws_bytes) {
-  if (!ws || ws_bytes < qlora::act8_workspace_bytes(M, N, K, r)) return QLORA_ERR_WORKSPACE;
+  if (!ws || ws_bytes < qlora::act8_workspace_bytes(M, N, K, r, what)) return QLORA_ERR_WORKSPACE;
   return aligned(ws, 256) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
 }
 
@@ -535,7 +540,7 @@ int qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* x_codes, const uint
   if (!aligned(dY, 16) || !aligned(B, 16) || !aligned(A, 2) || (T && !aligned(T, 4)) ||
       (dX && !aligned(dX, 2)) || !aligned(dA, 4) || !aligned(dB, 4))
     return QLORA_ERR_UNSUPPORTED;
-  st = check_act8_ws(M, N, K, r, ws, ws_bytes);
+  st = check_act8_ws(M, N, K, r, dX ? qlora::Act8Ws::kWeight : qlora::Act8Ws::kFactors, ws, ws_bytes);
   if (st != QLORA_OK) return st;
   qlora::Nf4Weight W{codes, absmax_q, absmax_s2, store_type};
   return hip_status(qlora::launch_bwd_act8(dY, qlora::ConstAct8{x_codes, x_scales}, fmt, T, W, A, B,
@@ -555,7 +560,7 @@ int qlora_fp8_linear_fwd(const uint8_t* x_codes, const uint8_t* x_scales, int32_
   if (st != QLORA_OK) return st;
   if (!aligned(B, 16) || !aligned(A, 2) || !aligned(Y, 2) || !aligned(T_out, 4))
     return QLORA_ERR_UNSUPPORTED;
-  st = check_act8_ws(M, N, K, r, ws, ws_bytes);
+  st = check_act8_ws(M, N, K, r, qlora::Act8Ws::kFactors, ws, ws_bytes);
   if (st != QLORA_OK) return st;
   return hip_status(qlora::launch_fp8_fwd(qlora::ConstAct8{x_codes, x_scales}, fmt,
                                           qlora::ConstAct8{w_codes, w_scales}, A, B, M, N, K, r,
@@ -578,7 +583,7 @@ int qlora_fp8_linear_bwd(const uint16_t* dY, int32_t dy_fmt, const uint8_t* x_co
   if (!aligned(dY, r ? 16 : 2) || !aligned(B, 16) || !aligned(A, 2) || !aligned(T, 4) ||
       !aligned(dX, 2) || !aligned(dA, 4) || !aligned(dB, 4))
     return QLORA_ERR_UNSUPPORTED;
-  st = check_act8_ws(M, N, K, r, ws, ws_bytes);
+  st = check_act8_ws(M, N, K, r, dX ? qlora::Act8Ws::kDy8 : qlora::Act8Ws::kFactors, ws, ws_bytes);
   if (st != QLORA_OK) return st;
   return hip_status(qlora::launch_fp8_bwd(dY, dy_fmt, qlora::ConstAct8{x_codes, x_scales}, fmt, T,
                                           qlora::ConstAct8{w_codes_t, w_scales_t}, A, B, M, N, K, r,

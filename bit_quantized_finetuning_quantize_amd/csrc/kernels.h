@@ -211,8 +211,11 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
 // dA = D(dec x)^T g, dB = t^T dY, g and t as launch_lowrank_out's vf (lowrank8.h).
 hipError_t launch_columns(const lr8::ColPair& p, hipStream_t stream);
 
-// Workspace of the three calls below (r may be 0 for the 8-bit weight's).
-size_t act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
+// Workspace of the three calls below (r may be 0 for the 8-bit weight's): the
+// adapter's factors alone (the forward, a backward pass without dX), with dY in
+// 8 bits (the 8-bit weight's dX), or with that or the bf16 copy of a 4-bit weight.
+enum class Act8Ws { kFactors, kDy8, kWeight };
+size_t act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r, Act8Ws what);
 // launch_bwd with the input in 8-bit blocks.
 hipError_t launch_bwd_act8(const uint16_t* dY, ConstAct8 x, int fmt, const float* T, Nf4Weight W,
                            const uint16_t* A, const uint16_t* B, int64_t M, int64_t N, int64_t K,

@@ -556,11 +556,18 @@ int qlora_fp8_weight_quantize(const uint16_t* W, int64_t N, int64_t K, uint8_t* 
  *   qlora_act8_workspace_bytes(M, N, K, r)
  * bytes of device memory, 256-byte aligned, as for the NF4 linear calls. For
  * r > 0 it has room for a bf16 copy of the weight, 2 N K bytes, which
- * qlora_linear_bwd_act8 decodes into it in every call.
+ * qlora_linear_bwd_act8 decodes into it in every call. The 8-bit weight's
+ * calls need
+ *   qlora_fp8_workspace_bytes(M, N, K, r, backward)
+ * bytes alone: backward 0 for the forward, else for the backward pass (which
+ * holds dY in 8 bits). A backward pass of either weight with dX NULL takes
+ * the forward's. The sizes grow with M, N, K and r and from the forward's to
+ * the backward's to the first: a larger one serves a smaller call.
  * r = 0 is the workspace of a call without an adapter. 0 for a shape the
  * calls reject: those of the NF4 linear calls (for r = 0 N and K need not be
  * multiples of 64 and the limits hold for them rounded up to 128). */
 size_t qlora_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
+size_t qlora_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int32_t backward);
 
 /* qlora_linear_bwd_act8 — qlora_linear_bwd (and, with a keep mask,
  * qlora_linear_bwd_dropout) from the input's 8-bit blocks: X is dec(x_*)
