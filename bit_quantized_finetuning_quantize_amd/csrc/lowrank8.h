@@ -111,7 +111,8 @@ __device__ __forceinline__ void split3(const floatx4 (&v)[2], u32x4 (&term)[kTer
 #pragma unroll
     for (int c = 0; c < kTerms; ++c) {
       const uint32_t w = c ? pack_bf16x2(a, b)
-                           : __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+                           : __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b),
+                                                   __builtin_bit_cast(uint32_t, a), 0x07060302u);  // upper halves
       term[c][e] = w;
       a -= __builtin_bit_cast(float, w << 16);
       b -= __builtin_bit_cast(float, w & 0xffff0000u);

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) row_product_kernel(RowProd p) {
 // What follows a row product: V = f * (sum of the partials, in split order),
 // written as any of
 //   out32  float32 V [M x r]
-//   u      bf16(s V), [Mp x r64], 0 past M and r
+//   u      bf16(s V), [M rounded up to 64 x r64], 0 past M and r
 //   vf     s V in float32 in the order a column product reads it
 //          (frag_index), 0 past M and r
 // 16 x 64 tiles, through LDS for the last form. 4.5 to 5.5 us up to 4096 rows:
@@ -252,8 +252,8 @@ __device__ __forceinline__ void out_product(const OutJob& jb, int64_t mt, int jc
 #endif
 }
 
-__device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, int64_t M, int64_t Mp,
-                                         int r, int64_t r64, int64_t rp, float s, float (*tile)[65]) {
+__device__ __forceinline__ void out_tile(const OutJob& jb, int64_t mt, int jc, int64_t M, int r,
+                                         int64_t r64, int64_t rp, float s, float (*tile)[65]) {
   const int t = threadIdx.x;
   float v[4];
   const int jl = t & 63, j = jc * 64 + jl;
@@ -393,7 +393,7 @@ __device__ __forceinline__ void nf4_decode_t(const Nf4Weight& W, int64_t N, int6
 struct OutArgs {
   OutJob o[2];
   PadJob pad;
-  int64_t M, Mp;
+  int64_t M;
   int r;
   int64_t r64, rp;
   float s;
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kOutThreads) lowrank_out_kernel(OutArgs p, Bes
   if (id == 0 && p.done) p.done[threadIdx.x] = 0;
   if (id < p.blocks) {
     const int b = id / p.cols, jc = id % p.cols;
-    if (b < p.blocks0) out_tile(p.o[0], b, jc, p.M, p.Mp, p.r, p.r64, p.rp, p.s, tile);
-    else if (b < p.blocks1) out_tile(p.o[1], b - p.blocks0, jc, p.M, p.Mp, p.r, p.r64, p.rp, p.s, tile);
+    if (b < p.blocks0) out_tile(p.o[0], b, jc, p.M, p.r, p.r64, p.rp, p.s, tile);
+    else if (b < p.blocks1) out_tile(p.o[1], b - p.blocks0, jc, p.M, p.r, p.r64, p.rp, p.s, tile);
     else pad_tile(p.pad, b - p.blocks1, jc, p.r, p.r64, tile);
     return;
   }
@@ -516,7 +516,6 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
   OutArgs p{};
   p.done = done;
   p.M = M;
-  p.Mp = ceil_div(M, 64) * 64;
   p.r = r;
   p.r64 = ceil_div(r, 64) * 64;
   p.rp = lowrank_cols(r);
@@ -525,7 +524,7 @@ hipError_t launch_lowrank_out(const LowrankOut* o, int n, LowrankPad pad, int64_
     p.o[i] = OutJob{o[i].part, o[i].s, o[i].w, o[i].C, o[i].splits, o[i].ldp, o[i].f, o[i].out32, o[i].u, o[i].vf};
   p.pad = PadJob{pad.src, pad.columns, pad.rows, pad.dst};
   p.cols = (int)(p.r64 / 64);
-  p.blocks0 = (int)(p.Mp / kOutRows);
+  p.blocks0 = (int)(ceil_div(M, 64) * 64 / kOutRows);
   p.blocks1 = n * p.blocks0;
   p.blocks = p.cols * (p.blocks1 + (pad.src ? (int)ceil_div(pad.rows, 64) : 0));
   BesideArgs q{};
