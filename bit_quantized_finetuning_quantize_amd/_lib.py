@@ -83,6 +83,15 @@ SIGNATURES = {
     "qlora_fp8_linear_bwd": (_c_int, [_vp, _c_i32, _vp, _vp, _c_i32, _vp, _vp, _vp, _vp, _vp,
                                       _c_i64, _c_i64, _c_i64, _c_i32, _c_f32, _vp, _vp, _vp, _vp,
                                       _c_size, _vp]),
+    "qlora_logits_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i32]),
+    "qlora_logprobs_fwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _c_f32, _vp, _vp, _c_i32,
+                                    _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "qlora_logprobs_bwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _c_f32, _vp, _vp, _vp,
+                                    _vp, _c_i64, _vp]),
+    "qlora_distill_fwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i32, _c_i32, _vp,
+                                   _c_f32, _vp, _vp, _vp, _c_size, _vp]),
+    "qlora_distill_bwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i32, _c_i32,
+                                   _c_f32, _vp, _vp, _vp, _c_i64, _vp]),
     "qlora_gemv_wait_limit": (_c_int, [_c_i64]),
     "qlora_status_string": (ctypes.c_char_p, [_c_int]),
     "qlora_last_hip_error": (_c_int, []),

@@ -703,3 +703,152 @@ def qlora_fp8_linear_bwd(dY, X8, T, W, A=None, B=None, scale=1.0, fmt=ACT8_E4M3,
                                     _ptr(W.scales_t), _ptr(A), _ptr(B), M, N, K, r, float(scale),
                                     _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream()))
     return dX, dA, dB
+
+
+# ---- rows of logits ------------------------------------------------------------
+
+_LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _on(t, dev, name):
+    if t.device != dev:
+        raise QloraError(f"{name} must be on {dev}")
+
+
+def _logits(Z, name="Z"):
+    """(dtype code, T, V, leading dimension, device) of rows of logits on the
+    current device."""
+    if Z.dim() != 2 or Z.dtype not in _LOGITS or not Z.is_cuda:
+        raise QloraError(f"{name} must be a bfloat16 or float32 matrix on the GPU")
+    if Z.device.index != torch._C._cuda_getDevice():
+        raise QloraError(f"{name} must be on the current device")
+    T, V = Z.shape
+    ld, step = Z.stride()
+    if V > 1 and step != 1:
+        raise QloraError(f"{name} must have contiguous rows")
+    if T == 1:  # one row: the stride has no meaning
+        ld = V
+    elif ld < V:
+        raise QloraError(f"{name} must not have overlapping rows")
+    return _LOGITS[Z.dtype], T, V, ld, Z.device
+
+
+def _row(t, shape, dtype, dev, name):
+    """A given tensor of one number (or list) per row, or None."""
+    if t is not None:
+        _need(t, dtype, name)
+        _on(t, dev, name)
+        if t.shape != shape:
+            raise QloraError(f"{name} must have shape {shape}")
+    return t
+
+
+def _dlogits(Z, dZ, T, V, dev):
+    """(dZ, its leading dimension)."""
+    if dZ is None:
+        return torch.empty(T, V, dtype=Z.dtype, device=dev), V
+    if dZ.shape != Z.shape or dZ.dtype is not Z.dtype:
+        raise QloraError("dZ must have the shape and type of Z")
+    return dZ, _logits(dZ, "dZ")[3]
+
+
+def qlora_logits_workspace_bytes(T, V, n_top=0):
+    return int(LIB.qlora_logits_workspace_bytes(T, V, n_top))
+
+
+def logits_workspace(T, V, n_top, device):
+    """Workspace of qlora_logprobs_fwd (n_top alternatives) and of
+    qlora_distill_fwd (n_top = 0)."""
+    n = qlora_logits_workspace_bytes(T, V, n_top)
+    if n == 0:
+        raise QloraError(f"unsupported rows of logits T={T} V={V} n_top={n_top}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _logits_ws(ws, T, V, n_top, dev):
+    if ws is None:
+        return logits_workspace(T, V, n_top, dev)
+    _on(ws, dev, "ws")
+    return _given_ws(ws)
+
+
+def qlora_logprobs_fwd(Z, target=None, temperature=1.0, n_top=0, want_entropy=True, want_stats=True,
+                       ws=None):
+    """Of rows of logits Z [T x V] at a temperature: (logp of target, entropy,
+    top_ids, top_logp, stats), each None where not asked for. `target` int64
+    [T], outside [0, V) where a row has none (logp 0); the n_top most likely
+    entries of each row in descending order, of equal ones the lowest id
+    first; `stats` float32 [T x 3] is what the backward pass takes."""
+    dt, T, V, ld, dev = _logits(Z)
+    _row(target, (T,), torch.int64, dev, "target")
+    f32 = torch.float32
+    logp = torch.empty(T, dtype=f32, device=dev) if target is not None else None
+    ent = torch.empty(T, dtype=f32, device=dev) if want_entropy else None
+    stats = torch.empty(T, 3, dtype=f32, device=dev) if want_stats else None
+    ids = top = None
+    if n_top:
+        ids = torch.empty(T, n_top, dtype=torch.int64, device=dev)
+        top = torch.empty(T, n_top, dtype=f32, device=dev)
+    ws = _logits_ws(ws, T, V, n_top, dev)
+    _check(LIB.qlora_logprobs_fwd(_ptr(Z), dt, T, V, ld, _ptr(target), float(temperature), _ptr(logp),
+                                  _ptr(ent), int(n_top), _ptr(ids), _ptr(top), _ptr(stats), _ptr(ws),
+                                  ws.numel(), _stream()))
+    return logp, ent, ids, top, stats
+
+
+def qlora_logprobs_bwd(Z, target, stats, g_logp=None, g_entropy=None, temperature=1.0, dZ=None):
+    """The gradient of the logits from those of the targets' log-probabilities
+    and of the entropies (float32 [T], either may be None), with the forward's
+    stats. dZ may be Z."""
+    dt, T, V, ld, dev = _logits(Z)
+    _row(target, (T,), torch.int64, dev, "target")
+    _row(stats, (T, 3), torch.float32, dev, "stats")
+    _row(g_logp, (T,), torch.float32, dev, "g_logp")
+    _row(g_entropy, (T,), torch.float32, dev, "g_entropy")
+    dZ, ldd = _dlogits(Z, dZ, T, V, dev)
+    _check(LIB.qlora_logprobs_bwd(_ptr(Z), dt, T, V, ld, _ptr(target), float(temperature), _ptr(stats),
+                                  _ptr(g_logp), _ptr(g_entropy), _ptr(dZ), ldd, _stream()))
+    return dZ
+
+
+def _teacher(ids, values, T, dev):
+    """(values' dtype code, k) of a teacher's top logits."""
+    if ids.dim() != 2 or values.dtype not in _LOGITS:
+        raise QloraError("ids must be [T x k] and values bfloat16 or float32")
+    k = ids.shape[1]
+    _row(ids, (T, k), torch.int64, dev, "ids")
+    _row(values, (T, k), values.dtype, dev, "values")
+    return _LOGITS[values.dtype], k
+
+
+def qlora_distill_fwd(Z, ids, values, teacher_lse=None, temperature=1.0, want_stats=True, loss=None,
+                      ws=None):
+    """Divergence of the rows of the student's logits Z [T x V] from a teacher
+    known by k logits of each row (ids int64 and values [T x k]; ids outside
+    [0, V) are left out) and, optionally, its log sum exp (at the temperature)
+    float32 [T]: the rest of its mass is then one more class, otherwise the
+    list alone is the distribution. Returns (loss float32 [T], stats [T x 6] or
+    None)."""
+    dt, T, V, ld, dev = _logits(Z)
+    vt, k = _teacher(ids, values, T, dev)
+    _row(teacher_lse, (T,), torch.float32, dev, "teacher_lse")
+    loss = _out(loss, (T,), torch.float32, dev, "loss")
+    stats = torch.empty(T, 6, dtype=torch.float32, device=dev) if want_stats else None
+    ws = _logits_ws(ws, T, V, 0, dev)
+    _check(LIB.qlora_distill_fwd(_ptr(Z), dt, T, V, ld, _ptr(ids), _ptr(values), vt, k,
+                                 _ptr(teacher_lse), float(temperature), _ptr(loss), _ptr(stats),
+                                 _ptr(ws), ws.numel(), _stream()))
+    return loss, stats
+
+
+def qlora_distill_bwd(Z, ids, values, stats, g, temperature=1.0, dZ=None):
+    """The gradient of the logits from that of qlora_distill_fwd's loss (g
+    float32 [T]), with the forward's stats. dZ may be Z."""
+    dt, T, V, ld, dev = _logits(Z)
+    vt, k = _teacher(ids, values, T, dev)
+    _row(stats, (T, 6), torch.float32, dev, "stats")
+    _row(g, (T,), torch.float32, dev, "g")
+    dZ, ldd = _dlogits(Z, dZ, T, V, dev)
+    _check(LIB.qlora_distill_bwd(_ptr(Z), dt, T, V, ld, _ptr(ids), _ptr(values), vt, k,
+                                 float(temperature), _ptr(stats), _ptr(g), _ptr(dZ), ldd, _stream()))
+    return dZ

@@ -100,6 +100,39 @@ int check_fp8_shape(int64_t M, int64_t N, int64_t K, int32_t r) {
   return QLORA_OK;
 }
 
+// Rows of logits.
+int check_logits(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz, float temperature,
+                 qlora::Logits* z) {
+  if (!Z || T <= 0 || V <= 0 || ldz < V) return QLORA_ERR_INVALID_ARG;
+  if (dtype != QLORA_LOGITS_BF16 && dtype != QLORA_LOGITS_F32) return QLORA_ERR_INVALID_ARG;
+  if (!(temperature > 0.0f) || std::isinf(temperature)) return QLORA_ERR_INVALID_ARG;
+  if (T > (int64_t)1 << 24 || V > (int64_t)1 << 21 || ldz > (int64_t)1 << 32) return QLORA_ERR_UNSUPPORTED;
+  if (temperature < 0x1p-40f || temperature > 0x1p40f) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned(Z, dtype == QLORA_LOGITS_F32 ? 4 : 2)) return QLORA_ERR_UNSUPPORTED;
+  *z = qlora::Logits{Z, dtype == QLORA_LOGITS_F32, T, V, ldz, temperature};
+  return QLORA_OK;
+}
+
+int check_top_logits(const int64_t* ids, const void* values, int32_t dtype, int32_t k, qlora::TopLogits* t) {
+  if (!ids || !values || k <= 0) return QLORA_ERR_INVALID_ARG;
+  if (dtype != QLORA_LOGITS_BF16 && dtype != QLORA_LOGITS_F32) return QLORA_ERR_INVALID_ARG;
+  if (k > QLORA_MAX_TEACHER_LOGITS) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned(ids, 8) || !aligned(values, dtype == QLORA_LOGITS_F32 ? 4 : 2)) return QLORA_ERR_UNSUPPORTED;
+  *t = qlora::TopLogits{ids, values, dtype == QLORA_LOGITS_F32, k};
+  return QLORA_OK;
+}
+
+int check_dlogits(const void* dZ, int64_t lddz, const qlora::Logits& z) {
+  if (!dZ || lddz < z.V) return QLORA_ERR_INVALID_ARG;
+  if (lddz > (int64_t)1 << 32 || !aligned(dZ, z.f32 ? 4 : 2)) return QLORA_ERR_UNSUPPORTED;
+  return QLORA_OK;
+}
+
+int check_logits_ws(const qlora::Logits& z, int n_top, const void* ws, size_t ws_bytes) {
+  if (!ws || ws_bytes < qlora::logits_workspace_bytes(z.T, z.V, n_top)) return QLORA_ERR_WORKSPACE;
+  return aligned(ws, 256) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 
 extern "C" {
@@ -589,6 +622,79 @@ int qlora_fp8_linear_bwd(const uint16_t* dY, int32_t dy_fmt, const uint8_t* x_co
                                           qlora::ConstAct8{w_codes_t, w_scales_t}, A, B, M, N, K, r,
                                           scale, dX, dA, dB, ws,
                                           reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top) {
+  if (T <= 0 || V <= 0 || T > (int64_t)1 << 24 || V > (int64_t)1 << 21) return 0;
+  if (n_top < 0 || n_top > QLORA_MAX_TOP_LOGITS || n_top > V) return 0;
+  return qlora::logits_workspace_bytes(T, V, n_top);
+}
+
+int qlora_logprobs_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                       const int64_t* target, float temperature, float* logp, float* entropy,
+                       int32_t n_top, int64_t* top_ids, float* top_logp, float* stats, void* ws,
+                       size_t ws_bytes, void* stream) {
+  qlora::Logits z;
+  int st = check_logits(Z, dtype, T, V, ldz, temperature, &z);
+  if (st != QLORA_OK) return st;
+  if (logp && !target) return QLORA_ERR_INVALID_ARG;
+  if (n_top < 0 || n_top > V || (n_top ? !top_ids || !top_logp : top_ids || top_logp)) return QLORA_ERR_INVALID_ARG;
+  if (!logp && !entropy && !n_top && !stats) return QLORA_ERR_INVALID_ARG;
+  if (n_top > QLORA_MAX_TOP_LOGITS) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned(target, 8) || !aligned(top_ids, 8) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+      !aligned(top_logp, 4) || !aligned(stats, 4))
+    return QLORA_ERR_UNSUPPORTED;
+  st = check_logits_ws(z, n_top, ws, ws_bytes);
+  if (st != QLORA_OK) return st;
+  return hip_status(qlora::launch_logprobs_fwd(z, target, logp, entropy, n_top, top_ids, top_logp, stats, ws,
+                                               reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                       const int64_t* target, float temperature, const float* stats,
+                       const float* g_logp, const float* g_entropy, void* dZ, int64_t lddz,
+                       void* stream) {
+  qlora::Logits z;
+  int st = check_logits(Z, dtype, T, V, ldz, temperature, &z);
+  if (st == QLORA_OK) st = check_dlogits(dZ, lddz, z);
+  if (st != QLORA_OK) return st;
+  if (!stats || (!g_logp && !g_entropy) || (g_logp && !target)) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(target, 8) || !aligned(stats, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
+    return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_logprobs_bwd(z, target, stats, g_logp, g_entropy, dZ, lddz,
+                                               reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_distill_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                      const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
+                      const float* teacher_lse, float temperature, float* loss, float* stats,
+                      void* ws, size_t ws_bytes, void* stream) {
+  qlora::Logits z;
+  qlora::TopLogits t;
+  int st = check_logits(Z, dtype, T, V, ldz, temperature, &z);
+  if (st == QLORA_OK) st = check_top_logits(ids, values, values_dtype, k, &t);
+  if (st != QLORA_OK) return st;
+  if (!loss) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(teacher_lse, 4) || !aligned(loss, 4) || !aligned(stats, 4)) return QLORA_ERR_UNSUPPORTED;
+  st = check_logits_ws(z, 0, ws, ws_bytes);
+  if (st != QLORA_OK) return st;
+  return hip_status(qlora::launch_distill_fwd(z, t, teacher_lse, loss, stats, ws,
+                                              reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_distill_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                      const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
+                      float temperature, const float* stats, const float* g, void* dZ,
+                      int64_t lddz, void* stream) {
+  qlora::Logits z;
+  qlora::TopLogits t;
+  int st = check_logits(Z, dtype, T, V, ldz, temperature, &z);
+  if (st == QLORA_OK) st = check_top_logits(ids, values, values_dtype, k, &t);
+  if (st == QLORA_OK) st = check_dlogits(dZ, lddz, z);
+  if (st != QLORA_OK) return st;
+  if (!stats || !g) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(stats, 4) || !aligned(g, 4)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_distill_bwd(z, t, stats, g, dZ, lddz, reinterpret_cast<hipStream_t>(stream)));
 }
 
 int qlora_gemv_wait_limit(int64_t microseconds) {

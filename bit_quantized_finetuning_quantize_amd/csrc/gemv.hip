@@ -50,6 +50,7 @@
 // the same order and arithmetic, so the result is the same bit for bit
 // either way.
 #include "common.h"
+#include "handover.h"
 #include "kernels.h"
 
 #include <algorithm>
@@ -87,9 +88,6 @@ std::atomic<int64_t> g_wait_us{200};
 constexpr int kSpinPolls = 1 << 16;  // a bound on polls as well
 constexpr int kXcds = 8;       // XCDs of the device, each with its own L2
 
-// The dispatch packet's index in its queue (a hardware-provided value).
-extern "C" __device__ uint64_t qlora_dispatch_index() __asm("llvm.amdgcn.dispatch.id");
-
 // The XCD this wave runs on (its L2 is shared by that XCD's CUs only).
 __device__ __forceinline__ int xcd_id() {
   unsigned v;
@@ -99,14 +97,6 @@ __device__ __forceinline__ int xcd_id() {
 
 // Flags sit 128 bytes apart, one to an L2 line.
 constexpr int kFlagStride = 16;  // u64 elements
-
-// A tag unique to this dispatch within the process: dispatch indices count
-// up per queue, and queues differ in address bits 12-39, so the value
-// repeats only after 2^36 dispatches on one queue.
-__device__ __forceinline__ uint64_t call_tag() {
-  const uint64_t q = (uint64_t)(uintptr_t)__builtin_amdgcn_queue_ptr();
-  return qlora_dispatch_index() ^ (q << 24);
-}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int64_t bytes) {
   if (bytes > 0x7ffffff0LL) bytes = 0x7ffffff0LL;

@@ -231,6 +231,32 @@ hipError_t launch_fp8_bwd(const uint16_t* dY, int dyfmt, ConstAct8 x, int fmt, c
                           int64_t K, int r, float scale, uint16_t* dX, float* dA, float* dB,
                           void* ws, hipStream_t stream);
 
+// ---- rows of logits (logits.hip) ------------------------------------------------
+
+// Z [T x V], rows ldz elements apart, bf16 or float32.
+struct Logits {
+  const void* Z;
+  bool f32;
+  int64_t T, V, ldz;
+  float temperature;
+};
+// A teacher's k largest logits of each row and their ids, [T x k].
+struct TopLogits {
+  const int64_t* ids;
+  const void* values;
+  bool f32;
+  int k;
+};
+size_t logits_workspace_bytes(int64_t T, int64_t V, int n_top);
+hipError_t launch_logprobs_fwd(const Logits& z, const int64_t* target, float* logp, float* entropy, int n_top,
+                               int64_t* top_ids, float* top_logp, float* stats, void* ws, hipStream_t stream);
+hipError_t launch_logprobs_bwd(const Logits& z, const int64_t* target, const float* stats, const float* g_logp,
+                               const float* g_entropy, void* dZ, int64_t lddz, hipStream_t stream);
+hipError_t launch_distill_fwd(const Logits& z, const TopLogits& t, const float* teacher_lse, float* loss,
+                              float* stats, void* ws, hipStream_t stream);
+hipError_t launch_distill_bwd(const Logits& z, const TopLogits& t, const float* stats, const float* g, void* dZ,
+                              int64_t lddz, hipStream_t stream);
+
 // Forward with the library's own scratch array (one per device, this many
 // bytes) in place of a caller workspace.
 constexpr size_t kNoAllocScratchBytes = (size_t)32 << 20;

@@ -628,6 +628,97 @@ int qlora_fp8_linear_bwd(const uint16_t* dY, int32_t dy_fmt, const uint8_t* x_co
                          float scale, uint16_t* dX, float* dA, float* dB, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* ---- rows of logits -------------------------------------------------------------
+ * What a model's output layer feeds: T rows of V logits, bf16 (QLORA_LOGITS_BF16,
+ * uint16_t bit patterns) or float32 (QLORA_LOGITS_F32), rows ldz >= V elements
+ * apart. For a row z and a temperature t
+ *   m = max z,   x = (z - m) / t,   l = log sum exp x,   log p_j = x_j - l.
+ * Sums are float32 (a row's few numbers in a distillation float64); every logit is
+ * read once. Rows and pointers need their elements' alignment only.
+ *
+ * Masked and other special rows. A logit of -inf, or so low that exp underflows,
+ * has p = 0 and adds nothing to an entropy or a gradient. A row whose logits are all
+ * -inf has no distribution: log p = -inf, entropy 0, gradient 0; a distillation
+ * loss is +inf if it has targets, else 0. A row with a NaN or +inf has NaN.
+ *
+ * Sizes: 1 <= T <= 2^24, 1 <= V <= 2^21, 1 <= n_top <= 64 (and <= V), 1 <= k <=
+ * 256, 2^-40 <= t <= 2^40.
+ *
+ * Workspace of the two forward passes: at least
+ *   qlora_logits_workspace_bytes(T, V, n_top)
+ * bytes of device memory, 256-byte aligned (n_top = 0 without alternatives and for a
+ * distillation; 0 for a shape the calls reject). Few rows are split over
+ * workgroups and joined in the same launch by way of it. Its contents on entry do
+ * not matter. */
+#define QLORA_LOGITS_BF16 0
+#define QLORA_LOGITS_F32 1
+#define QLORA_MAX_TOP_LOGITS 64
+#define QLORA_MAX_TEACHER_LOGITS 256
+size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top);
+
+/* qlora_logprobs_fwd — for each row
+ *   logp     device float [T]: log p of target, 0 where it lies outside [0, V) (a
+ *            token that does not count, e.g. -100); or NULL (target may then be)
+ *   target   device int64 [T]
+ *   entropy  device float [T], -sum p log p; or NULL
+ *   top_ids, top_logp  device int64 and float [T x n_top]: the n_top largest logits'
+ *            ids and log p, in descending order, of equal logits (-0 equals +0) the
+ *            lowest id first, NaN last; both NULL with n_top = 0
+ *   stats    device float [T x 3], (m, l, entropy), which the backward pass
+ *            takes; or NULL
+ * qlora_logprobs_bwd — the gradient of the logits from those of logp and entropy:
+ *   dz_j = (g_logp ([j = target] - p_j) - g_entropy p_j (log p_j + entropy)) / t
+ *   g_logp, g_entropy  device float [T]; either may be NULL (with g_logp NULL
+ *            target may be too). A target outside [0, V) has no g_logp.
+ *   dZ       device, the type of Z, rows lddz >= V elements apart; may be Z (same base
+ *            and same row distance). Rows whose gradients are both 0 become 0,
+ *            whatever their logits.
+ * Errors: INVALID_ARG (null required pointer, no output, n_top without both outputs or
+ * above V, sizes not positive, ldz or lddz < V, unknown dtype, t not a positive
+ * finite number); UNSUPPORTED (a size, temperature or alignment outside the
+ * above); WORKSPACE. */
+int qlora_logprobs_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                       const int64_t* target, float temperature, float* logp, float* entropy,
+                       int32_t n_top, int64_t* top_ids, float* top_logp, float* stats, void* ws,
+                       size_t ws_bytes, void* stream);
+int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                       const int64_t* target, float temperature, const float* stats,
+                       const float* g_logp, const float* g_entropy, void* dZ, int64_t lddz,
+                       void* stream);
+
+/* qlora_distill_fwd — the divergence of the student's rows from a teacher known by k of
+ * its logits to a row. With tm the largest of them and q_i = exp((t_i - tm) / t - tl),
+ *   tl = teacher_lse - tm / t     teacher_lse = log sum exp(t_j / t) over the teacher's
+ *                                 whole vocabulary: the rest q_r = max(0, 1 - sum q)
+ *                                 is one more class, p_r the student's mass off the list
+ *   tl = log sum exp((t_i - tm) / t)   without teacher_lse: q is the softmax of the list
+ *   loss = sum q_i (log q_i - log p_i) + q_r (log q_r - log p_r)
+ *   ids      device int64 [T x k]; an id outside [0, V) is no entry (lists of
+ *            different lengths). An id given twice has both entries' q.
+ *   values   device [T x k], the teacher's logits, values_dtype as Z's dtype; -inf
+ *            has q = 0. They need no order.
+ *   teacher_lse  device float [T] or NULL
+ *   loss     device float [T]. The gradient of a temperature t is usually scaled by
+ *            t^2: that is the caller's g.
+ *   stats    device float [T x 6], (m, l, w, w - q_r / p_r, tm, tl) with w = sum q +
+ *            q_r, which the backward pass takes; or NULL
+ * Where the student has no mass off the list (p_r = 0) the rest's term is left out and
+ * w = sum q. q_r / p_r is kept in float32's range: where the student's mass off the list
+ * is below 1e-38, the gradient there is smaller than the formula's. A row without entries has loss 0 without teacher_lse.
+ * qlora_distill_bwd — dz_j = g / t (w p_j - q_j) for j on the list, and g / t
+ * (w - q_r / p_r) p_j off it.
+ *   g        device float [T], the gradient of loss; a row with g = 0 becomes 0
+ *   dZ       as in qlora_logprobs_bwd
+ * Errors: as qlora_logprobs_fwd and _bwd. */
+int qlora_distill_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                      const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
+                      const float* teacher_lse, float temperature, float* loss, float* stats,
+                      void* ws, size_t ws_bytes, void* stream);
+int qlora_distill_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
+                      const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
+                      float temperature, const float* stats, const float* g, void* dZ,
+                      int64_t lddz, void* stream);
+
 /* qlora_gemv_wait_limit — how long, in microseconds, the row-tile
  * workgroups of a small-M forward (M <= 16) wait for the workgroups of the
  * same launch that form T = X A, before forming T themselves; the default,
