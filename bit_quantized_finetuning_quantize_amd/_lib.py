@@ -83,6 +83,10 @@ SIGNATURES = {
     "qlora_fp8_linear_bwd": (_c_int, [_vp, _c_i32, _vp, _vp, _c_i32, _vp, _vp, _vp, _vp, _vp,
                                       _c_i64, _c_i64, _c_i64, _c_i32, _c_f32, _vp, _vp, _vp, _vp,
                                       _c_size, _vp]),
+    "qlora_int4_quantize": (_c_int, [_vp, _c_i64, _c_i64, _c_i64, _c_i32, _vp, _vp, _vp, _vp]),
+    "qlora_int4_dequantize": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_i32, _vp, _c_i64, _vp]),
+    "qlora_int4_linear_fwd": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp, _c_i64, _c_i64, _c_i32, _vp,
+                                       _c_i32, _c_i64, _vp]),
     "qlora_logits_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i32]),
     "qlora_logprobs_fwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _c_f32, _vp, _vp, _c_i32,
                                     _vp, _vp, _vp, _vp, _c_size, _vp]),

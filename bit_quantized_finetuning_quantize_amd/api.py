@@ -705,9 +705,9 @@ def qlora_fp8_linear_bwd(dY, X8, T, W, A=None, B=None, scale=1.0, fmt=ACT8_E4M3,
     return dX, dA, dB
 
 
-# ---- rows of logits ------------------------------------------------------------
+# ---- 4 bits in groups ----------------------------------------------------------
 
-_LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+_FLOATS = {torch.bfloat16: 0, torch.float32: 1}  # QLORA_LOGITS_BF16, QLORA_LOGITS_F32
 
 
 def _on(t, dev, name):
@@ -715,22 +715,110 @@ def _on(t, dev, name):
         raise QloraError(f"{name} must be on {dev}")
 
 
-def _logits(Z, name="Z"):
-    """(dtype code, T, V, leading dimension, device) of rows of logits on the
-    current device."""
-    if Z.dim() != 2 or Z.dtype not in _LOGITS or not Z.is_cuda:
-        raise QloraError(f"{name} must be a bfloat16 or float32 matrix on the GPU")
-    if Z.device.index != torch._C._cuda_getDevice():
+def _matrix(t, name, dtypes=_FLOATS):
+    """(rows, columns, leading dimension, device) of a matrix on the current
+    device whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda:
+        raise QloraError(f"{name} must be a matrix of {' or '.join(map(str, dtypes))} on the GPU")
+    if t.device.index != torch._C._cuda_getDevice():
         raise QloraError(f"{name} must be on the current device")
-    T, V = Z.shape
-    ld, step = Z.stride()
-    if V > 1 and step != 1:
+    M, K = t.shape
+    ld, step = t.stride()
+    if K > 1 and step != 1:
         raise QloraError(f"{name} must have contiguous rows")
-    if T == 1:  # one row: the stride has no meaning
-        ld = V
-    elif ld < V:
+    if M <= 1:  # one row: the stride has no meaning
+        return M, K, K, t.device
+    if ld < K:
         raise QloraError(f"{name} must not have overlapping rows")
-    return _LOGITS[Z.dtype], T, V, ld, Z.device
+    return M, K, ld, t.device
+
+
+class Int4Weight:
+    """A weight [N x K] in 4 bits with a bf16 scale and a zero point (`zeros`
+    uint8, or None for 8) for each group of 32, 64 or 128 columns of a row
+    (include/qlora.h): codes uint8 [N, K / 2], scales and zeros [N, groups]."""
+
+    __slots__ = ("codes", "scales", "zeros", "shape", "group")
+
+    def __init__(self, codes, scales, zeros, shape, group):
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.shape = tuple(shape)
+        self.group = int(group)
+
+    def nbytes(self):
+        return self.codes.numel() + 2 * self.scales.numel() + (0 if self.zeros is None else self.zeros.numel())
+
+
+def _need_int4(w, dev):
+    N, K = w.shape
+    groups = -(-K // w.group) if w.group > 0 else -1
+    for t, shape, dtype, name in ((w.codes, (N, K // 2), torch.uint8, "codes"),
+                                  (w.scales, (N, groups), torch.bfloat16, "scales"),
+                                  (w.zeros, (N, groups), torch.uint8, "zeros")):
+        if t is None and name == "zeros":
+            continue
+        _need(t, dtype, f"the weight's {name}")
+        if t.shape != shape:
+            raise QloraError(f"the weight's {name} must have shape {shape}")
+        _on(t, dev, f"the weight's {name}")
+    return N, K
+
+
+def qlora_int4_quantize(W, group=128, symmetric=False):
+    """A bf16 weight [N x K] (rows may be strided) in 4 bits with a scale, and
+    unless `symmetric` a zero point, for each `group` columns of a row."""
+    N, K, ld, dev = _matrix(W, "W", (torch.bfloat16,))
+    if group not in (32, 64, 128) or K % 32:
+        raise QloraError("groups of 32, 64 or 128 columns, and a multiple of 32 of them")
+    ng = -(-K // group)
+    w = Int4Weight(torch.empty(N, K // 2, dtype=torch.uint8, device=dev),
+                   torch.empty(N, ng, dtype=torch.bfloat16, device=dev),
+                   None if symmetric else torch.empty(N, ng, dtype=torch.uint8, device=dev), (N, K), group)
+    _check(LIB.qlora_int4_quantize(_ptr(W), N, K, ld, w.group, _ptr(w.codes), _ptr(w.scales),
+                                   _ptr(w.zeros), _stream()))
+    return w
+
+
+def qlora_int4_dequantize(w, out=None):
+    """bf16 [N x K] of a weight in groups of 4-bit codes."""
+    dev = w.codes.device
+    N, K = _need_int4(w, dev)
+    out = out if out is not None else torch.empty(N, K, dtype=torch.bfloat16, device=dev)
+    n, k, ld, on = _matrix(out, "out", (torch.bfloat16,))
+    if (n, k) != (N, K) or on != dev:
+        raise QloraError(f"out must have shape {(N, K)}, on {dev}")
+    _check(LIB.qlora_int4_dequantize(_ptr(w.codes), _ptr(w.scales), _ptr(w.zeros), N, K, w.group,
+                                     _ptr(out), ld, _stream()))
+    return out
+
+
+def qlora_int4_linear_fwd(X, w, dtype=torch.bfloat16, Y=None):
+    """Y = X W^T of few tokens X bf16 [M x K] (rows may be strided), in `dtype`
+    bfloat16 or float32 (or that of a given Y)."""
+    M, K, ldx, dev = _matrix(X, "X", (torch.bfloat16,))
+    N, k = _need_int4(w, dev)
+    if k != K:
+        raise QloraError("W must be [N x K] with the K of X")
+    if Y is None:
+        if dtype not in _FLOATS:
+            raise QloraError("dtype must be bfloat16 or float32")
+        Y, ldy = torch.empty(M, N, dtype=dtype, device=dev), N
+    else:
+        m, n, ldy, on = _matrix(Y, "Y")
+        if (m, n) != (M, N) or on != dev:
+            raise QloraError(f"Y must have shape {(M, N)}, on {dev}")
+    _check(LIB.qlora_int4_linear_fwd(_ptr(X), M, ldx, _ptr(w.codes), _ptr(w.scales), _ptr(w.zeros), N, K,
+                                     w.group, _ptr(Y), _FLOATS[Y.dtype], ldy, _stream()))
+    return Y
+
+
+# ---- rows of logits ------------------------------------------------------------
+
+
+def _logits(Z, name="Z"):
+    """(dtype code, T, V, leading dimension, device) of rows of logits."""
+    T, V, ld, dev = _matrix(Z, name)
+    return _FLOATS[Z.dtype], T, V, ld, dev
 
 
 def _row(t, shape, dtype, dev, name):
@@ -813,12 +901,12 @@ def qlora_logprobs_bwd(Z, target, stats, g_logp=None, g_entropy=None, temperatur
 
 def _teacher(ids, values, T, dev):
     """(values' dtype code, k) of a teacher's top logits."""
-    if ids.dim() != 2 or values.dtype not in _LOGITS:
+    if ids.dim() != 2 or values.dtype not in _FLOATS:
         raise QloraError("ids must be [T x k] and values bfloat16 or float32")
     k = ids.shape[1]
     _row(ids, (T, k), torch.int64, dev, "ids")
     _row(values, (T, k), values.dtype, dev, "values")
-    return _LOGITS[values.dtype], k
+    return _FLOATS[values.dtype], k
 
 
 def qlora_distill_fwd(Z, ids, values, teacher_lse=None, temperature=1.0, want_stats=True, loss=None,

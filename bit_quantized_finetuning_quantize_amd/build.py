@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqlora.so")
 SOURCES = ["quant.hip", "gemv.hip", "linear.hip", "adamw.hip", "dropout.hip", "noalloc.hip",
-           "act8.hip", "fp8_gemm.hip", "lowrank8.hip", "act8_linear.hip", "logits.hip", "api.cpp"]
+           "act8.hip", "fp8_gemm.hip", "lowrank8.hip", "act8_linear.hip", "logits.hip",
+           "int4.hip", "api.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -100,6 +100,15 @@ int check_fp8_shape(int64_t M, int64_t N, int64_t K, int32_t r) {
   return QLORA_OK;
 }
 
+// A weight in groups of 4-bit codes.
+int check_int4(const void* codes, const void* scales, int64_t N, int64_t K, int32_t group) {
+  if (!codes || !scales || N <= 0 || K <= 0) return QLORA_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return QLORA_ERR_UNSUPPORTED;
+  if (K % 32 || N > (int64_t)1 << 21 || K > (int64_t)1 << 21 || N * K >= (int64_t)1 << 32)
+    return QLORA_ERR_UNSUPPORTED;
+  return aligned(codes, 16) && aligned(scales, 2) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
+}
+
 // Rows of logits.
 int check_logits(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz, float temperature,
                  qlora::Logits* z) {
@@ -622,6 +631,44 @@ int qlora_fp8_linear_bwd(const uint16_t* dY, int32_t dy_fmt, const uint8_t* x_co
                                           qlora::ConstAct8{w_codes_t, w_scales_t}, A, B, M, N, K, r,
                                           scale, dX, dA, dB, ws,
                                           reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_int4_quantize(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, int32_t group,
+                        uint8_t* codes, uint16_t* scales, uint8_t* zeros, void* stream) {
+  if (!W || ldw < K) return QLORA_ERR_INVALID_ARG;
+  const int st = check_int4(codes, scales, N, K, group);
+  if (st != QLORA_OK) return st;
+  if (!aligned(W, 2) || ldw > (int64_t)1 << 32) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_int4_quantize(W, N, K, ldw, group, codes, scales, zeros,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_int4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                          int64_t N, int64_t K, int32_t group, uint16_t* W, int64_t ldw,
+                          void* stream) {
+  if (!W || ldw < K) return QLORA_ERR_INVALID_ARG;
+  const int st = check_int4(codes, scales, N, K, group);
+  if (st != QLORA_OK) return st;
+  if (!aligned(W, 2) || ldw > (int64_t)1 << 32) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_int4_dequantize(qlora::Int4Weight{codes, scales, zeros, N, K, group}, W,
+                                                  ldw, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8_t* codes,
+                          const uint16_t* scales, const uint8_t* zeros, int64_t N, int64_t K,
+                          int32_t group, void* Y, int32_t y_dtype, int64_t ldy, void* stream) {
+  if (!X || !Y || M <= 0 || ldx < K || ldy < N) return QLORA_ERR_INVALID_ARG;
+  if (y_dtype != QLORA_LOGITS_BF16 && y_dtype != QLORA_LOGITS_F32) return QLORA_ERR_INVALID_ARG;
+  const int st = check_int4(codes, scales, N, K, group);
+  if (st != QLORA_OK) return st;
+  // 32-bit offsets into X; a token tile per row of the grid
+  if (M > (int64_t)1 << 20 || ldx >= (int64_t)1 << 30 || M * ldx >= (int64_t)1 << 30 || ldx % 8 ||
+      ldy > (int64_t)1 << 32)
+    return QLORA_ERR_UNSUPPORTED;
+  if (!aligned(X, 16) || !aligned(Y, y_dtype == QLORA_LOGITS_F32 ? 4 : 2)) return QLORA_ERR_UNSUPPORTED;
+  return hip_status(qlora::launch_int4_linear_fwd(X, M, ldx, qlora::Int4Weight{codes, scales, zeros, N, K, group},
+                                                  Y, y_dtype == QLORA_LOGITS_F32, ldy,
+                                                  reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top) {

@@ -257,6 +257,22 @@ hipError_t launch_distill_fwd(const Logits& z, const TopLogits& t, const float* 
 hipError_t launch_distill_bwd(const Logits& z, const TopLogits& t, const float* stats, const float* g, void* dZ,
                               int64_t lddz, hipStream_t stream);
 
+// ---- 4 bits in groups (int4.hip) --------------------------------------------------
+
+// [N x K] codes, scales bf16 and zero points (null: 8) [N x ceil(K / group)].
+struct Int4Weight {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  int64_t N, K;
+  int group;  // 32, 64 or 128
+};
+hipError_t launch_int4_quantize(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, int group, uint8_t* codes,
+                                uint16_t* scales, uint8_t* zeros, hipStream_t stream);
+hipError_t launch_int4_dequantize(const Int4Weight& w, uint16_t* out, int64_t ldo, hipStream_t stream);
+hipError_t launch_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const Int4Weight& w, void* Y, bool f32,
+                                  int64_t ldy, hipStream_t stream);
+
 // Forward with the library's own scratch array (one per device, this many
 // bytes) in place of a caller workspace.
 constexpr size_t kNoAllocScratchBytes = (size_t)32 << 20;

@@ -628,6 +628,51 @@ int qlora_fp8_linear_bwd(const uint16_t* dY, int32_t dy_fmt, const uint8_t* x_co
                          float scale, uint16_t* dX, float* dA, float* dB, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* ---- 4 bits in groups -----------------------------------------------------------
+ * A weight to serve from, without an adapter (a merged one, qlora_nf4_merge):
+ * W [N x K] in groups of G = 32, 64 or 128 columns of a row, the last of a row
+ * shorter where G does not divide K,
+ *   w = s (q - z)
+ *   codes   uint8 [N][K / 2]: q in [0, 15], column 2i in the low nibble of byte i
+ *   scales  bf16 [N][ceil(K / G)]: s
+ *   zeros   uint8 [N][ceil(K / G)]: z in [0, 15] (the low four bits are read), or
+ *           NULL for z = 8
+ * codes are 16-byte, scales 2-byte aligned. N and K are at most 2^21, K a
+ * multiple of 32, N K below 2^32.
+ *
+ * qlora_int4_quantize — from bf16 W, rows ldw >= K elements apart, over a
+ * group's values (float32 operations, each rounded once):
+ *   zeros given  lo = min(w, 0), hi = max(w, 0), s = bf16((hi - lo) / 15),
+ *                z = the integer nearest to -lo / s, at most 15
+ *   zeros NULL   s = bf16(max|w| / 7), z = 8
+ *   q = the integer nearest to w / s, ties to even, plus z, cut to [0, 15]
+ * A group with s = 0 has z = 0 (zeros NULL: 8) and q = z. Values that are not
+ * finite, or above 2^126, are unsupported.
+ * qlora_int4_dequantize — bf16(s (q - z)), rows ldw >= K apart.
+ * Errors: INVALID_ARG (null pointer, sizes not positive, ldw < K);
+ * UNSUPPORTED (another G, K not a multiple of 32, a size or alignment outside
+ * the above). */
+int qlora_int4_quantize(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, int32_t group,
+                        uint8_t* codes, uint16_t* scales, uint8_t* zeros, void* stream);
+int qlora_int4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
+                          int64_t N, int64_t K, int32_t group, uint16_t* W, int64_t ldw,
+                          void* stream);
+
+/* qlora_int4_linear_fwd — Y = X W^T for few tokens, in one launch and without a
+ * workspace. The products x (q - z) are exact and summed in float32, each
+ * group's sum times s in float32. Any M is served, 64 tokens to a pass over the
+ * weight. A token with an infinity or NaN has NaN in all of its row of Y, and one
+ * above 2^110 may (its products are formed with 16 + q and 16 + z apart).
+ *   X        device bf16 [M x K], rows ldx >= K elements apart, ldx a multiple of 8
+ *            and the base 16-byte aligned
+ *   Y        device [M x N], bf16 or float32 (y_dtype: QLORA_LOGITS_BF16 or
+ *            QLORA_LOGITS_F32), rows ldy >= N apart
+ * Errors: INVALID_ARG (null pointer, sizes not positive, ldx < K, ldy < N, unknown
+ * y_dtype); UNSUPPORTED (as above; M ldx at least 2^30, M above 2^20). */
+int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8_t* codes,
+                          const uint16_t* scales, const uint8_t* zeros, int64_t N, int64_t K,
+                          int32_t group, void* Y, int32_t y_dtype, int64_t ldy, void* stream);
+
 /* ---- rows of logits -------------------------------------------------------------
  * What a model's output layer feeds: T rows of V logits, bf16 (QLORA_LOGITS_BF16,
  * uint16_t bit patterns) or float32 (QLORA_LOGITS_F32), rows ldz >= V elements

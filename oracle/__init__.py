@@ -54,3 +54,4 @@ from . import store  # noqa: F401
 from .adamw8 import BLOCK8, adamw8_step, dequantize_state, num_blocks8, quantize_state  # noqa: F401
 from . import act8  # noqa: F401
 from . import logits  # noqa: F401
+from . import int4  # noqa: F401
