@@ -93,13 +93,27 @@ int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __rest
 
 // ---------------------------------------------------------------------------
 // Y [M x N] = X [M x K] W^T. A workgroup owns 16 kNR weight rows and 16 kMT
-// tokens over the whole K, its waves taking runs of 128 columns in turn. The
-// codes go to the matrix units as bf16 integers, without a table: a nibble
-// moved to bits 3-6 of 0x4180 (16.0) is 16 + q, and a second product with
-// the constant -(16 + z) takes the offset and the zero point away, all of it
-// exact up to the float32 sums; each group's sum is then scaled in float32.
-// The nibbles of a code word come out in the order 0, 4, 1, 5, 2, 6, 3, 7, and
-// the tokens' eight values are put in that order too.
+// tokens over the whole K, its waves taking steps of 128 kRuns columns in turn,
+// the next step's loads in flight while one is computed.
+//
+// Codes. Lane (c, g) loads 16 bytes of weight row c, the 32 columns at 32 g of
+// each run of 128; where a group is shorter, the code words change lanes so
+// that the four lanes of a row hold words of one group at a time. They go to
+// the matrix units as bf16 integers, without a table: a byte times 0x8008 has
+// its two nibbles at bits 3-6 and 19-22, where 0x4180 (16.0) beneath makes them
+// 16 + q. A second product with the constant -(16 + z) takes the offset and the
+// zero point away, all of it exact up to the float32 sums, and each group's sum
+// is scaled in float32.
+//
+// Tokens. Up to 16 (kX > 0): a wave loads its step's columns of every token in
+// kX loads of whole lines and reads the operands back from LDS rows of its own
+// (no barrier: LDS accesses of one wave complete in order). Straight from
+// memory a step takes eight loads in which, for one token, 4 lanes of 64
+// matter, and their return bounds the kernel (32768 x 8192, one token: 48 us).
+// More tokens (kX = 0) are loaded straight into operands.
+//
+// Rows past the end repeat the last one, tokens past it are 0 or repeat it;
+// their sums are not stored.
 
 constexpr int kWaves = 8;
 constexpr int kOut = 0x7ffffff0;  // an offset past every range: the load returns 0
@@ -114,121 +128,304 @@ struct Int4Args {
   int f32;
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int64_t bytes) {
-  if (bytes > 0x7ffffff0LL) bytes = 0x7ffffff0LL;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+// The code word's eight values 16 + q, in order. mask 0x00780078 and base
+// 0x41804180 come in registers: as constants they make two instructions of one
+// for want of operands.
+__device__ __forceinline__ u32x4 nibbles_bf16(uint32_t w, uint32_t mask, uint32_t base) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (__umul24((w >> (8 * i)) & 0xffu, 0x8008u) & mask) | base;
+  return r;
 }
 
-__device__ __forceinline__ u32x4 nibbles_bf16(uint32_t w) {
-  constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
-  return u32x4{((w << 3) & kMask) | kBase, ((w >> 1) & kMask) | kBase, ((w >> 5) & kMask) | kBase,
-               ((w >> 9) & kMask) | kBase};
-}
-__device__ __forceinline__ u32x4 nibble_order(const u32x4& v) {
-  return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-               __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+// kBytes (a power of two) at any address, as words (the last one's upper bytes 0).
+template <int kBytes>
+__device__ __forceinline__ void load_bytes(uint32_t* w, const void* p) {
+  typedef uint16_t u16_1 __attribute__((aligned(1)));
+  typedef uint32_t u32_1 __attribute__((aligned(1)));
+  typedef u32x2 u32x2_1 __attribute__((aligned(1)));
+  typedef u32x4 u32x4_1 __attribute__((aligned(1)));
+  if constexpr (kBytes == 1) {
+    w[0] = *reinterpret_cast<const uint8_t*>(p);
+  } else if constexpr (kBytes == 2) {
+    w[0] = *reinterpret_cast<const u16_1*>(p);
+  } else if constexpr (kBytes == 4) {
+    w[0] = *reinterpret_cast<const u32_1*>(p);
+  } else if constexpr (kBytes == 8) {
+    const u32x2 v = *reinterpret_cast<const u32x2_1*>(p);
+    w[0] = v[0];
+    w[1] = v[1];
+  } else {
+    const u32x4 v = *reinterpret_cast<const u32x4_1*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v[i];
+  }
 }
 
-template <int kG, int kMT, int kNR>
+// Swaps the upper 32 lanes of a with the lower 32 of b; the odd rows of 16
+// lanes of a with the even ones of b.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+// First column, within a run, of the eight of lane group g in product t (of
+// four): those of its own code word t, or of the word that comes to it.
+template <int kG>
+__device__ __forceinline__ int column_of(int t, int g) {
+  if constexpr (kG == 128) return 32 * g + 8 * t;
+  if constexpr (kG == 64) return 64 * (t >> 1) + 32 * (g & 1) + 16 * (g >> 1) + 8 * (t & 1);
+  return 32 * t + 8 * g;
+}
+template <int kG>
+__device__ __forceinline__ void to_groups(uint32_t (&w)[4]) {
+  if constexpr (kG < 128) {
+    swap32(w[0], w[2]);
+    swap32(w[1], w[3]);
+  }
+  if constexpr (kG == 32) {
+    swap16(w[0], w[1]);
+    swap16(w[2], w[3]);
+  }
+}
+
+// Where a lane reads.
+template <int kX, int kMT, int kNR>
+struct Lane {
+  static constexpr int kRows = kX ? kX : kMT;
+  uint32_t code[kNR];   // byte of its first code
+  uint32_t group[kNR];  // its row's first group
+  int token[kRows];     // byte in x of its first value of each load
+  __amdgpu_buffer_rsrc_t x;
+  uint32_t put, get[4];  // LDS bytes: of its first load's values, of its operands in a run
+};
+
+template <int kG, bool kZ, int kX, int kMT, int kNR, int kRuns>
+struct Int4Step {
+  static constexpr int kColumns = 128 * kRuns;
+  static constexpr int kGroups = kColumns / kG;
+  static constexpr int kPitch = kColumns * 2 + 16;  // LDS bytes of a token's row
+  static constexpr int kPer = kX ? 512 / kColumns : 0;  // tokens of a load of whole rows
+  static_assert(kX == 0 || kMT == 1);
+  using At = Lane<kX, kMT, kNR>;
+  uint32_t w[kNR][kRuns][4];
+  uint32_t s[kNR][(kGroups + 1) / 2], z[kNR][(kGroups + 3) / 4];
+  u32x4 x[kX ? kX : kMT * kRuns * 4];
+
+  __device__ __forceinline__ static u32x4 load_x(const At& at, int m, int bytes, int k0) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(at.x, at.token[m] + bytes, k0 * 2, 0));
+  }
+  // kTail: the end of the rows; what lies past it is 0. Otherwise loads alone
+  // and no branch, so that waits can count them.
+  template <bool kTail>
+  __device__ __forceinline__ void load(const Int4Args& a, int k0, const At& at, int lane) {
+    const int K = (int)a.K, g = lane >> 4;
+    const uint8_t* codes = a.codes + k0 / 2;
+    const uint16_t* scales = a.scales + k0 / kG;
+    const uint8_t* zeros = a.zeros + k0 / kG;
+#pragma unroll
+    for (int r = 0; r < kNR; ++r) {
+#pragma unroll
+      for (int n = 0; n < kRuns; ++n) {
+        if (kTail && k0 + 128 * n + 32 * g >= K) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[r][n][e] = 0;
+        } else {
+          load_bytes<16>(w[r][n], codes + at.code[r] + n * 64);
+        }
+      }
+      if constexpr (kTail) {
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          if (j % 2 == 0) s[r][j / 2] = 0;
+          if (j % 4 == 0) z[r][j / 4] = 0;
+          if (k0 + kG * j < K) {
+            s[r][j / 2] |= (uint32_t)scales[at.group[r] + j] << (16 * (j & 1));
+            z[r][j / 4] |= (kZ ? (uint32_t)zeros[at.group[r] + j] : 8u) << (8 * (j & 3));
+          }
+        }
+      } else {
+        load_bytes<kGroups * 2>(s[r], scales + at.group[r]);
+#pragma unroll
+        for (int j = 0; j < (kGroups + 3) / 4; ++j) z[r][j] = 0x08080808u;
+        if constexpr (kZ) load_bytes<kGroups>(z[r], zeros + at.group[r]);
+      }
+    }
+    if constexpr (kX > 0) {
+      const bool in = !kTail || k0 + (lane % (kColumns / 8)) * 8 < K;
+#pragma unroll
+      for (int m = 0; m < kX; ++m) {
+        if (kTail) x[m] = u32x4{0, 0, 0, 0};
+        if (in) x[m] = load_x(at, m, 0, k0);
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int n = 0; n < kRuns; ++n)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            // the lane part of column_of is in at.token, the rest known here
+            const int c = column_of<kG>(t, 0) + 128 * n;
+            u32x4& v = x[(m * kRuns + n) * 4 + t];
+            if (kTail) v = u32x4{0, 0, 0, 0};
+            if (!kTail || k0 + 128 * n + column_of<kG>(t, g) < K) v = load_x(at, m, c * 2, k0);
+          }
+    }
+  }
+
+  __device__ __forceinline__ void add(floatx4 (&acc)[kMT][kNR], const At& at, uint8_t* lds, uint32_t mask,
+                                      uint32_t base) {
+    const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (kX > 0) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int m = 0; m < kX; ++m) *reinterpret_cast<u32x4*>(lds + at.put + m * (kPer * kPitch)) = x[m];
+      asm volatile("" ::: "memory");
+    }
+#pragma unroll
+    for (int n = 0; n < kRuns; ++n) {
+      bf16x8 t[kMT][4];
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kX > 0)
+            t[m][i] = as_bf16x8(*reinterpret_cast<const u32x4*>(lds + at.get[i] + n * 256));
+          else
+            t[m][i] = as_bf16x8(x[(m * kRuns + n) * 4 + i]);
+        }
+#pragma unroll
+      for (int r = 0; r < kNR; ++r) {
+        to_groups<kG>(w[r][n]);
+        floatx4 p[kMT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = (128 * n + 32 * i) / kG;  // the product's group
+          const bool begins = (32 * i) % kG == 0, ends = (32 * (i + 1)) % kG == 0;
+          const uint32_t off = (0xc180u | (((z[r][j / 4] >> (8 * (j & 3))) & 15u) << 3)) * 0x10001u;  // -(16 + z), twice
+          const bf16x8 of = as_bf16x8(u32x4{off, off, off, off});
+          const bf16x8 q = as_bf16x8(nibbles_bf16(w[r][n][i], mask, base));
+#pragma unroll
+          for (int m = 0; m < kMT; ++m) {
+            p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[m][i], q, begins ? zero : p[m], 0, 0, 0);
+            p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[m][i], of, p[m], 0, 0, 0);
+          }
+          if (ends) {
+            const uint32_t sw = s[r][j / 2];
+            const float sc = (j & 1) ? bf16_hi(sw) : bf16_lo(sw);
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[m][r][v] = __builtin_fmaf(sc, p[m][v], acc[m][r][v]);
+          }
+        }
+      }
+    }
+    if constexpr (kX > 0) asm volatile("" ::: "memory");
+  }
+};
+
+template <int kG, bool kZ, int kX, int kMT, int kNR, int kRuns>
 __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
-  constexpr int kGroups = 128 / kG;  // groups of a run
-  constexpr int kWords = kG / 32;    // code words a lane holds of a group
-  __shared__ floatx4 s_red[kWaves][kMT * kNR][64];
+  using Step = Int4Step<kG, kZ, kX, kMT, kNR, kRuns>;
+  using At = typename Step::At;
+  constexpr int kColumns = Step::kColumns, kPitch = Step::kPitch;
+  constexpr int kTokenLds = kX ? kX * Step::kPer * kPitch : 0;  // of a wave
+  constexpr int kRedLds = kMT * kNR * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t s_mem[kWaves * (kTokenLds > kRedLds ? kTokenLds : kRedLds)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * kNR), m0 = (int64_t)blockIdx.y * (16 * kMT);
   const int K = (int)a.K;
-  const __amdgpu_buffer_rsrc_t rc = rsrc_of(a.codes, a.N * a.K / 2);
-  const __amdgpu_buffer_rsrc_t rs = rsrc_of(a.scales, a.N * a.ng * 2);
-  const __amdgpu_buffer_rsrc_t rz = rsrc_of(a.zeros, a.zeros ? a.N * a.ng : 0);
-  const __amdgpu_buffer_rsrc_t rx = rsrc_of(a.X, ((a.M - 1) * a.ldx + K) * 2);
-  const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  uint8_t* lds = s_mem + wave * kTokenLds;
+  At at;
+  at.x = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.X), (short)0, (int)(((a.M - 1) * a.ldx + K) * 2), 0x00020000);
+#pragma unroll
+  for (int r = 0; r < kNR; ++r) {
+    const int64_t n = n0 + 16 * r + c < a.N ? n0 + 16 * r + c : a.N - 1;
+    at.code[r] = (uint32_t)(n * K / 2) + 16 * g;
+    at.group[r] = (uint32_t)(n * a.ng);
+  }
+  if constexpr (kX > 0) {
+    constexpr int kLanes = kColumns / 8;  // lanes to a token's row
+#pragma unroll
+    for (int m = 0; m < kX; ++m) {
+      const int64_t t = m * Step::kPer + lane / kLanes;
+      at.token[m] = (int)(((t < a.M ? t : a.M - 1) * a.ldx + (lane % kLanes) * 8) * 2);
+    }
+    at.put = (uint32_t)((lane / kLanes) * kPitch + (lane % kLanes) * 16);
+    const int row = c < a.M ? c : (int)a.M - 1;  // below kX kPer, which is at least min(M, 16)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at.get[i] = (uint32_t)(row * kPitch + column_of<kG>(i, g) * 2);
+  } else {
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      const int64_t t = m0 + 16 * m + c;
+      at.token[m] = t < a.M ? (int)((t * a.ldx + column_of<kG>(0, g)) * 2) : kOut;
+    }
+  }
   floatx4 acc[kMT][kNR];
 #pragma unroll
   for (int m = 0; m < kMT; ++m)
 #pragma unroll
-    for (int r = 0; r < kNR; ++r) acc[m][r] = zero;
+    for (int r = 0; r < kNR; ++r) acc[m][r] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int k0 = wave * 128; k0 < K; k0 += kWaves * 128) {
-    uint32_t w[kNR][kGroups][kWords];
-    uint32_t s[kNR][kGroups], z[kNR][kGroups];
-    u32x4 x[kMT][kGroups][kWords];
-#pragma unroll
-    for (int r = 0; r < kNR; ++r) {
-      const int64_t n = n0 + 16 * r + c;
-#pragma unroll
-      for (int j = 0; j < kGroups; ++j) {
-        const int k = k0 + kG * j + (kG / 4) * g;
-        const int at = n < a.N && k < K ? (int)((n * K + k) / 2) : kOut;
-        if constexpr (kWords == 4) {
-          const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0));
-          w[r][j][0] = v[0]; w[r][j][1] = v[1]; w[r][j][2] = v[2]; w[r][j][3] = v[3];
-        } else if constexpr (kWords == 2) {
-          const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, at, 0, 0));
-          w[r][j][0] = v[0]; w[r][j][1] = v[1];
-        } else {
-          w[r][j][0] = __builtin_amdgcn_raw_buffer_load_b32(rc, at, 0, 0);
-        }
-        const int b = n < a.N && k0 + kG * j < K ? (int)(n * a.ng + k0 / kG + j) : -1;
-        s[r][j] = __builtin_amdgcn_raw_buffer_load_b16(rs, b >= 0 ? b * 2 : kOut, 0, 0);
-        z[r][j] = a.zeros ? __builtin_amdgcn_raw_buffer_load_b8(rz, b >= 0 ? b : kOut, 0, 0) : 8u;
-      }
+  uint32_t mask = 0x00780078u, base = 0x41804180u;
+  asm("" : "+v"(mask));
+  asm("" : "+s"(base));
+  const int whole = K / kColumns;                         // steps; this wave's are wave, wave + kWaves, ...
+  const int left = (whole - wave + kWaves - 1) / kWaves;  // ... so many
+  auto column = [&](int i) { return (wave + i * kWaves) * kColumns; };
+  if (left > 0) {
+    Step even, odd;
+    even.template load<false>(a, column(0), at, lane);
+    int i = 0;
+    for (; i + 2 < left; i += 2) {
+      odd.template load<false>(a, column(i + 1), at, lane);
+      __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the sums
+      even.add(acc, at, lds, mask, base);
+      __builtin_amdgcn_sched_barrier(0);
+      even.template load<false>(a, column(i + 2), at, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      odd.add(acc, at, lds, mask, base);
+      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      const int64_t t = m0 + 16 * m + c;
-#pragma unroll
-      for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-        for (int e = 0; e < kWords; ++e) {
-          const int k = k0 + kG * j + (kG / 4) * g + 8 * e;
-          x[m][j][e] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         rx, t < a.M && k < K ? (int)((t * a.ldx + k) * 2) : kOut, 0, 0));
-        }
+    if (i + 1 < left) {
+      odd.template load<false>(a, column(i + 1), at, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      even.add(acc, at, lds, mask, base);
+      odd.add(acc, at, lds, mask, base);
+    } else {
+      even.add(acc, at, lds, mask, base);
     }
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      bf16x8 xf[kMT][kWords];
-#pragma unroll
-      for (int m = 0; m < kMT; ++m)
-#pragma unroll
-        for (int e = 0; e < kWords; ++e) xf[m][e] = as_bf16x8(nibble_order(x[m][j][e]));
-#pragma unroll
-      for (int r = 0; r < kNR; ++r) {
-        const float sc = __builtin_bit_cast(float, s[r][j] << 16);
-        const uint32_t off = (0xc180u | ((z[r][j] & 15u) << 3)) * 0x10001u;  // -(16 + z), twice
-        const bf16x8 of = as_bf16x8(u32x4{off, off, off, off});
-        floatx4 p[kMT];
-#pragma unroll
-        for (int e = 0; e < kWords; ++e) {
-          const bf16x8 q = as_bf16x8(nibbles_bf16(w[r][j][e]));
-#pragma unroll
-          for (int m = 0; m < kMT; ++m) {
-            p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m][e], q, e ? p[m] : zero, 0, 0, 0);
-            p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m][e], of, p[m], 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < kMT; ++m)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[m][r][v] = __builtin_fmaf(sc, p[m][v], acc[m][r][v]);
-      }
-    }
+  }
+  if (whole * kColumns < K && wave == whole % kWaves) {
+    Step tail;
+    tail.template load<true>(a, whole * kColumns, at, lane);
+    tail.add(acc, at, lds, mask, base);
   }
   // the waves' sums, added in the order of the waves; lane (c, g) holds tokens
   // 4 g .. 4 g + 3 of weight row c
+  floatx4* s_red = reinterpret_cast<floatx4*>(s_mem);
+  if constexpr (kX > 0) __syncthreads();  // the tokens' rows are done with
 #pragma unroll
   for (int m = 0; m < kMT; ++m)
 #pragma unroll
-    for (int r = 0; r < kNR; ++r) s_red[wave][m * kNR + r][lane] = acc[m][r];
+    for (int r = 0; r < kNR; ++r) s_red[(wave * kMT * kNR + m * kNR + r) * 64 + lane] = acc[m][r];
   __syncthreads();
   for (int i = wave; i < kMT * kNR; i += kWaves) {
-    floatx4 y = s_red[0][i][lane];
+    floatx4 y = s_red[i * 64 + lane];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) {
-      const floatx4 u = s_red[w][i][lane];
+      const floatx4 u = s_red[(w * kMT * kNR + i) * 64 + lane];
 #pragma unroll
       for (int v = 0; v < 4; ++v) y[v] += u[v];
     }
@@ -245,10 +442,13 @@ __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
   }
 }
 
-template <int kG, int kMT, int kNR>
+template <int kG, int kX, int kMT, int kNR, int kRuns>
 hipError_t run_linear(const Int4Args& a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.N + 16 * kNR - 1) / (16 * kNR)), (unsigned)((a.M + 16 * kMT - 1) / (16 * kMT)));
-  int4_linear_kernel<kG, kMT, kNR><<<grid, dim3(kWaves * 64), 0, stream>>>(a);
+  if (a.zeros)
+    int4_linear_kernel<kG, true, kX, kMT, kNR, kRuns><<<grid, dim3(kWaves * 64), 0, stream>>>(a);
+  else
+    int4_linear_kernel<kG, false, kX, kMT, kNR, kRuns><<<grid, dim3(kWaves * 64), 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -290,10 +490,12 @@ hipError_t launch_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, con
   Int4Args a{X, w.codes, w.scales, w.zeros, M, w.N, w.K, (w.K + w.group - 1) / w.group, ldx, ldy, Y, f32};
   return by_group(w.group, [&](auto g) {
     constexpr int kG = decltype(g)::value;
-    if (M <= 16) return run_linear<kG, 1, 1>(a, stream);
-    if (M <= 32) return run_linear<kG, 2, 1>(a, stream);
-    if (M <= 48) return run_linear<kG, 3, 1>(a, stream);
-    return run_linear<kG, 4, 1>(a, stream);
+    if (M <= 2) return run_linear<kG, 1, 1, 1, 2>(a, stream);
+    if (M <= 8) return run_linear<kG, 4, 1, 1, 2>(a, stream);
+    if (M <= 16) return run_linear<kG, 8, 1, 1, 2>(a, stream);
+    if (M <= 32) return run_linear<kG, 0, 2, 2, 1>(a, stream);
+    if (M <= 48) return run_linear<kG, 0, 3, 2, 1>(a, stream);
+    return run_linear<kG, 0, 4, 2, 1>(a, stream);
   });
 }
 
