@@ -5,6 +5,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <atomic>
 
 namespace qlora {
 
@@ -96,7 +97,14 @@ int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __rest
 // tokens over the whole K, its waves taking steps of 128 kRuns columns in turn,
 // the next step's loads in flight while one is computed.
 //
-// Codes. Lane (c, g) loads 16 bytes of weight row c, the 32 columns at 32 g of
+// Loads are of whole lines, four neighbouring lanes to 64 bytes of a row, and
+// the values reach the lanes that multiply them, (c, g) = (lane & 15, lane >> 4),
+// by way of LDS rows of the wave's own (no barrier: LDS accesses of one wave
+// complete in order). Loaded by the lanes that multiply them, 16 bytes each from
+// another row than its neighbour's, they took one pass of the memory pipe a
+// lane, which bounded the kernel (32768 x 8192, one token: 39 us).
+//
+// Codes. A lane multiplies 16 bytes of weight row c, the 32 columns at 32 g of
 // each run of 128; where a group is shorter, the code words change lanes so
 // that the four lanes of a row hold words of one group at a time. They go to
 // the matrix units as bf16 integers, without a table: a byte times 0x8008 has
@@ -105,18 +113,9 @@ int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __rest
 // zero point away, all of it exact up to the float32 sums, and each group's sum
 // is scaled in float32.
 //
-// Tokens. Up to 16 (kX > 0): a wave loads its step's columns of every token in
-// kX loads of whole lines and reads the operands back from LDS rows of its own
-// (no barrier: LDS accesses of one wave complete in order). Straight from
-// memory a step takes eight loads in which, for one token, 4 lanes of 64
-// matter, and their return bounds the kernel (32768 x 8192, one token: 48 us).
-// More tokens (kX = 0) are loaded straight into operands.
-//
-// Rows past the end repeat the last one, tokens past it are 0 or repeat it;
-// their sums are not stored.
+// Rows and tokens past the end repeat the last one; their sums are not stored.
 
 constexpr int kWaves = 8;
-constexpr int kOut = 0x7ffffff0;  // an offset past every range: the load returns 0
 
 struct Int4Args {
   const uint16_t* X;
@@ -162,6 +161,12 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, const void* p) {
   }
 }
 
+__device__ __forceinline__ void load_lds(uint32_t (&w)[4], const uint8_t* p) {
+  const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = v[i];
+}
+
 // Swaps the upper 32 lanes of a with the lower 32 of b; the odd rows of 16
 // lanes of a with the even ones of b.
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
@@ -195,37 +200,42 @@ __device__ __forceinline__ void to_groups(uint32_t (&w)[4]) {
   }
 }
 
-// Where a lane reads.
-template <int kX, int kMT, int kNR>
+// Where a lane loads and what LDS bytes it takes its operands from.
+template <int kX, int kNR>
 struct Lane {
-  static constexpr int kRows = kX ? kX : kMT;
   uint32_t code[kNR];   // byte of its first code
   uint32_t group[kNR];  // its row's first group
-  int token[kRows];     // byte in x of its first value of each load
+  int token[kX];        // byte in x of its first value of each load
   __amdgpu_buffer_rsrc_t x;
-  uint32_t put, get[4];  // LDS bytes: of its first load's values, of its operands in a run
+  uint32_t put;      // of its first load's token values
+  uint32_t get[4];   // of its token operands in a run
+  uint32_t code_get; // of its codes in a run
+  int from;          // the lane, times 4, that loads its row's scales
 };
 
-template <int kG, bool kZ, int kX, int kMT, int kNR, int kRuns>
+// Four lanes load a row's 64 bytes of a run; lane i of them takes piece
+// i ^ swizzle(row), so that the reads, one piece of 16 rows, spread over the
+// banks.
+__device__ __forceinline__ int swizzle(int row) { return (row >> 2) & 3; }
+
+template <int kG, bool kZ, int kMT, int kNR, int kRuns, int kX>
 struct Int4Step {
   static constexpr int kColumns = 128 * kRuns;
   static constexpr int kGroups = kColumns / kG;
   static constexpr int kPitch = kColumns * 2 + 16;  // LDS bytes of a token's row
-  static constexpr int kPer = kX ? 512 / kColumns : 0;  // tokens of a load of whole rows
-  static_assert(kX == 0 || kMT == 1);
-  using At = Lane<kX, kMT, kNR>;
+  static constexpr int kPer = 512 / kColumns;       // tokens of a load
+  static constexpr int kTokenLds = kX * kPer * kPitch;
+  static constexpr int kLds = kTokenLds + kNR * kRuns * 1024;  // of a wave: tokens, codes
+  using At = Lane<kX, kNR>;
   uint32_t w[kNR][kRuns][4];
   uint32_t s[kNR][(kGroups + 1) / 2], z[kNR][(kGroups + 3) / 4];
-  u32x4 x[kX ? kX : kMT * kRuns * 4];
+  u32x4 x[kX];
 
-  __device__ __forceinline__ static u32x4 load_x(const At& at, int m, int bytes, int k0) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(at.x, at.token[m] + bytes, k0 * 2, 0));
-  }
   // kTail: the end of the rows; what lies past it is 0. Otherwise loads alone
   // and no branch, so that waits can count them.
   template <bool kTail>
   __device__ __forceinline__ void load(const Int4Args& a, int k0, const At& at, int lane) {
-    const int K = (int)a.K, g = lane >> 4;
+    const int K = (int)a.K;
     const uint8_t* codes = a.codes + k0 / 2;
     const uint16_t* scales = a.scales + k0 / kG;
     const uint8_t* zeros = a.zeros + k0 / kG;
@@ -233,7 +243,7 @@ struct Int4Step {
     for (int r = 0; r < kNR; ++r) {
 #pragma unroll
       for (int n = 0; n < kRuns; ++n) {
-        if (kTail && k0 + 128 * n + 32 * g >= K) {
+        if (kTail && k0 + 128 * n + 32 * ((lane & 3) ^ swizzle(lane >> 2)) >= K) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[r][n][e] = 0;
         } else {
@@ -257,53 +267,50 @@ struct Int4Step {
         if constexpr (kZ) load_bytes<kGroups>(z[r], zeros + at.group[r]);
       }
     }
-    if constexpr (kX > 0) {
-      const bool in = !kTail || k0 + (lane % (kColumns / 8)) * 8 < K;
+    const bool in = !kTail || k0 + (lane % (kColumns / 8)) * 8 < K;
 #pragma unroll
-      for (int m = 0; m < kX; ++m) {
-        if (kTail) x[m] = u32x4{0, 0, 0, 0};
-        if (in) x[m] = load_x(at, m, 0, k0);
-      }
-    } else {
-#pragma unroll
-      for (int m = 0; m < kMT; ++m)
-#pragma unroll
-        for (int n = 0; n < kRuns; ++n)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            // the lane part of column_of is in at.token, the rest known here
-            const int c = column_of<kG>(t, 0) + 128 * n;
-            u32x4& v = x[(m * kRuns + n) * 4 + t];
-            if (kTail) v = u32x4{0, 0, 0, 0};
-            if (!kTail || k0 + 128 * n + column_of<kG>(t, g) < K) v = load_x(at, m, c * 2, k0);
-          }
+    for (int m = 0; m < kX; ++m) {
+      if (kTail) x[m] = u32x4{0, 0, 0, 0};
+      if (in) x[m] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(at.x, at.token[m], k0 * 2, 0));
     }
   }
 
-  __device__ __forceinline__ void add(floatx4 (&acc)[kMT][kNR], const At& at, uint8_t* lds, uint32_t mask,
+  __device__ __forceinline__ void add(floatx4 (&acc)[kMT][kNR], const At& at, uint8_t* lds, int lane, uint32_t mask,
                                       uint32_t base) {
     const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (kX > 0) {
-      asm volatile("" ::: "memory");
+    uint8_t* lds_codes = lds + kTokenLds;
+    asm volatile("" ::: "memory");
 #pragma unroll
-      for (int m = 0; m < kX; ++m) *reinterpret_cast<u32x4*>(lds + at.put + m * (kPer * kPitch)) = x[m];
-      asm volatile("" ::: "memory");
+    for (int r = 0; r < kNR; ++r)
+#pragma unroll
+      for (int n = 0; n < kRuns; ++n)
+        *reinterpret_cast<u32x4*>(lds_codes + (r * kRuns + n) * 1024 + lane * 16) =
+            u32x4{w[r][n][0], w[r][n][1], w[r][n][2], w[r][n][3]};
+#pragma unroll
+    for (int m = 0; m < kX; ++m) *reinterpret_cast<u32x4*>(lds + at.put + m * (kPer * kPitch)) = x[m];
+#pragma unroll
+    for (int r = 0; r < kNR; ++r) {
+#pragma unroll
+      for (int j = 0; j < (kGroups + 1) / 2; ++j) s[r][j] = __builtin_amdgcn_ds_bpermute(at.from, s[r][j]);
+      if constexpr (kZ) {
+#pragma unroll
+        for (int j = 0; j < (kGroups + 3) / 4; ++j) z[r][j] = __builtin_amdgcn_ds_bpermute(at.from, z[r][j]);
+      }
     }
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int n = 0; n < kRuns; ++n) {
       bf16x8 t[kMT][4];
 #pragma unroll
       for (int m = 0; m < kMT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (kX > 0)
-            t[m][i] = as_bf16x8(*reinterpret_cast<const u32x4*>(lds + at.get[i] + n * 256));
-          else
-            t[m][i] = as_bf16x8(x[(m * kRuns + n) * 4 + i]);
-        }
+        for (int i = 0; i < 4; ++i)
+          t[m][i] = as_bf16x8(*reinterpret_cast<const u32x4*>(lds + at.get[i] + m * (16 * kPitch) + n * 256));
 #pragma unroll
       for (int r = 0; r < kNR; ++r) {
-        to_groups<kG>(w[r][n]);
+        uint32_t c[4];
+        load_lds(c, lds_codes + (r * kRuns + n) * 1024 + at.code_get);
+        to_groups<kG>(c);
         floatx4 p[kMT];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -311,7 +318,7 @@ struct Int4Step {
           const bool begins = (32 * i) % kG == 0, ends = (32 * (i + 1)) % kG == 0;
           const uint32_t off = (0xc180u | (((z[r][j / 4] >> (8 * (j & 3))) & 15u) << 3)) * 0x10001u;  // -(16 + z), twice
           const bf16x8 of = as_bf16x8(u32x4{off, off, off, off});
-          const bf16x8 q = as_bf16x8(nibbles_bf16(w[r][n][i], mask, base));
+          const bf16x8 q = as_bf16x8(nibbles_bf16(c[i], mask, base));
 #pragma unroll
           for (int m = 0; m < kMT; ++m) {
             p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[m][i], q, begins ? zero : p[m], 0, 0, 0);
@@ -328,49 +335,44 @@ struct Int4Step {
         }
       }
     }
-    if constexpr (kX > 0) asm volatile("" ::: "memory");
+    asm volatile("" ::: "memory");
   }
 };
 
-template <int kG, bool kZ, int kX, int kMT, int kNR, int kRuns>
+template <int kG, bool kZ, int kMT, int kNR, int kRuns, int kX>
 __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
-  using Step = Int4Step<kG, kZ, kX, kMT, kNR, kRuns>;
-  using At = typename Step::At;
+  using Step = Int4Step<kG, kZ, kMT, kNR, kRuns, kX>;
   constexpr int kColumns = Step::kColumns, kPitch = Step::kPitch;
-  constexpr int kTokenLds = kX ? kX * Step::kPer * kPitch : 0;  // of a wave
-  constexpr int kRedLds = kMT * kNR * 1024;
-  __shared__ __attribute__((aligned(16))) uint8_t s_mem[kWaves * (kTokenLds > kRedLds ? kTokenLds : kRedLds)];
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_mem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * kNR), m0 = (int64_t)blockIdx.y * (16 * kMT);
   const int K = (int)a.K;
-  uint8_t* lds = s_mem + wave * kTokenLds;
-  At at;
+  uint8_t* lds = s_mem + wave * Step::kLds;
+  typename Step::At at;
   at.x = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.X), (short)0, (int)(((a.M - 1) * a.ldx + K) * 2), 0x00020000);
+  {
+    const int row = lane >> 2, piece = (lane & 3) ^ swizzle(row);
 #pragma unroll
-  for (int r = 0; r < kNR; ++r) {
-    const int64_t n = n0 + 16 * r + c < a.N ? n0 + 16 * r + c : a.N - 1;
-    at.code[r] = (uint32_t)(n * K / 2) + 16 * g;
-    at.group[r] = (uint32_t)(n * a.ng);
-  }
-  if constexpr (kX > 0) {
+    for (int r = 0; r < kNR; ++r) {
+      const int64_t n = n0 + 16 * r + row < a.N ? n0 + 16 * r + row : a.N - 1;
+      at.code[r] = (uint32_t)(n * K / 2) + 16 * piece;
+      at.group[r] = (uint32_t)(n * a.ng);
+    }
+    at.from = c * 16;  // lane 4 c
+    at.code_get = (uint32_t)(c * 64 + (g ^ swizzle(c)) * 16);
     constexpr int kLanes = kColumns / 8;  // lanes to a token's row
 #pragma unroll
     for (int m = 0; m < kX; ++m) {
-      const int64_t t = m * Step::kPer + lane / kLanes;
+      const int64_t t = m0 + m * Step::kPer + lane / kLanes;
       at.token[m] = (int)(((t < a.M ? t : a.M - 1) * a.ldx + (lane % kLanes) * 8) * 2);
     }
     at.put = (uint32_t)((lane / kLanes) * kPitch + (lane % kLanes) * 16);
-    const int row = c < a.M ? c : (int)a.M - 1;  // below kX kPer, which is at least min(M, 16)
+    // fewer tokens than 16 are loaded where kX kPer is less: the last repeats
+    const int t = kX * Step::kPer < 16 && c >= kX * Step::kPer ? kX * Step::kPer - 1 : c;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) at.get[i] = (uint32_t)(row * kPitch + column_of<kG>(i, g) * 2);
-  } else {
-#pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      const int64_t t = m0 + 16 * m + c;
-      at.token[m] = t < a.M ? (int)((t * a.ldx + column_of<kG>(0, g)) * 2) : kOut;
-    }
+    for (int i = 0; i < 4; ++i) at.get[i] = (uint32_t)(t * kPitch + column_of<kG>(i, g) * 2);
   }
   floatx4 acc[kMT][kNR];
 #pragma unroll
@@ -391,31 +393,31 @@ __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
     for (; i + 2 < left; i += 2) {
       odd.template load<false>(a, column(i + 1), at, lane);
       __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the sums
-      even.add(acc, at, lds, mask, base);
+      even.add(acc, at, lds, lane, mask, base);
       __builtin_amdgcn_sched_barrier(0);
       even.template load<false>(a, column(i + 2), at, lane);
       __builtin_amdgcn_sched_barrier(0);
-      odd.add(acc, at, lds, mask, base);
+      odd.add(acc, at, lds, lane, mask, base);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (i + 1 < left) {
       odd.template load<false>(a, column(i + 1), at, lane);
       __builtin_amdgcn_sched_barrier(0);
-      even.add(acc, at, lds, mask, base);
-      odd.add(acc, at, lds, mask, base);
+      even.add(acc, at, lds, lane, mask, base);
+      odd.add(acc, at, lds, lane, mask, base);
     } else {
-      even.add(acc, at, lds, mask, base);
+      even.add(acc, at, lds, lane, mask, base);
     }
   }
   if (whole * kColumns < K && wave == whole % kWaves) {
     Step tail;
     tail.template load<true>(a, whole * kColumns, at, lane);
-    tail.add(acc, at, lds, mask, base);
+    tail.add(acc, at, lds, lane, mask, base);
   }
   // the waves' sums, added in the order of the waves; lane (c, g) holds tokens
   // 4 g .. 4 g + 3 of weight row c
   floatx4* s_red = reinterpret_cast<floatx4*>(s_mem);
-  if constexpr (kX > 0) __syncthreads();  // the tokens' rows are done with
+  __syncthreads();  // the steps' LDS is done with
 #pragma unroll
   for (int m = 0; m < kMT; ++m)
 #pragma unroll
@@ -442,14 +444,31 @@ __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
   }
 }
 
-template <int kG, int kX, int kMT, int kNR, int kRuns>
-hipError_t run_linear(const Int4Args& a, hipStream_t stream) {
+template <int kG, bool kZ, int kMT, int kNR, int kRuns, int kX>
+hipError_t run_kernel(const Int4Args& a, hipStream_t stream) {
+  using Step = Int4Step<kG, kZ, kMT, kNR, kRuns, kX>;
+  constexpr int kLds = kWaves * std::max(Step::kLds, kMT * kNR * 1024);
+  auto kern = int4_linear_kernel<kG, kZ, kMT, kNR, kRuns, kX>;
+  if constexpr (kLds > 65536) {  // the limit on dynamic LDS, raised once per device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(raised.load(std::memory_order_acquire) & bit)) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+      if (e != hipSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_acq_rel);
+    }
+  }
   const dim3 grid((unsigned)((a.N + 16 * kNR - 1) / (16 * kNR)), (unsigned)((a.M + 16 * kMT - 1) / (16 * kMT)));
-  if (a.zeros)
-    int4_linear_kernel<kG, true, kX, kMT, kNR, kRuns><<<grid, dim3(kWaves * 64), 0, stream>>>(a);
-  else
-    int4_linear_kernel<kG, false, kX, kMT, kNR, kRuns><<<grid, dim3(kWaves * 64), 0, stream>>>(a);
+  kern<<<grid, dim3(kWaves * 64), kLds, stream>>>(a);
   return hipGetLastError();
+}
+template <int kG, int kMT, int kNR, int kRuns, int kX>
+hipError_t run_linear(const Int4Args& a, hipStream_t stream) {
+  return a.zeros ? run_kernel<kG, true, kMT, kNR, kRuns, kX>(a, stream)
+                 : run_kernel<kG, false, kMT, kNR, kRuns, kX>(a, stream);
 }
 
 template <typename F>
@@ -490,12 +509,12 @@ hipError_t launch_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, con
   Int4Args a{X, w.codes, w.scales, w.zeros, M, w.N, w.K, (w.K + w.group - 1) / w.group, ldx, ldy, Y, f32};
   return by_group(w.group, [&](auto g) {
     constexpr int kG = decltype(g)::value;
-    if (M <= 2) return run_linear<kG, 1, 1, 1, 2>(a, stream);
-    if (M <= 8) return run_linear<kG, 4, 1, 1, 2>(a, stream);
-    if (M <= 16) return run_linear<kG, 8, 1, 1, 2>(a, stream);
-    if (M <= 32) return run_linear<kG, 0, 2, 2, 1>(a, stream);
-    if (M <= 48) return run_linear<kG, 0, 3, 2, 1>(a, stream);
-    return run_linear<kG, 0, 4, 2, 1>(a, stream);
+    if (M <= 2) return run_linear<kG, 1, 1, 2, 1>(a, stream);
+    if (M <= 8) return run_linear<kG, 1, 1, 2, 4>(a, stream);
+    if (M <= 16) return run_linear<kG, 1, 1, 2, 8>(a, stream);
+    if (M <= 32) return run_linear<kG, 2, 2, 1, 8>(a, stream);
+    if (M <= 48) return run_linear<kG, 3, 2, 1, 12>(a, stream);
+    return run_linear<kG, 4, 2, 1, 16>(a, stream);
   });
 }
 
