@@ -155,9 +155,12 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, const void* p) {
     w[0] = v[0];
     w[1] = v[1];
   } else {
-    const u32x4 v = *reinterpret_cast<const u32x4_1*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = v[i];
+    for (int n = 0; n < kBytes / 16; ++n) {
+      const u32x4 v = *(reinterpret_cast<const u32x4_1*>(p) + n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[4 * n + i] = v[i];
+    }
   }
 }
 
@@ -218,7 +221,7 @@ struct Lane {
 // banks.
 __device__ __forceinline__ int swizzle(int row) { return (row >> 2) & 3; }
 
-template <int kG, bool kZ, int kMT, int kNR, int kRuns, int kX>
+template <int kG, int kMT, int kNR, int kRuns, int kX>
 struct Int4Step {
   static constexpr int kColumns = 128 * kRuns;
   static constexpr int kGroups = kColumns / kG;
@@ -227,12 +230,14 @@ struct Int4Step {
   static constexpr int kTokenLds = kX * kPer * kPitch;
   static constexpr int kLds = kTokenLds + kNR * kRuns * 1024;  // of a wave: tokens, codes
   using At = Lane<kX, kNR>;
+  struct Scales {
+    uint32_t s[kNR][(kGroups + 1) / 2], z[kNR][(kGroups + 3) / 4];
+  };
   uint32_t w[kNR][kRuns][4];
   uint32_t s[kNR][(kGroups + 1) / 2], z[kNR][(kGroups + 3) / 4];
   u32x4 x[kX];
 
-  // kTail: the end of the rows; what lies past it is 0. Otherwise loads alone
-  // and no branch, so that waits can count them.
+  // kTail: the end of the rows; what lies past it is 0.
   template <bool kTail>
   __device__ __forceinline__ void load(const Int4Args& a, int k0, const At& at, int lane) {
     const int K = (int)a.K;
@@ -257,14 +262,14 @@ struct Int4Step {
           if (j % 4 == 0) z[r][j / 4] = 0;
           if (k0 + kG * j < K) {
             s[r][j / 2] |= (uint32_t)scales[at.group[r] + j] << (16 * (j & 1));
-            z[r][j / 4] |= (kZ ? (uint32_t)zeros[at.group[r] + j] : 8u) << (8 * (j & 3));
+            z[r][j / 4] |= (a.zeros ? (uint32_t)zeros[at.group[r] + j] : 8u) << (8 * (j & 3));
           }
         }
       } else {
         load_bytes<kGroups * 2>(s[r], scales + at.group[r]);
 #pragma unroll
         for (int j = 0; j < (kGroups + 3) / 4; ++j) z[r][j] = 0x08080808u;
-        if constexpr (kZ) load_bytes<kGroups>(z[r], zeros + at.group[r]);
+        if (a.zeros) load_bytes<kGroups>(z[r], zeros + at.group[r]);
       }
     }
     const bool in = !kTail || k0 + (lane % (kColumns / 8)) * 8 < K;
@@ -275,9 +280,8 @@ struct Int4Step {
     }
   }
 
-  __device__ __forceinline__ void add(floatx4 (&acc)[kMT][kNR], const At& at, uint8_t* lds, int lane, uint32_t mask,
-                                      uint32_t base) {
-    const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  // The loaded values to the wave's LDS, its rows' scales and zero points to cur.
+  __device__ __forceinline__ void stage(const At& at, uint8_t* lds, int lane, Scales& cur) const {
     uint8_t* lds_codes = lds + kTokenLds;
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -291,13 +295,17 @@ struct Int4Step {
 #pragma unroll
     for (int r = 0; r < kNR; ++r) {
 #pragma unroll
-      for (int j = 0; j < (kGroups + 1) / 2; ++j) s[r][j] = __builtin_amdgcn_ds_bpermute(at.from, s[r][j]);
-      if constexpr (kZ) {
+      for (int j = 0; j < (kGroups + 1) / 2; ++j) cur.s[r][j] = __builtin_amdgcn_ds_bpermute(at.from, s[r][j]);
 #pragma unroll
-        for (int j = 0; j < (kGroups + 3) / 4; ++j) z[r][j] = __builtin_amdgcn_ds_bpermute(at.from, z[r][j]);
-      }
+      for (int j = 0; j < (kGroups + 3) / 4; ++j) cur.z[r][j] = __builtin_amdgcn_ds_bpermute(at.from, z[r][j]);
     }
     asm volatile("" ::: "memory");
+  }
+
+  __device__ __forceinline__ static void add(floatx4 (&acc)[kMT][kNR], const At& at, const uint8_t* lds,
+                                             const Scales& cur, uint32_t mask, uint32_t base) {
+    const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint8_t* lds_codes = lds + kTokenLds;
 #pragma unroll
     for (int n = 0; n < kRuns; ++n) {
       bf16x8 t[kMT][4];
@@ -316,7 +324,7 @@ struct Int4Step {
         for (int i = 0; i < 4; ++i) {
           const int j = (128 * n + 32 * i) / kG;  // the product's group
           const bool begins = (32 * i) % kG == 0, ends = (32 * (i + 1)) % kG == 0;
-          const uint32_t off = (0xc180u | (((z[r][j / 4] >> (8 * (j & 3))) & 15u) << 3)) * 0x10001u;  // -(16 + z), twice
+          const uint32_t off = (0xc180u | (((cur.z[r][j / 4] >> (8 * (j & 3))) & 15u) << 3)) * 0x10001u;  // -(16 + z), twice
           const bf16x8 of = as_bf16x8(u32x4{off, off, off, off});
           const bf16x8 q = as_bf16x8(nibbles_bf16(c[i], mask, base));
 #pragma unroll
@@ -325,7 +333,7 @@ struct Int4Step {
             p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[m][i], of, p[m], 0, 0, 0);
           }
           if (ends) {
-            const uint32_t sw = s[r][j / 2];
+            const uint32_t sw = cur.s[r][j / 2];
             const float sc = (j & 1) ? bf16_hi(sw) : bf16_lo(sw);
 #pragma unroll
             for (int m = 0; m < kMT; ++m)
@@ -339,9 +347,9 @@ struct Int4Step {
   }
 };
 
-template <int kG, bool kZ, int kMT, int kNR, int kRuns, int kX>
+template <int kG, int kMT, int kNR, int kRuns, int kX>
 __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
-  using Step = Int4Step<kG, kZ, kMT, kNR, kRuns, kX>;
+  using Step = Int4Step<kG, kMT, kNR, kRuns, kX>;
   constexpr int kColumns = Step::kColumns, kPitch = Step::kPitch;
   extern __shared__ __attribute__((aligned(16))) uint8_t s_mem[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -386,48 +394,33 @@ __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
   const int whole = K / kColumns;                         // steps; this wave's are wave, wave + kWaves, ...
   const int left = (whole - wave + kWaves - 1) / kWaves;  // ... so many
   auto column = [&](int i) { return (wave + i * kWaves) * kColumns; };
-  if (left > 0) {
-    Step even, odd;
-    even.template load<false>(a, column(0), at, lane);
-    int i = 0;
-    for (; i + 2 < left; i += 2) {
-      odd.template load<false>(a, column(i + 1), at, lane);
-      __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the sums
-      even.add(acc, at, lds, lane, mask, base);
-      __builtin_amdgcn_sched_barrier(0);
-      even.template load<false>(a, column(i + 2), at, lane);
-      __builtin_amdgcn_sched_barrier(0);
-      odd.add(acc, at, lds, lane, mask, base);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (i + 1 < left) {
-      odd.template load<false>(a, column(i + 1), at, lane);
-      __builtin_amdgcn_sched_barrier(0);
-      even.add(acc, at, lds, lane, mask, base);
-      odd.add(acc, at, lds, lane, mask, base);
-    } else {
-      even.add(acc, at, lds, lane, mask, base);
-    }
+  Step step;
+  typename Step::Scales cur;
+  if (left > 0) step.template load<false>(a, column(0), at, lane);
+  for (int i = 0; i < left; ++i) {
+    step.stage(at, lds, lane, cur);
+    if (i + 1 < left) step.template load<false>(a, column(i + 1), at, lane);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the sums
+    Step::add(acc, at, lds, cur, mask, base);
   }
   if (whole * kColumns < K && wave == whole % kWaves) {
-    Step tail;
-    tail.template load<true>(a, whole * kColumns, at, lane);
-    tail.add(acc, at, lds, lane, mask, base);
+    step.template load<true>(a, whole * kColumns, at, lane);
+    step.stage(at, lds, lane, cur);
+    Step::add(acc, at, lds, cur, mask, base);
   }
   // the waves' sums, added in the order of the waves; lane (c, g) holds tokens
   // 4 g .. 4 g + 3 of weight row c
+  constexpr int kSums = kMT * kNR;
   floatx4* s_red = reinterpret_cast<floatx4*>(s_mem);
   __syncthreads();  // the steps' LDS is done with
 #pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int r = 0; r < kNR; ++r) s_red[(wave * kMT * kNR + m * kNR + r) * 64 + lane] = acc[m][r];
+  for (int i = 0; i < kSums; ++i) s_red[(wave * kSums + i) * 64 + lane] = acc[i / kNR][i % kNR];
   __syncthreads();
-  for (int i = wave; i < kMT * kNR; i += kWaves) {
+  for (int i = wave; i < kSums; i += kWaves) {
     floatx4 y = s_red[i * 64 + lane];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) {
-      const floatx4 u = s_red[(w * kMT * kNR + i) * 64 + lane];
+      const floatx4 u = s_red[(w * kSums + i) * 64 + lane];
 #pragma unroll
       for (int v = 0; v < 4; ++v) y[v] += u[v];
     }
@@ -444,11 +437,12 @@ __global__ void __launch_bounds__(kWaves * 64) int4_linear_kernel(Int4Args a) {
   }
 }
 
-template <int kG, bool kZ, int kMT, int kNR, int kRuns, int kX>
-hipError_t run_kernel(const Int4Args& a, hipStream_t stream) {
-  using Step = Int4Step<kG, kZ, kMT, kNR, kRuns, kX>;
+template <int kG, int kMT, int kNR, int kRuns, int kX>
+hipError_t run_linear(const Int4Args& a, hipStream_t stream) {
+  using Step = Int4Step<kG, kMT, kNR, kRuns, kX>;
   constexpr int kLds = kWaves * std::max(Step::kLds, kMT * kNR * 1024);
-  auto kern = int4_linear_kernel<kG, kZ, kMT, kNR, kRuns, kX>;
+  static_assert(kLds <= 160 * 1024);
+  auto kern = int4_linear_kernel<kG, kMT, kNR, kRuns, kX>;
   if constexpr (kLds > 65536) {  // the limit on dynamic LDS, raised once per device
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
@@ -465,10 +459,18 @@ hipError_t run_kernel(const Int4Args& a, hipStream_t stream) {
   kern<<<grid, dim3(kWaves * 64), kLds, stream>>>(a);
   return hipGetLastError();
 }
-template <int kG, int kMT, int kNR, int kRuns, int kX>
-hipError_t run_linear(const Int4Args& a, hipStream_t stream) {
-  return a.zeros ? run_kernel<kG, true, kMT, kNR, kRuns, kX>(a, stream)
-                 : run_kernel<kG, false, kMT, kNR, kRuns, kX>(a, stream);
+
+// 16, 32 or 48 weight rows to a workgroup: as few as leave one workgroup to a
+// compute unit, since every workgroup reads all of the tokens (us from a graph,
+// with 16, 32 and 48: 48 tokens x 11008 x 4096 25.3, 24.9, 18.8; x 4096 x 4096
+// 10.4, 12.2, 14.5; 16 x 11008 x 4096 11.8, 12.6, 11.1). Four tokens or fewer
+// cost little to read, and 16 rows do better at any size (4 x 11008 x 4096 8.9,
+// 10.1, 9.3).
+template <int kG, int kMT, int kX>
+hipError_t run_rows(const Int4Args& a, hipStream_t stream) {
+  if (a.N <= 16 * 256) return run_linear<kG, kMT, 1, 1, kX>(a, stream);
+  if (a.N <= 32 * 256) return run_linear<kG, kMT, 2, 1, kX>(a, stream);
+  return run_linear<kG, kMT, 3, 1, kX>(a, stream);
 }
 
 template <typename F>
@@ -510,11 +512,11 @@ hipError_t launch_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, con
   return by_group(w.group, [&](auto g) {
     constexpr int kG = decltype(g)::value;
     if (M <= 2) return run_linear<kG, 1, 1, 2, 1>(a, stream);
-    if (M <= 8) return run_linear<kG, 1, 1, 2, 4>(a, stream);
-    if (M <= 16) return run_linear<kG, 1, 1, 2, 8>(a, stream);
-    if (M <= 32) return run_linear<kG, 2, 2, 1, 8>(a, stream);
-    if (M <= 48) return run_linear<kG, 3, 2, 1, 12>(a, stream);
-    return run_linear<kG, 4, 2, 1, 16>(a, stream);
+    if (M <= 4) return run_linear<kG, 1, 1, 2, 2>(a, stream);
+    if (M <= 16) return run_rows<kG, 1, 4>(a, stream);
+    if (M <= 32) return run_rows<kG, 2, 8>(a, stream);
+    if (M <= 48) return run_rows<kG, 3, 12>(a, stream);
+    return run_rows<kG, 4, 16>(a, stream);
   });
 }
 
