@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace qlora {
 
@@ -19,52 +20,117 @@ __device__ __forceinline__ uint32_t bits_of(float f) { return __builtin_bit_cast
 // bf16(f), as a float.
 __device__ __forceinline__ float to_bf16(float f) { return bf16_lo(pack_bf16x2(f, 0.0f)); }
 
+// Largest with that of another lane (update_dpp's control).
+template <int kCtrl>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, true);
+  return v > o ? v : o;
+}
+
+// Row and group of flat group index b = first + i, first the same in the whole
+// workgroup and i below kPer: a scalar division unless rows are short.
+template <uint32_t kPer>
+__device__ __forceinline__ void split_index(uint32_t first, uint32_t i, uint32_t ng, uint32_t& row, uint32_t& g) {
+  if (ng >= kPer) {
+    row = first / ng;
+    g = first - row * ng + i;
+    if (g >= ng) {
+      g -= ng;
+      ++row;
+    }
+  } else {
+    row = (first + i) / ng;
+    g = first + i - row * ng;
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Quantization: kG / 8 lanes own a group, eight values each.
+// Quantization: kG / 16 lanes own a group, two vectors of eight values each, so that
+// what a group costs once is shared by 16 values.
 //   asymmetric  lo = min(w, 0), hi = max(w, 0), s = bf16((hi - lo) / 15),
 //               z = rint(-lo / s) in [0, 15]
 //   symmetric   s = bf16(max|w| / 7), z = 8
 //   q = rint(w / s) + z in [0, 15]; where s = 0, z = 0 (symmetric 8) and q = z.
 template <int kG, bool kSym>
 __global__ void __launch_bounds__(kThreads)
-int4_quantize_kernel(const uint16_t* __restrict__ W, int64_t ldw, int K, int ng, int64_t groups,
+int4_quantize_kernel(const uint16_t* __restrict__ W, int64_t ldw, int K, uint32_t ng, uint32_t groups,
                      uint8_t* __restrict__ codes, uint16_t* __restrict__ scales, uint8_t* __restrict__ zeros) {
 #pragma clang fp contract(off)
-  constexpr int kLanes = kG / 8;
-  const int64_t b = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  constexpr uint32_t kLanes = kG / 16, kPer = kThreads / kLanes;
+  const uint32_t first = blockIdx.x * kPer, b = first + threadIdx.x / kLanes;
   if (b >= groups) return;
-  const int l = threadIdx.x % kLanes;
-  const int64_t row = b / ng;
-  const int g = (int)(b - row * ng), col = g * kG + l * 8;
-  u32x4 v = {0, 0, 0, 0};
-  if (col < K) v = *reinterpret_cast<const u32x4_row*>(W + row * ldw + col);
-  float x[8];
+  const uint32_t l = threadIdx.x % kLanes;
+  uint32_t row, g;
+  split_index<kPer>(first, threadIdx.x / kLanes, ng, row, g);
+  const int col = (int)(g * kG + l * 8);  // and kG / 2 columns on
+  const uint16_t* w = W + (int64_t)row * ldw + col;
+  u32x4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = v[i];
-    x[2 * i] = bf16_lo(w);
-    x[2 * i + 1] = bf16_hi(w);
+  for (int h = 0; h < 2; ++h)
+    if (col + h * (kG / 2) < K) v[h] = *reinterpret_cast<const u32x4_row*>(w + h * (kG / 2));
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t p = v[i / 4][i % 4];
+    x[2 * i] = bf16_lo(p);
+    x[2 * i + 1] = bf16_hi(p);
   }
   float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     lo = fminf(lo, x[i]);
     hi = fmaxf(hi, x[i]);
   }
+  // -lo and hi over two lanes, four and eight: the bits of numbers
+  // that are not negative have their order
+  uint32_t lob = bits_of(lo) & 0x7fffffffu, hib = bits_of(hi) & 0x7fffffffu;
+  auto join = [&](auto ctrl) {
+    lob = max_dpp<decltype(ctrl)::value>(lob);
+    hib = max_dpp<decltype(ctrl)::value>(hib);
+  };
+  join(std::integral_constant<int, 0xb1>{});
+  if constexpr (kLanes >= 4) join(std::integral_constant<int, 0x4e>{});
+  if constexpr (kLanes >= 8) join(std::integral_constant<int, 0x141>{});
+  lo = __builtin_bit_cast(float, lob);  // -lo from here on
+  hi = __builtin_bit_cast(float, hib);
+  // The quotient by 7 or 15, correctly rounded: the product with the rounded
+  // inverse and one step from its exact remainder (a division for values whose
+  // remainder float32 does not hold).
+  constexpr float kD = kSym ? 7.0f : 15.0f, kInv = 1.0f / kD;
+  const float span = kSym ? fmaxf(lo, hi) : hi + lo;
+  float s = span * kInv;
+  s = __builtin_fmaf(__builtin_fmaf(-kD, s, span), kInv, s);
+  if (__any(span < 0x1p-90f)) s = span / kD;
+  s = to_bf16(s);
+  // rint(x / s) without a division to each value. x and s have 8 significant
+  // bits: x / s below 32 is half-way between two integers or at least 2^-10 from
+  // it. x times the hardware's inverse (one unit in the last place) is within
+  // 2^-17 of x / s; rounded to multiples of 2^-12 it is exactly half-way in the
+  // first case, and on the right side in the second. Scales whose inverse
+  // float32 does not hold are taken 2^64 times, and the values with them.
+  float sk = s;
+  if (s < 0x1p-100f) {
+    sk *= 0x1p64f;
+    lo *= 0x1p64f;
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) {
-    lo = fminf(lo, __shfl_xor(lo, d));
-    hi = fmaxf(hi, __shfl_xor(hi, d));
+    for (int i = 0; i < 16; ++i) x[i] *= 0x1p64f;
   }
-  const float s = to_bf16(kSym ? fmaxf(-lo, hi) / 7.0f : (hi - lo) / 15.0f);
-  const float z = kSym ? 8.0f : s > 0.0f ? fminf(__builtin_rintf(-lo / s), 15.0f) : 0.0f;
-  uint32_t word = 0;
+  const float r = s > 0.0f ? __builtin_amdgcn_rcpf(sk) : 0.0f;
+  auto near = [&](float v) { return __builtin_fmaf(v, r, 0x1.8p11f) - 0x1.8p11f; };
+  const float z = kSym ? 8.0f : fminf(__builtin_rintf(near(lo)), 15.0f);
+  // q - z in [-z, 15 - z], then its integer in the low bits of 1.5 2^23 + q - z
+  // (ties to even); the eight integers in one word, modulo 2^32, and z to each
+  uint8_t* c = codes + ((int64_t)row * K + col) / 2;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = s > 0.0f ? __builtin_rintf(x[i] / s) + z : z;
-    word |= (uint32_t)fminf(fmaxf(q, 0.0f), 15.0f) << (4 * i);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t word = (uint32_t)z * 0x11111111u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = __builtin_amdgcn_fmed3f(near(x[8 * h + i]), -z, 15.0f - z) + 0x1.8p23f;
+      word += (bits_of(q) << (4 * i)) - (0x4b400000u << (4 * i));
+    }
+    if (col + h * (kG / 2) < K) *reinterpret_cast<uint32_t*>(c + h * (kG / 4)) = word;
   }
-  if (col < K) *reinterpret_cast<uint32_t*>(codes + (row * K + col) / 2) = word;
   if (l == 0) {
     scales[b] = (uint16_t)(bits_of(s) >> 16);
     if (!kSym) zeros[b] = (uint8_t)z;
@@ -75,14 +141,14 @@ int4_quantize_kernel(const uint16_t* __restrict__ W, int64_t ldw, int K, int ng,
 template <int kG>
 __global__ void __launch_bounds__(kThreads)
 int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
-                       const uint8_t* __restrict__ zeros, int K, int ng, int64_t units,
+                       const uint8_t* __restrict__ zeros, int K, uint32_t ng, uint32_t units,
                        uint16_t* __restrict__ W, int64_t ldw) {
-  const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;  // eight values
+  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;  // eight values
   if (u >= units) return;
-  const int per = K / 8;
+  const uint32_t per = (uint32_t)K / 8;
   const int64_t row = u / per;
-  const int col = (int)(u - row * per) * 8;
-  const int64_t b = row * ng + col / kG;
+  const int col = (int)(u % per) * 8;
+  const uint32_t b = (uint32_t)row * ng + col / kG;
   const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (row * K + col) / 2);
   const float s = bf16_to_f32(scales[b]), z = zeros ? (float)zeros[b] : 8.0f;
   u32x4 v;
@@ -484,14 +550,14 @@ hipError_t by_group(int group, F f) {
 
 hipError_t launch_int4_quantize(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, int group, uint8_t* codes,
                                 uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
-  const int64_t ng = (K + group - 1) / group, groups = N * ng, per = kThreads * 8 / group;
+  const int64_t ng = (K + group - 1) / group, groups = N * ng, per = kThreads * 16 / group;
   return by_group(group, [&](auto g) {
     constexpr int kG = decltype(g)::value;
     const dim3 grid((unsigned)((groups + per - 1) / per));
     if (zeros)
-      int4_quantize_kernel<kG, false><<<grid, dim3(kThreads), 0, stream>>>(W, ldw, (int)K, (int)ng, groups, codes, scales, zeros);
+      int4_quantize_kernel<kG, false><<<grid, dim3(kThreads), 0, stream>>>(W, ldw, (int)K, (uint32_t)ng, (uint32_t)groups, codes, scales, zeros);
     else
-      int4_quantize_kernel<kG, true><<<grid, dim3(kThreads), 0, stream>>>(W, ldw, (int)K, (int)ng, groups, codes, scales, zeros);
+      int4_quantize_kernel<kG, true><<<grid, dim3(kThreads), 0, stream>>>(W, ldw, (int)K, (uint32_t)ng, (uint32_t)groups, codes, scales, zeros);
     return hipGetLastError();
   });
 }
@@ -501,7 +567,7 @@ hipError_t launch_int4_dequantize(const Int4Weight& w, uint16_t* out, int64_t ld
   return by_group(w.group, [&](auto g) {
     constexpr int kG = decltype(g)::value;
     int4_dequantize_kernel<kG><<<dim3((unsigned)((units + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream>>>(
-        w.codes, w.scales, w.zeros, (int)w.K, (int)((w.K + kG - 1) / kG), units, out, ldo);
+        w.codes, w.scales, w.zeros, (int)w.K, (uint32_t)((w.K + kG - 1) / kG), (uint32_t)units, out, ldo);
     return hipGetLastError();
   });
 }
