@@ -33,9 +33,13 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr float kLow = -1e30f;       // 0 * kLow is 0 where 0 * -inf would be NaN
 constexpr double kLn2 = 0.693147180559945309417;
 
-// A vector is 16 bytes at any element of a row: the loads and stores need no
-// more than the elements' alignment, and cost the same (copying 512 MiB: 190 us
-// aligned, 193 to 195 at odd elements; reading it 87 and 99).
+// A row is cut into vectors of 16 bytes where its addresses are multiples of 16:
+// `shift` elements of the first vector lie before the row, and a position is an
+// element's index plus shift. (Vectors at any element are allowed, and cost
+// the same at multiples of 4 bytes; at odd bf16 elements each lane's 16 bytes
+// take a pass of their own: 1024 rows of 100001 53 us forward and 106
+// backward, of 100000 42 and 92.) Where a gradient's rows start at another
+// offset than the logits', its stores are the ones not aligned.
 typedef u32x4 u32x4_row __attribute__((aligned(2)));
 
 template <bool kF32>
@@ -45,52 +49,36 @@ struct Elem {
   static constexpr int kBytes = kF32 ? 4 : 2;
 };
 
+// Positions [lo, n) of a part hold elements of the row; of vector v those
+// outside are -inf.
 template <bool kF32>
-__device__ __forceinline__ u32x4 load_vec(const char* part, int v, int n);
-// A thread's vectors of a step, the first of them v0: without a branch to a load
-// where the whole step lies in the part.
-template <bool kF32>
-__device__ __forceinline__ void load_step(u32x4 (&r)[kVecs], const char* part, int c, int v0, int n) {
-  if ((c + 1) * Elem<kF32>::kChunk <= n) {  // uniform
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      r[u] = *reinterpret_cast<const u32x4_row*>(part + (int64_t)(v0 + u * kThreads) * 16);
-  } else {
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) r[u] = load_vec<kF32>(part, v0 + u * kThreads, n);
-  }
-}
-
-// Vector v of a row part of n elements; elements past the end are -inf.
-template <bool kF32>
-__device__ __forceinline__ u32x4 load_vec(const char* part, int v, int n) {
+__device__ __forceinline__ u32x4 load_vec(const char* part, int v, int lo, int n) {
   constexpr int kE = Elem<kF32>::kE;
-  const int left = n - v * kE;
-  if (left >= kE) return *reinterpret_cast<const u32x4_row*>(part + (int64_t)v * 16);
+  const int from = lo - v * kE, to = n - v * kE;
+  if (from <= 0 && to >= kE) return *reinterpret_cast<const u32x4_row*>(part + (int64_t)v * 16);
+  const uint32_t none = kF32 ? 0xff800000u : 0xff80ff80u;
+  u32x4 r = {none, none, none, none};
   if constexpr (kF32) {
-    u32x4 r = {0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
     const uint32_t* e = reinterpret_cast<const uint32_t*>(part + (int64_t)v * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < left) r[i] = e[i];
-    return r;
+      if (i >= from && i < to) r[i] = e[i];
   } else {
-    u32x4 r = {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
     const uint16_t* e = reinterpret_cast<const uint16_t*>(part + (int64_t)v * 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) {
+      if (i >= from && i < to) {
         const uint32_t keep = (i & 1) ? 0x0000ffffu : 0xffff0000u;
         r[i >> 1] = (r[i >> 1] & keep) | ((uint32_t)e[i] << (16 * (i & 1)));
       }
-    return r;
   }
+  return r;
 }
 template <bool kF32>
-__device__ __forceinline__ void store_vec(char* part, int v, int n, u32x4 r) {
+__device__ __forceinline__ void store_vec(char* part, int v, int lo, int n, u32x4 r) {
   constexpr int kE = Elem<kF32>::kE;
-  const int left = n - v * kE;
-  if (left >= kE) {
+  const int from = lo - v * kE, to = n - v * kE;
+  if (from <= 0 && to >= kE) {
     *reinterpret_cast<u32x4_row*>(part + (int64_t)v * 16) = r;
     return;
   }
@@ -98,13 +86,44 @@ __device__ __forceinline__ void store_vec(char* part, int v, int n, u32x4 r) {
     uint32_t* e = reinterpret_cast<uint32_t*>(part + (int64_t)v * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < left) e[i] = r[i];
+      if (i >= from && i < to) e[i] = r[i];
   } else {
     uint16_t* e = reinterpret_cast<uint16_t*>(part + (int64_t)v * 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) e[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
+      if (i >= from && i < to) e[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
   }
+}
+// A thread's vectors of a step, the first of them v0: without a branch to a load
+// where the whole step lies in the row.
+template <bool kF32>
+__device__ __forceinline__ void load_step(u32x4 (&r)[kVecs], const char* part, int c, int v0, int lo, int n) {
+  if (c * Elem<kF32>::kChunk >= lo && (c + 1) * Elem<kF32>::kChunk <= n) {  // uniform
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      r[u] = *reinterpret_cast<const u32x4_row*>(part + (int64_t)(v0 + u * kThreads) * 16);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) r[u] = load_vec<kF32>(part, v0 + u * kThreads, lo, n);
+  }
+}
+
+// A workgroup's part of a row: positions [first, first + n), of which the first lo
+// hold nothing.
+struct Part {
+  int64_t row;
+  int shift, first, lo, n;
+};
+template <bool kF32>
+__device__ __forceinline__ Part part_of(const char* Z, int64_t ldz, int S, int part, int V) {
+  Part p;
+  const uint32_t row = blockIdx.x / (uint32_t)S;
+  p.row = row;
+  p.shift = (int)((uintptr_t)(Z + row * ldz) & 15) / Elem<kF32>::kBytes;
+  p.first = (int)(blockIdx.x - row * (uint32_t)S) * part;
+  p.lo = p.first == 0 ? p.shift : 0;
+  p.n = max(0, min(part, V + p.shift - p.first));
+  return p;
 }
 
 template <bool kF32>
@@ -135,16 +154,42 @@ __device__ __forceinline__ Soft joined(const Soft& a, const Soft& b, float c2) {
   const Soft x = rescaled(a, m, c2), y = rescaled(b, m, c2);
   return Soft{m, x.s + y.s, x.u + y.u};
 }
+// Reductions over a wave whose lanes are all active, the same in every lane: by
+// rows of 16 lanes, then of the rows; the last lane holds the result.
+template <int kCtrl, int kRows, typename T>
+__device__ __forceinline__ T dpp(T v, T none) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v),
+                                                             kCtrl, kRows, 0xf, false));
+  } else {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v), n = __builtin_bit_cast(uint64_t, none);
+    const uint32_t lo = __builtin_amdgcn_update_dpp((int)(uint32_t)n, (int)(uint32_t)w, kCtrl, kRows, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp((int)(n >> 32), (int)(w >> 32), kCtrl, kRows, 0xf, false);
+    return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
+  }
+}
+template <typename T, typename F>
+__device__ __forceinline__ T wave_reduce(T v, T none, F f) {
+  v = f(v, dpp<0x111, 0xf>(v, none));  // row_shr 1, 2, 4, 8
+  v = f(v, dpp<0x112, 0xf>(v, none));
+  v = f(v, dpp<0x114, 0xf>(v, none));
+  v = f(v, dpp<0x118, 0xf>(v, none));
+  v = f(v, dpp<0x142, 0xa>(v, none));  // row_bcast 15, 31
+  v = f(v, dpp<0x143, 0xc>(v, none));
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+  } else {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)w, 63), hi = __builtin_amdgcn_readlane((int)(w >> 32), 63);
+    return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
+  }
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
+  return wave_reduce(v, -kInf, [](float a, float b) { return fmaxf(a, b); });
 }
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
 }
 __device__ __forceinline__ Soft wave_join(const Soft& a, float c2) {
   Soft r = rescaled(a, wave_max(a.m), c2);
@@ -170,25 +215,8 @@ __device__ __forceinline__ uint64_t pair_of(uint32_t key, uint32_t idx) {
 }
 __device__ __forceinline__ uint32_t idx_of(uint64_t pair) { return 0xffffffffu - (uint32_t)pair; }
 
-template <int kCtrl, int kRows>
-__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
-  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, kCtrl, kRows, 0xf, true);
-  const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), kCtrl, kRows, 0xf, true);
-  return ((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo;
-}
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
-// Largest over the wave (every lane active), the same in every lane.
-__device__ __forceinline__ uint64_t wave_largest(uint64_t v) {
-  v = larger(v, dpp64<0x111, 0xf>(v));  // row_shr 1, 2, 4, 8
-  v = larger(v, dpp64<0x112, 0xf>(v));
-  v = larger(v, dpp64<0x114, 0xf>(v));
-  v = larger(v, dpp64<0x118, 0xf>(v));
-  v = larger(v, dpp64<0x142, 0xa>(v));  // row_bcast 15, 31
-  v = larger(v, dpp64<0x143, 0xc>(v));
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, 63);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(v >> 32), 63);
-  return ((uint64_t)hi << 32) | lo;
-}
+__device__ __forceinline__ uint64_t wave_largest(uint64_t v) { return wave_reduce(v, (uint64_t)0, larger); }
 // The r-th largest of the lanes' values (with multiplicity).
 __device__ __forceinline__ uint64_t wave_rth(uint64_t v, int r) {
   uint64_t top = wave_largest(v);
@@ -258,14 +286,14 @@ __device__ __forceinline__ void rank_candidates(const TopLds& t, int count, int 
 
 // The `need` largest entries of a part. bins [chunks][kThreads]: key of the
 // maximum of each thread's vectors of each step; best: the thread's largest
-// bin as (key, first index of the step), an upper bound in that coarser order
+// bin as (key, first position of the step), an upper bound in that coarser order
 // for all its entries, and attained by one of them unless they are all NaN.
 // The r-th largest of them in each of w full waves, r = need / w rounded up,
 // has r entries at or above it in that wave, so the smallest of the waves'
 // has `need`: only the bins that reach it are read again (from the L2), and
 // what reaches it there is ranked.
 template <bool kF32, typename Put>
-__device__ __forceinline__ void select_top(const char* part, int n, int first, int chunks,
+__device__ __forceinline__ void select_top(const char* part, int lo, int n, int first, int chunks,
                                            const uint32_t* bins, uint64_t best, int need, TopLds& t,
                                            Put put) {
   constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
@@ -289,17 +317,17 @@ __device__ __forceinline__ void select_top(const char* part, int n, int first, i
   }
   __syncthreads();
   const int items = t.n_items;
-  // f(key, index, step) over the entries of the bins listed, or of all
+  // f(key, position, step) over the entries of the bins listed, or of all
   auto each = [&](bool all, auto f) {
     const int units = (all ? chunks * kThreads : items) * kVecs;
     for (int w = tid; w < units; w += kThreads) {
       const int it = all ? w / kVecs : t.items[w / kVecs];
       const int b = it / kThreads, v = (b * kVecs + w % kVecs) * kThreads + it % kThreads;
       if (v * kE >= n) continue;
-      const u32x4 x = load_vec<kF32>(part, v, n);
+      const u32x4 x = load_vec<kF32>(part, v, lo, n);
 #pragma unroll
       for (int i = 0; i < kE; ++i)
-        if (v * kE + i < n) f(key_of(elem<kF32>(x, i)), (uint32_t)(first + v * kE + i), b);
+        if (v * kE + i >= lo && v * kE + i < n) f(key_of(elem<kF32>(x, i)), (uint32_t)(first + v * kE + i), b);
     }
   };
   bool all = items > kMaxItems;
@@ -345,37 +373,39 @@ template <bool kF32, int kOp, bool kTop>
 __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  __shared__ Soft s_soft[2][kWaves];
-  __shared__ int s_last;
+  __shared__ Soft s_soft[kWaves];
+  __shared__ int s_last, s_twice;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t row = blockIdx.x / (uint32_t)a.S;
-  const int split = (int)(blockIdx.x - (uint32_t)row * (uint32_t)a.S);
-  const int first = split * a.part, n = min(a.part, a.V - first);
+  const Part in = part_of<kF32>(a.Z, a.ldz, a.S, a.part, a.V);
+  const int64_t row = in.row;
+  const int shift = in.shift, first = in.first, lo = in.lo, n = in.n, split = first / a.part;
   const char* zrow = a.Z + row * a.ldz;
-  const char* part = zrow + (int64_t)first * Elem<kF32>::kBytes;
+  const char* part = zrow + (int64_t)(first - shift) * Elem<kF32>::kBytes;
   const int chunks = (n + kChunk - 1) / kChunk;
   const float c2 = a.c2;
 
   TopLds& top = *reinterpret_cast<TopLds*>(dyn);
   uint32_t* bins = reinterpret_cast<uint32_t*>(dyn + sizeof(TopLds));
-  uint32_t* mask = reinterpret_cast<uint32_t*>(dyn);  // bit i: entry first + i is on the list
+  uint32_t* mask = reinterpret_cast<uint32_t*>(dyn);  // bit i: position first + i is on the list
   if constexpr (kOp == kDistillRest) {
+    if (tid == 0) s_twice = 0;
     const int words = (n + 127) / 128 * 4;
     for (int i = tid * 4; i < words; i += kThreads * 4) *reinterpret_cast<u32x4*>(mask + i) = u32x4{0, 0, 0, 0};
     __syncthreads();
-    for (int i = tid; i < a.k; i += kThreads) {
-      const int64_t at = a.ids[row * a.k + i] - first;
-      if (at >= 0 && at < n) atomicOr(mask + (at >> 5), 1u << (at & 31));
+    if (tid < a.k) {  // k <= kThreads
+      const int64_t at = a.ids[row * a.k + tid] + shift - first;
+      const uint32_t bit = 1u << (at & 31);
+      if (at >= lo && at < n && (atomicOr(mask + (at >> 5), bit) & bit)) s_twice = 1;
     }
     __syncthreads();
   }
 
-  Soft acc = kNone, list = kNone;  // list: the listed entries, where they are kept apart
+  Soft acc = kNone;  // without the listed entries where the list's rest is a class
   uint64_t best = 0;
   for (int c = 0; c < chunks; ++c) {
     u32x4 r[kVecs];
     const int v0 = c * kVecs * kThreads + tid;
-    load_step<kF32>(r, part, c, v0, n);
+    load_step<kF32>(r, part, c, v0, lo, n);
     float z[kVecs * kE];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
@@ -391,11 +421,7 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
                    : reinterpret_cast<const uint8_t*>(mask)[v];
         if (b) {
 #pragma unroll
-          for (int i = 0; i < kE; ++i)
-            if ((b >> i) & 1) {
-              list = joined(list, Soft{z[u * kE + i], z[u * kE + i] == -kInf ? 0.0f : 1.0f, 0.0f}, c2);
-              z[u * kE + i] = -kInf;
-            }
+          for (int i = 0; i < kE; ++i) z[u * kE + i] = (b >> i) & 1 ? -kInf : z[u * kE + i];
         }
       }
     }
@@ -410,53 +436,63 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
     m = fmaxf(m, acc.m);
     const float base = base_of(m);
     float s[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
+    auto sums = [&](auto y_of) {
 #pragma unroll
-    for (int i = 0; i < kVecs * kE; ++i) {
-      const float y = (z[i] - base) * c2;
-      const float e = exp2_(y);
-      s[i & 3] += e;
-      if constexpr (kOp == kLogprobs) q[i & 3] = __builtin_fmaf(e, fmaxf(y, kLow), q[i & 3]);
+      for (int i = 0; i < kVecs * kE; ++i) {
+        const float y = y_of(z[i]);
+        const float e = exp2_(y);
+        s[i & 3] += e;
+        if constexpr (kOp == kLogprobs) q[i & 3] = __builtin_fmaf(e, fmaxf(y, kLow), q[i & 3]);
+      }
+    };
+    // z c2 - b, b = fl(m c2), is one operation to (z - m) c2's two, and off by what
+    // b was rounded by: d for every entry, taken out of the sums below. Far from
+    // zero (a row of the type's lowest values, say) d would not be small.
+    const float b = base * c2;
+    float d = 0.0f;
+    if (__all(fabsf(b) < 1024.0f)) {
+      d = __builtin_fmaf(base, c2, -b);
+      sums([&](float v) { return __builtin_fmaf(v, c2, -b); });
+    } else {
+      sums([&](float v) { return (v - base) * c2; });
     }
+    const float f = exp2_(-d), sc = (s[0] + s[1]) + (s[2] + s[3]), qc = (q[0] + q[1]) + (q[2] + q[3]);
     acc = rescaled(acc, m, c2);
-    acc.s += (s[0] + s[1]) + (s[2] + s[3]);
-    acc.u += (q[0] + q[1]) + (q[2] + q[3]);
+    acc.s = __builtin_fmaf(sc, f, acc.s);
+    acc.u = __builtin_fmaf(qc - sc * d, f, acc.u);
   }
 
-  // the workgroup's statistics, the same in every thread
+  // the workgroup's statistics; one wave goes on with them, all where a selection
+  // is to come
   acc = wave_join(acc, c2);
-  if (lane == 0) s_soft[0][wave] = acc;
-  if constexpr (kOp == kDistillRest) {
-    list = wave_join(list, c2);
-    if (lane == 0) s_soft[1][wave] = list;
-  }
+  if (lane == 0) s_soft[wave] = acc;
   __syncthreads();
-  acc = s_soft[0][0];
-  for (int w = 1; w < kWaves; ++w) acc = joined(acc, s_soft[0][w], c2);
-  if constexpr (kOp == kDistillRest) {
-    list = s_soft[1][0];
-    for (int w = 1; w < kWaves; ++w) list = joined(list, s_soft[1][w], c2);
-  }
+  if (!kTop && wave) return;
+  acc = s_soft[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) acc = joined(acc, s_soft[w], c2);
+  bool twice = kOp == kDistillRest && s_twice;  // an id is twice on the list
 
   if (a.S > 1) {
     const int64_t at = row * a.S + split;
     if constexpr (kTop) {
-      const int need = min(a.n_top, n);
+      const int need = min(a.n_top, n - lo);
       uint64_t* mine = a.lists + at * a.n_top;
       auto put = [&](int r, uint64_t p) {
         __hip_atomic_store(mine + r, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       };
       if (tid >= need && tid < a.n_top) put(tid, 0);
-      select_top<kF32>(part, n, first, chunks, bins, best, need, top, put);
+      if (need > 0) select_top<kF32>(part, lo, n, first, chunks, bins, best, need, top, put);
     }
     if (tid == 0) {
       put_agent(a.sums + at * 4, acc.m);
       put_agent(a.sums + at * 4 + 1, acc.s);
-      put_agent(a.sums + at * 4 + 2, kOp == kLogprobs ? acc.u : list.m);
-      put_agent(a.sums + at * 4 + 3, list.s);
+      put_agent(a.sums + at * 4 + 2, kOp == kLogprobs ? acc.u : twice ? 1.0f : 0.0f);
     }
     // every store of the workgroup acknowledged before its flag
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+    if constexpr (kTop) __syncthreads();
+    bool last = true;
     if (wave == 0) {
       const uint64_t tag = call_tag();
       uint64_t* flags = a.flags + row * a.S;
@@ -466,23 +502,27 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       const uint64_t zero = (uint64_t)(a.V >> 30);  // an addition that the compiler keeps
-      const bool there = lane >= a.S || __hip_atomic_fetch_add(flags + (lane < a.S ? lane : 0), zero, __ATOMIC_RELAXED,
-                                                               __HIP_MEMORY_SCOPE_AGENT) == tag;
-      if (lane == 0) s_last = 0;
-      if (__all(there) && lane == 0) s_last = 1;
+      last = lane >= a.S || __hip_atomic_fetch_add(flags + (lane < a.S ? lane : 0), zero, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT) == tag;
+      last = __all(last);
+      if (kTop && lane == 0) s_last = last;
     }
-    __syncthreads();
-    if (!s_last) return;
-    acc = list = kNone;
+    if constexpr (kTop) {
+      __syncthreads();
+      last = s_last;
+    }
+    if (!last) return;
+    acc = kNone;
+    float third = 0.0f;
     if (lane < a.S) {
       const float* p = a.sums + (row * a.S + lane) * 4;
       acc.m = get_agent(p);
       acc.s = get_agent(p + 1);
-      (kOp == kLogprobs ? acc.u : list.m) = get_agent(p + 2);
-      list.s = get_agent(p + 3);
+      third = get_agent(p + 2);
     }
+    if constexpr (kOp == kLogprobs) acc.u = third;
+    twice = __any(kOp == kDistillRest && third != 0.0f);
     acc = wave_join(acc, c2);
-    if constexpr (kOp == kDistillRest) list = wave_join(list, c2);
   }
 
   if constexpr (kOp == kLogprobs) {
@@ -504,11 +544,11 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
     }
     if constexpr (kTop) {
       auto put = [&](int r, uint64_t p) {
-        a.top_ids[row * a.n_top + r] = (int64_t)idx_of(p);
+        a.top_ids[row * a.n_top + r] = (int64_t)idx_of(p) - shift;
         a.top_logp[row * a.n_top + r] = logp_of(of_key((uint32_t)(p >> 32)));
       };
       if (a.S == 1) {
-        select_top<kF32>(part, n, 0, chunks, bins, best, a.n_top, top, put);
+        select_top<kF32>(part, lo, n, 0, chunks, bins, best, a.n_top, top, put);
       } else {
         // the parts' lists are sorted, and all but the last are whole: each has
         // r = n_top / (S - 1) rounded up entries at or above its r-th
@@ -530,33 +570,48 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       }
     }
   } else {
-    // one wave: up to four list entries a lane, in 64 bits
-    if (wave) return;
+    // up to four list entries a lane, in 64 bits
     constexpr int kPer = 4;
     const int64_t at = row * a.k;
+    int64_t id[kPer];
     bool ok[kPer];
     float t[kPer], z[kPer];
-    float tm = -kInf;
+    float tm = -kInf, zm = -kInf;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = i * 64 + lane;
-      const int64_t id = e < a.k ? a.ids[at + e] : -1;
-      ok[i] = id >= 0 && id < a.V;
+      id[i] = e < a.k ? a.ids[at + e] : -1;
+      ok[i] = id[i] >= 0 && id[i] < a.V;
       t[i] = z[i] = -kInf;
       if (ok[i]) {
         t[i] = a.values_f32 ? load_elem<true>(a.values, at + e) : load_elem<false>(a.values, at + e);
-        z[i] = load_elem<kF32>(zrow, id);
+        z[i] = load_elem<kF32>(zrow, id[i]);
       }
-      ok[i] = ok[i] && t[i] != -kInf;
       tm = fmaxf(tm, t[i]);
+      zm = fmaxf(zm, z[i]);
     }
     tm = wave_max(tm);
     if (tm == -kInf) tm = 0.0f;
-    double rel[kPer], sum = 0.0;
+    // the student's mass on the list, each token once
+    float on = 0.0f;
+    if constexpr (kOp == kDistillRest) {
+      zm = wave_max(zm);
+      const float base = base_of(zm);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        bool once = ok[i];
+        if (twice)  // uniform
+          for (int e = 0; e < i * 64 + lane && once; ++e) once = a.ids[at + e] != id[i];
+        if (once) on += exp2_((z[i] - base) * c2);
+      }
+      on = wave_sum(on);
+    }
+    double q[kPer], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      rel[i] = ((double)t[i] - tm) * a.inv_t64;
-      if (kOp == kDistill && ok[i]) sum += exp(rel[i]);
+      ok[i] = ok[i] && t[i] != -kInf;
+      q[i] = 0.0;
+      if (kOp == kDistill && ok[i]) sum += q[i] = exp(((double)t[i] - tm) * a.inv_t64);
     }
     double tl;
     if constexpr (kOp == kDistillRest) {
@@ -566,15 +621,15 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       tl = sum > 0.0 ? log(sum) : 0.0;
     }
     // the student's log sums over m = the larger maximum: of the rest, of the list
-    const float m = kOp == kDistillRest ? fmaxf(acc.m, list.m) : acc.m;
-    const bool empty = m == -kInf && acc.s == 0.0f && list.s == 0.0f;
+    const float m = kOp == kDistillRest ? fmaxf(acc.m, zm) : acc.m;
+    const bool empty = m == -kInf && acc.s == 0.0f && on == 0.0f;
     double l = 0.0, logr = 0.0;
     bool rest = false;
     if (!empty) {
       if constexpr (kOp == kDistillRest) {
         rest = acc.s != 0.0f;
         const double r = rest ? log((double)acc.s) + ((double)acc.m - m) * a.inv_t64 : -(double)kInf;
-        const double g = list.s != 0.0f ? log((double)list.s) + ((double)list.m - m) * a.inv_t64 : -(double)kInf;
+        const double g = on != 0.0f ? log((double)on) + ((double)zm - m) * a.inv_t64 : -(double)kInf;
         const double hi = r > g ? r : g, lo = r > g ? g : r, d = log1p(exp(lo - hi));
         l = hi + d;
         logr = r > g ? -d : (r - g) - d;
@@ -587,10 +642,11 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (!ok[i]) continue;
-      const double q = exp(rel[i] - tl);
+      const double logq = ((double)t[i] - tm) * a.inv_t64 - tl;
+      const double qi = kOp == kDistill ? q[i] / sum : exp(logq);
       const double logp = empty ? -(double)kInf : ((double)z[i] - m) * a.inv_t64 - l;
-      q_sum += q;
-      if (!(q <= 0.0)) loss += q * (rel[i] - tl - logp);
+      q_sum += qi;
+      if (!(qi <= 0.0)) loss += qi * (logq - logp);
     }
     q_sum = wave_sum(q_sum);
     loss = wave_sum(loss);
@@ -652,14 +708,19 @@ __device__ __forceinline__ u32x4 pack_vec(const float* f) {
   }
 }
 
-// f(v, value) over the vectors of a part: the new value of each element.
+// f(v, value) over the vectors of a part: the new value of each element. A step's
+// loads are issued before the stores of the one before it, so that a wait for
+// them does not wait for the stores.
 template <bool kF32, typename F>
-__device__ __forceinline__ void map_part(const char* z, char* dz, int n, F f) {
+__device__ __forceinline__ void map_part(const char* z, char* dz, int lo, int n, F f) {
   constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
+  const int tid = (int)threadIdx.x;
+  u32x4 r[kVecs];
+  load_step<kF32>(r, z, 0, tid, lo, n);
   for (int c = 0; c * kChunk < n; ++c) {
-    const int v0 = c * kVecs * kThreads + (int)threadIdx.x;
-    u32x4 r[kVecs];
-    load_step<kF32>(r, z, c, v0, n);
+    const int v0 = c * kVecs * kThreads + tid;
+    u32x4 next[kVecs];
+    if ((c + 1) * kChunk < n) load_step<kF32>(next, z, c + 1, v0 + kVecs * kThreads, lo, n);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int v = v0 + u * kThreads;
@@ -668,36 +729,39 @@ __device__ __forceinline__ void map_part(const char* z, char* dz, int n, F f) {
 #pragma unroll
       for (int i = 0; i < kE; ++i) x[i] = elem<kF32>(r[u], i);
       f(v, x);
-      store_vec<kF32>(dz, v, n, pack_vec<kF32>(x));
+      store_vec<kF32>(dz, v, lo, n, pack_vec<kF32>(x));
     }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) r[u] = next[u];
   }
 }
 template <bool kF32>
-__device__ __forceinline__ void zero_part(char* dz, int n) {
+__device__ __forceinline__ void zero_part(char* dz, int lo, int n) {
   for (int v = threadIdx.x; v * Elem<kF32>::kE < n; v += kThreads)
-    store_vec<kF32>(dz, v, n, u32x4{0, 0, 0, 0});
+    store_vec<kF32>(dz, v, lo, n, u32x4{0, 0, 0, 0});
 }
 
 // dz_j = (g ([j = target] - p_j) - h p_j (log p_j + H)) / t.
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(RowsBwd a) {
   constexpr int kE = Elem<kF32>::kE;
-  const int64_t row = blockIdx.x / (uint32_t)a.S;
-  const int first = (int)(blockIdx.x - (uint32_t)row * (uint32_t)a.S) * a.part, n = min(a.part, a.V - first);
-  const char* z = a.Z + row * a.ldz + (int64_t)first * Elem<kF32>::kBytes;
-  char* dz = a.dZ + row * a.lddz + (int64_t)first * Elem<kF32>::kBytes;
+  const Part in = part_of<kF32>(a.Z, a.ldz, a.S, a.part, a.V);
+  const int64_t row = in.row;
+  const int shift = in.shift, first = in.first, lo = in.lo, n = in.n;
+  const char* z = a.Z + row * a.ldz + (int64_t)(first - shift) * Elem<kF32>::kBytes;
+  char* dz = a.dZ + row * a.lddz + (int64_t)(first - shift) * Elem<kF32>::kBytes;
   const float m = a.stats[row * 3], l = a.stats[row * 3 + 1], H = a.stats[row * 3 + 2];
   const int64_t y = a.target ? a.target[row] : -1;
   const float g = a.g_logp && y >= 0 && y < a.V ? a.g_logp[row] : 0.0f;
   const float h = a.g_entropy ? a.g_entropy[row] : 0.0f;
   if ((m == -kInf && l == 0.0f) || (g == 0.0f && h == 0.0f)) {
-    zero_part<kF32>(dz, n);
+    zero_part<kF32>(dz, lo, n);
     return;
   }
   const float c2 = a.c2, l2 = l * 1.44269504088896340736f;
   const float ca = -(g + h * H) * a.inv_t, cb = -h * (float)kLn2 * a.inv_t, one = g * a.inv_t;
-  const int hot = (int)(y - first);  // may lie outside the part
-  map_part<kF32>(z, dz, n, [&](int v, float* x) {
+  const int hot = (int)(y + shift - first);  // may lie outside the part
+  map_part<kF32>(z, dz, lo, n, [&](int v, float* x) {
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const float p2 = __builtin_fmaf(x[i] - m, c2, -l2);
@@ -718,23 +782,24 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(RowsBwd a) {
   __shared__ int s_id[kThreads];
   __shared__ float s_q[kThreads];
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x / (uint32_t)a.S;
-  const int first = (int)(blockIdx.x - (uint32_t)row * (uint32_t)a.S) * a.part, n = min(a.part, a.V - first);
-  const char* z = a.Z + row * a.ldz + (int64_t)first * Elem<kF32>::kBytes;
-  char* dz = a.dZ + row * a.lddz + (int64_t)first * Elem<kF32>::kBytes;
+  const Part in = part_of<kF32>(a.Z, a.ldz, a.S, a.part, a.V);
+  const int64_t row = in.row;
+  const int shift = in.shift, first = in.first, lo = in.lo, n = in.n;
+  const char* z = a.Z + row * a.ldz + (int64_t)(first - shift) * Elem<kF32>::kBytes;
+  char* dz = a.dZ + row * a.lddz + (int64_t)(first - shift) * Elem<kF32>::kBytes;
   const float* s = a.stats + row * 6;
   const float m = s[0], l2 = s[1] * 1.44269504088896340736f, w = s[2], off = s[3];
   const float gt = a.g[row] * a.inv_t;
   if ((m == -kInf && s[1] == 0.0f) || gt == 0.0f) {
-    zero_part<kF32>(dz, n);
+    zero_part<kF32>(dz, lo, n);
     return;
   }
   const float c2 = a.c2;
   int id = -1;
   float zi = -kInf, q = 0.0f;
   if (tid < a.k) {
-    const int64_t at = row * a.k + tid, j = a.ids[at] - first;
-    if (j >= 0 && j < n) {
+    const int64_t at = row * a.k + tid, j = a.ids[at] + shift - first;
+    if (j >= lo && j < n) {
       id = (int)j;
       zi = load_elem<kF32>(z, j);
       const float t = a.values_f32 ? load_elem<true>(a.values, at) : load_elem<false>(a.values, at);
@@ -756,10 +821,10 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(RowsBwd a) {
     }
   }
   // off p_j as one power of two: off may be as large as p_j is small
-  const float go = off < 0.0f ? -gt : gt, shift = __log2f(fabsf(off)) - l2;
-  map_part<kF32>(z, dz, n, [&](int, float* x) {
+  const float go = off < 0.0f ? -gt : gt, up = __log2f(fabsf(off)) - l2;
+  map_part<kF32>(z, dz, lo, n, [&](int, float* x) {
 #pragma unroll
-    for (int i = 0; i < Elem<kF32>::kE; ++i) x[i] = exp2_(__builtin_fmaf(x[i] - m, c2, shift)) * go;
+    for (int i = 0; i < Elem<kF32>::kE; ++i) x[i] = exp2_(__builtin_fmaf(x[i] - m, c2, up)) * go;
   });
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -773,21 +838,29 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(RowsBwd a) {
   }
 }
 
-// Parts of a row in the forward passes.
+// Parts of a row, for positions up to V and the largest shift of its rows.
 struct Parts {
   int S, part;
 };
-Parts fwd_parts(int64_t T, int64_t V) {
-  const int64_t units = (V + kUnit - 1) / kUnit;
-  int64_t S = std::min<int64_t>({(int64_t)kMaxParts, units, (1024 + T - 1) / T});
-  S = std::max(S, (units + kMaxUnits - 1) / kMaxUnits);
+Parts split_row(int64_t units, int64_t S) {
   const int64_t per = (units + S - 1) / S;
   return Parts{(int)((units + per - 1) / per), (int)(per * kUnit)};
 }
-// ... and in the backward passes: more of it to a workgroup where there are many rows.
-Parts bwd_parts(int64_t T, int64_t V) {
-  const int64_t units = (V + kUnit - 1) / kUnit, per = T * units >= 4096 ? 4 : 1;
-  return Parts{(int)((units + per - 1) / per), (int)(per * kUnit)};
+int64_t units_of(int64_t V, int shift) { return (V + shift + kUnit - 1) / kUnit; }
+Parts fwd_parts(int64_t T, int64_t V, int shift) {
+  const int64_t units = units_of(V, shift);
+  const int64_t S = std::min<int64_t>({(int64_t)kMaxParts, units, (1024 + T - 1) / T});
+  return split_row(units, std::max(S, (units + kMaxUnits - 1) / kMaxUnits));
+}
+// In the backward passes, more of a row to a workgroup where there are many rows.
+Parts bwd_parts(int64_t T, int64_t V, int shift) {
+  const int64_t units = units_of(V, shift), per = T * units >= 4096 ? 4 : 1;
+  return split_row(units, (units + per - 1) / per);
+}
+int largest_shift(const Logits& z) {
+  const int64_t bytes = z.f32 ? 4 : 2;
+  const bool aligned = reinterpret_cast<uintptr_t>(z.Z) % 16 == 0 && (z.T == 1 || z.ldz * bytes % 16 == 0);
+  return aligned ? 0 : (int)(16 / bytes - 1);
 }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -804,8 +877,9 @@ void carve(RowsFwd& a, int64_t T, int n_top, void* ws) {
 template <bool kF32, int kOp, bool kTop>
 hipError_t run_fwd(const RowsFwd& a, int64_t T, hipStream_t stream) {
   size_t lds = 0;
-  if (kOp == kDistillRest) lds = ((size_t)std::min(a.part, a.V) + 127) / 128 * 16;
-  if (kTop) lds = sizeof(TopLds) + (size_t)((std::min(a.part, a.V) + Elem<kF32>::kChunk - 1) / Elem<kF32>::kChunk) * kThreads * 4;
+  const size_t n = (size_t)std::min(a.part, a.V + 7);  // positions of a part
+  if (kOp == kDistillRest) lds = (n + 127) / 128 * 16;
+  if (kTop) lds = sizeof(TopLds) + (n + Elem<kF32>::kChunk - 1) / Elem<kF32>::kChunk * kThreads * 4;
   rows_fwd_kernel<kF32, kOp, kTop><<<dim3((unsigned)(T * a.S)), dim3(kThreads), lds, stream>>>(a);
   return hipGetLastError();
 }
@@ -813,14 +887,13 @@ hipError_t run_fwd(const RowsFwd& a, int64_t T, hipStream_t stream) {
 }  // namespace
 
 size_t logits_workspace_bytes(int64_t T, int64_t V, int n_top) {
-  const Parts p = fwd_parts(T, V);
-  if (p.S == 1) return 256;
-  return (size_t)(up256(T * p.S * 8) + up256(T * p.S * 16) + up256(T * p.S * 8 * n_top));
+  const int64_t S = std::max(fwd_parts(T, V, 0).S, fwd_parts(T, V, 7).S);
+  return (size_t)(up256(T * S * 8) + up256(T * S * 16) + up256(T * S * 8 * n_top));
 }
 
 hipError_t launch_logprobs_fwd(const Logits& z, const int64_t* target, float* logp, float* entropy, int n_top,
                                int64_t* top_ids, float* top_logp, float* stats, void* ws, hipStream_t stream) {
-  const Parts p = fwd_parts(z.T, z.V);
+  const Parts p = fwd_parts(z.T, z.V, largest_shift(z));
   RowsFwd a{};
   a.Z = reinterpret_cast<const char*>(z.Z);
   a.ldz = z.ldz * (z.f32 ? 4 : 2);
@@ -838,7 +911,7 @@ hipError_t launch_logprobs_fwd(const Logits& z, const int64_t* target, float* lo
 
 hipError_t launch_distill_fwd(const Logits& z, const TopLogits& t, const float* teacher_lse, float* loss,
                               float* stats, void* ws, hipStream_t stream) {
-  const Parts p = fwd_parts(z.T, z.V);
+  const Parts p = fwd_parts(z.T, z.V, largest_shift(z));
   RowsFwd a{};
   a.Z = reinterpret_cast<const char*>(z.Z);
   a.ldz = z.ldz * (z.f32 ? 4 : 2);
@@ -856,7 +929,7 @@ hipError_t launch_distill_fwd(const Logits& z, const TopLogits& t, const float* 
 }
 
 static RowsBwd bwd_args(const Logits& z, const float* stats, void* dZ, int64_t lddz) {
-  const Parts p = bwd_parts(z.T, z.V);
+  const Parts p = bwd_parts(z.T, z.V, largest_shift(z));
   RowsBwd a{};
   a.Z = reinterpret_cast<const char*>(z.Z);
   a.ldz = z.ldz * (z.f32 ? 4 : 2);
