@@ -15,6 +15,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace qlora {
 
@@ -49,6 +50,12 @@ struct Elem {
   static constexpr int kBytes = kF32 ? 4 : 2;
 };
 
+// kPast: past the caches, for logits that outgrow the last-level one (256 MiB)
+// together with what is written: us without and with, forward 4096 x 32768 52
+// and 46, 2048 x 131072 95 and 86, backward 98 and 92, 186 and 181; forward and
+// backward of 1024 x 32768, which fits, 39 and 41.
+constexpr int64_t kPastBytes = (int64_t)128 << 20;
+
 // Positions [lo, n) of a part hold elements of the row; of vector v those
 // outside are -inf.
 template <bool kF32>
@@ -74,12 +81,14 @@ __device__ __forceinline__ u32x4 load_vec(const char* part, int v, int lo, int n
   }
   return r;
 }
-template <bool kF32>
+template <bool kF32, bool kPast>
 __device__ __forceinline__ void store_vec(char* part, int v, int lo, int n, u32x4 r) {
   constexpr int kE = Elem<kF32>::kE;
   const int from = lo - v * kE, to = n - v * kE;
   if (from <= 0 && to >= kE) {
-    *reinterpret_cast<u32x4_row*>(part + (int64_t)v * 16) = r;
+    u32x4_row* to = reinterpret_cast<u32x4_row*>(part + (int64_t)v * 16);
+    if constexpr (kPast) __builtin_nontemporal_store(r, to);
+    else *to = r;
     return;
   }
   if constexpr (kF32) {
@@ -96,12 +105,15 @@ __device__ __forceinline__ void store_vec(char* part, int v, int lo, int n, u32x
 }
 // A thread's vectors of a step, the first of them v0: without a branch to a load
 // where the whole step lies in the row.
-template <bool kF32>
+template <bool kF32, bool kPast>
 __device__ __forceinline__ void load_step(u32x4 (&r)[kVecs], const char* part, int c, int v0, int lo, int n) {
   if (c * Elem<kF32>::kChunk >= lo && (c + 1) * Elem<kF32>::kChunk <= n) {  // uniform
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-      r[u] = *reinterpret_cast<const u32x4_row*>(part + (int64_t)(v0 + u * kThreads) * 16);
+    for (int u = 0; u < kVecs; ++u) {
+      const u32x4_row* from = reinterpret_cast<const u32x4_row*>(part + (int64_t)(v0 + u * kThreads) * 16);
+      if constexpr (kPast) r[u] = __builtin_nontemporal_load(from);
+      else r[u] = *from;
+    }
   } else {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) r[u] = load_vec<kF32>(part, v0 + u * kThreads, lo, n);
@@ -369,7 +381,7 @@ __device__ __forceinline__ void select_top(const char* part, int lo, int n, int 
 // them all, both write the same values). None waits for another, and the
 // flags need no clearing.
 // kBins: steps whose maxima are kept for the largest entries; 0 for none.
-template <bool kF32, int kOp, bool kTop>
+template <bool kF32, int kOp, bool kTop, bool kPast>
 __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   for (int c = 0; c < chunks; ++c) {
     u32x4 r[kVecs];
     const int v0 = c * kVecs * kThreads + tid;
-    load_step<kF32>(r, part, c, v0, lo, n);
+    load_step<kF32, kPast>(r, part, c, v0, lo, n);
     float z[kVecs * kE];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
@@ -711,16 +723,16 @@ __device__ __forceinline__ u32x4 pack_vec(const float* f) {
 // f(v, value) over the vectors of a part: the new value of each element. A step's
 // loads are issued before the stores of the one before it, so that a wait for
 // them does not wait for the stores.
-template <bool kF32, typename F>
+template <bool kF32, bool kPast, typename F>
 __device__ __forceinline__ void map_part(const char* z, char* dz, int lo, int n, F f) {
   constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
   const int tid = (int)threadIdx.x;
   u32x4 r[kVecs];
-  load_step<kF32>(r, z, 0, tid, lo, n);
+  load_step<kF32, kPast>(r, z, 0, tid, lo, n);
   for (int c = 0; c * kChunk < n; ++c) {
     const int v0 = c * kVecs * kThreads + tid;
     u32x4 next[kVecs];
-    if ((c + 1) * kChunk < n) load_step<kF32>(next, z, c + 1, v0 + kVecs * kThreads, lo, n);
+    if ((c + 1) * kChunk < n) load_step<kF32, kPast>(next, z, c + 1, v0 + kVecs * kThreads, lo, n);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int v = v0 + u * kThreads;
@@ -729,7 +741,7 @@ __device__ __forceinline__ void map_part(const char* z, char* dz, int lo, int n,
 #pragma unroll
       for (int i = 0; i < kE; ++i) x[i] = elem<kF32>(r[u], i);
       f(v, x);
-      store_vec<kF32>(dz, v, lo, n, pack_vec<kF32>(x));
+      store_vec<kF32, kPast>(dz, v, lo, n, pack_vec<kF32>(x));
     }
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) r[u] = next[u];
@@ -738,11 +750,11 @@ __device__ __forceinline__ void map_part(const char* z, char* dz, int lo, int n,
 template <bool kF32>
 __device__ __forceinline__ void zero_part(char* dz, int lo, int n) {
   for (int v = threadIdx.x; v * Elem<kF32>::kE < n; v += kThreads)
-    store_vec<kF32>(dz, v, lo, n, u32x4{0, 0, 0, 0});
+    store_vec<kF32, false>(dz, v, lo, n, u32x4{0, 0, 0, 0});
 }
 
 // dz_j = (g ([j = target] - p_j) - h p_j (log p_j + H)) / t.
-template <bool kF32>
+template <bool kF32, bool kPast>
 __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(RowsBwd a) {
   constexpr int kE = Elem<kF32>::kE;
   const Part in = part_of<kF32>(a.Z, a.ldz, a.S, a.part, a.V);
@@ -761,7 +773,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(RowsBwd a) {
   const float c2 = a.c2, l2 = l * 1.44269504088896340736f;
   const float ca = -(g + h * H) * a.inv_t, cb = -h * (float)kLn2 * a.inv_t, one = g * a.inv_t;
   const int hot = (int)(y + shift - first);  // may lie outside the part
-  map_part<kF32>(z, dz, lo, n, [&](int v, float* x) {
+  map_part<kF32, kPast>(z, dz, lo, n, [&](int v, float* x) {
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const float p2 = __builtin_fmaf(x[i] - m, c2, -l2);
@@ -777,7 +789,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(RowsBwd a) {
 // dz_j = g / t (w p_j - q_j) on the list, g / t off p_j off it. Every element
 // is first written as one off the list; the listed ones, whose logits were
 // read before, after that.
-template <bool kF32>
+template <bool kF32, bool kPast>
 __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(RowsBwd a) {
   __shared__ int s_id[kThreads];
   __shared__ float s_q[kThreads];
@@ -822,7 +834,7 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(RowsBwd a) {
   }
   // off p_j as one power of two: off may be as large as p_j is small
   const float go = off < 0.0f ? -gt : gt, up = __log2f(fabsf(off)) - l2;
-  map_part<kF32>(z, dz, lo, n, [&](int, float* x) {
+  map_part<kF32, kPast>(z, dz, lo, n, [&](int, float* x) {
 #pragma unroll
     for (int i = 0; i < Elem<kF32>::kE; ++i) x[i] = exp2_(__builtin_fmaf(x[i] - m, c2, up)) * go;
   });
@@ -852,9 +864,10 @@ Parts fwd_parts(int64_t T, int64_t V, int shift) {
   const int64_t S = std::min<int64_t>({(int64_t)kMaxParts, units, (1024 + T - 1) / T});
   return split_row(units, std::max(S, (units + kMaxUnits - 1) / kMaxUnits));
 }
-// In the backward passes, more of a row to a workgroup where there are many rows.
+// In the backward passes one unit to a workgroup (us with one, two and four:
+// 4096 x 32768 98, 106, 111, 1024 x 98304 76, 81, 87), as long as the grid holds them.
 Parts bwd_parts(int64_t T, int64_t V, int shift) {
-  const int64_t units = units_of(V, shift), per = T * units >= 4096 ? 4 : 1;
+  const int64_t units = units_of(V, shift), per = T * units >> 30 ? 4 : 1;
   return split_row(units, (units + per - 1) / per);
 }
 int largest_shift(const Logits& z) {
@@ -874,14 +887,29 @@ void carve(RowsFwd& a, int64_t T, int n_top, void* ws) {
   a.lists = reinterpret_cast<uint64_t*>(p);
 }
 
-template <bool kF32, int kOp, bool kTop>
-hipError_t run_fwd(const RowsFwd& a, int64_t T, hipStream_t stream) {
-  size_t lds = 0;
-  const size_t n = (size_t)std::min(a.part, a.V + 7);  // positions of a part
-  if (kOp == kDistillRest) lds = (n + 127) / 128 * 16;
-  if (kTop) lds = sizeof(TopLds) + (n + Elem<kF32>::kChunk - 1) / Elem<kF32>::kChunk * kThreads * 4;
-  rows_fwd_kernel<kF32, kOp, kTop><<<dim3((unsigned)(T * a.S)), dim3(kThreads), lds, stream>>>(a);
-  return hipGetLastError();
+bool past_caches(const Logits& z) { return z.T * z.V * (z.f32 ? 4 : 2) > kPastBytes; }
+
+// f(type is float32, past the caches), both as constants.
+template <typename F>
+hipError_t by_kind(const Logits& z, F f) {
+  const auto of = [&](auto f32) {
+    return past_caches(z) ? f(f32, std::true_type{}) : f(f32, std::false_type{});
+  };
+  return z.f32 ? of(std::true_type{}) : of(std::false_type{});
+}
+
+template <int kOp, bool kTop>
+hipError_t run_fwd(const RowsFwd& a, const Logits& z, hipStream_t stream) {
+  return by_kind(z, [&](auto f32, auto past) {
+    constexpr bool kF32 = decltype(f32)::value;
+    const size_t n = (size_t)std::min(a.part, a.V + 7);  // positions of a part
+    size_t lds = 0;
+    if (kOp == kDistillRest) lds = (n + 127) / 128 * 16;
+    if (kTop) lds = sizeof(TopLds) + (n + Elem<kF32>::kChunk - 1) / Elem<kF32>::kChunk * kThreads * 4;
+    rows_fwd_kernel<kF32, kOp, kTop, decltype(past)::value>
+        <<<dim3((unsigned)(z.T * a.S)), dim3(kThreads), lds, stream>>>(a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
@@ -905,8 +933,7 @@ hipError_t launch_logprobs_fwd(const Logits& z, const int64_t* target, float* lo
   a.target = target; a.logp = logp; a.entropy = entropy;
   a.n_top = n_top; a.top_ids = top_ids; a.top_logp = top_logp;
   carve(a, z.T, n_top, ws);
-  if (n_top) return z.f32 ? run_fwd<true, kLogprobs, true>(a, z.T, stream) : run_fwd<false, kLogprobs, true>(a, z.T, stream);
-  return z.f32 ? run_fwd<true, kLogprobs, false>(a, z.T, stream) : run_fwd<false, kLogprobs, false>(a, z.T, stream);
+  return n_top ? run_fwd<kLogprobs, true>(a, z, stream) : run_fwd<kLogprobs, false>(a, z, stream);
 }
 
 hipError_t launch_distill_fwd(const Logits& z, const TopLogits& t, const float* teacher_lse, float* loss,
@@ -923,9 +950,7 @@ hipError_t launch_distill_fwd(const Logits& z, const TopLogits& t, const float* 
   a.ids = t.ids; a.values = t.values; a.values_f32 = t.f32; a.k = t.k;
   a.teacher_lse = teacher_lse; a.loss = loss;
   carve(a, z.T, 0, ws);
-  if (teacher_lse)
-    return z.f32 ? run_fwd<true, kDistillRest, false>(a, z.T, stream) : run_fwd<false, kDistillRest, false>(a, z.T, stream);
-  return z.f32 ? run_fwd<true, kDistill, false>(a, z.T, stream) : run_fwd<false, kDistill, false>(a, z.T, stream);
+  return teacher_lse ? run_fwd<kDistillRest, false>(a, z, stream) : run_fwd<kDistill, false>(a, z, stream);
 }
 
 static RowsBwd bwd_args(const Logits& z, const float* stats, void* dZ, int64_t lddz) {
@@ -946,24 +971,22 @@ hipError_t launch_logprobs_bwd(const Logits& z, const int64_t* target, const flo
                                const float* g_entropy, void* dZ, int64_t lddz, hipStream_t stream) {
   RowsBwd a = bwd_args(z, stats, dZ, lddz);
   a.target = target; a.g_logp = g_logp; a.g_entropy = g_entropy;
-  const dim3 grid((unsigned)(z.T * a.S));
-  if (z.f32)
-    logprobs_bwd_kernel<true><<<grid, dim3(kThreads), 0, stream>>>(a);
-  else
-    logprobs_bwd_kernel<false><<<grid, dim3(kThreads), 0, stream>>>(a);
-  return hipGetLastError();
+  return by_kind(z, [&](auto f32, auto past) {
+    logprobs_bwd_kernel<decltype(f32)::value, decltype(past)::value>
+        <<<dim3((unsigned)(z.T * a.S)), dim3(kThreads), 0, stream>>>(a);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_distill_bwd(const Logits& z, const TopLogits& t, const float* stats, const float* g, void* dZ,
                               int64_t lddz, hipStream_t stream) {
   RowsBwd a = bwd_args(z, stats, dZ, lddz);
   a.ids = t.ids; a.values = t.values; a.values_f32 = t.f32; a.k = t.k; a.g = g;
-  const dim3 grid((unsigned)(z.T * a.S));
-  if (z.f32)
-    distill_bwd_kernel<true><<<grid, dim3(kThreads), 0, stream>>>(a);
-  else
-    distill_bwd_kernel<false><<<grid, dim3(kThreads), 0, stream>>>(a);
-  return hipGetLastError();
+  return by_kind(z, [&](auto f32, auto past) {
+    distill_bwd_kernel<decltype(f32)::value, decltype(past)::value>
+        <<<dim3((unsigned)(z.T * a.S)), dim3(kThreads), 0, stream>>>(a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace qlora
