@@ -23,8 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kVecs = 4;             // vectors of 16 bytes a thread loads at once
-constexpr int kUnit = 8192;          // parts of a row are multiples of this many elements
+constexpr int kUnit = 8192;          // entries of a step of a workgroup; parts of a row are multiples of it
 constexpr int kMaxUnits = 16;        // ... and at most this many of them
 constexpr int kMaxParts = 32;
 constexpr int kMaxTop = 64;
@@ -46,7 +45,7 @@ typedef u32x4 u32x4_row __attribute__((aligned(2)));
 template <bool kF32>
 struct Elem {
   static constexpr int kE = kF32 ? 4 : 8;                       // elements of a vector
-  static constexpr int kChunk = kThreads * kVecs * kE;          // a workgroup's loads of one step
+  static constexpr int kVecs = kUnit / kThreads / kE;           // vectors a thread loads at once
   static constexpr int kBytes = kF32 ? 4 : 2;
 };
 
@@ -106,8 +105,9 @@ __device__ __forceinline__ void store_vec(char* part, int v, int lo, int n, u32x
 // A thread's vectors of a step, the first of them v0: without a branch to a load
 // where the whole step lies in the row.
 template <bool kF32, bool kPast>
-__device__ __forceinline__ void load_step(u32x4 (&r)[kVecs], const char* part, int c, int v0, int lo, int n) {
-  if (c * Elem<kF32>::kChunk >= lo && (c + 1) * Elem<kF32>::kChunk <= n) {  // uniform
+__device__ __forceinline__ void load_step(u32x4 (&r)[Elem<kF32>::kVecs], const char* part, int c, int v0, int lo, int n) {
+  constexpr int kVecs = Elem<kF32>::kVecs;
+  if (c * kUnit >= lo && (c + 1) * kUnit <= n) {  // uniform
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const u32x4_row* from = reinterpret_cast<const u32x4_row*>(part + (int64_t)(v0 + u * kThreads) * 16);
@@ -229,15 +229,38 @@ __device__ __forceinline__ uint32_t idx_of(uint64_t pair) { return 0xffffffffu -
 
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint64_t wave_largest(uint64_t v) { return wave_reduce(v, (uint64_t)0, larger); }
-// The r-th largest of the lanes' values (with multiplicity).
-__device__ __forceinline__ uint64_t wave_rth(uint64_t v, int r) {
-  uint64_t top = wave_largest(v);
-  for (int i = 1; i < r; ++i) {
-    const uint64_t at = __ballot(v == top);
-    if ((int)(threadIdx.x & 63) == __builtin_ctzll(at)) v = 0;
-    top = wave_largest(v);
+// Of the lanes' pairs of a key and a step, the r-th in the order larger keys, lower
+// steps first (with multiplicity; r at most the lanes).
+template <bool kF32>
+__device__ __forceinline__ void wave_rth(uint32_t& key, uint32_t& step, int r) {
+  uint32_t v = key, top;
+  const uint32_t mine = step;
+  if (r <= 2) {  // the largest, and perhaps the next
+    for (;;) {
+      top = wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+      const int c = __builtin_popcountll(__ballot(v == top));
+      if (r <= c) break;
+      r -= c;
+      if (v == top) v = 0;
+    }
+  } else {
+    // bit by bit, the lanes whose key may be it (the keys of bf16 logits differ in
+    // their upper 16 bits if at all)
+    uint64_t left = ~0ull;
+#pragma unroll 1
+    for (int bit = 31; bit >= (kF32 ? 0 : 16); --bit) {
+      const uint64_t ones = __ballot((v >> bit) & 1) & left;
+      const int c = __builtin_popcountll(ones);
+      left = c >= r ? ones : left & ~ones;
+      r -= c >= r ? 0 : c;
+    }
+    top = __builtin_amdgcn_readlane((int)v, __builtin_ctzll(left));
   }
-  return top;
+  uint32_t s = 0;
+#pragma unroll 1
+  while (__builtin_popcountll(__ballot(v == top && mine <= s)) < r) ++s;
+  key = top;
+  step = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -285,42 +308,37 @@ struct TopLds {
   int n_items, n_cand;
 };
 
-// Ranks the candidates (all pairs differ) and hands the first `need` to put.
-template <typename Put>
-__device__ __forceinline__ void rank_candidates(const TopLds& t, int count, int need, Put put) {
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    const uint64_t mine = t.cand[i];
-    int rank = 0;
-    for (int j = 0; j < count; ++j) rank += t.cand[j] > mine;
-    if (rank < need) put(rank, mine);
-  }
-}
-
-// The `need` largest entries of a part. bins [chunks][kThreads]: key of the
-// maximum of each thread's vectors of each step; best: the thread's largest
-// bin as (key, first position of the step), an upper bound in that coarser order
-// for all its entries, and attained by one of them unless they are all NaN.
-// The r-th largest of them in each of w full waves, r = need / w rounded up,
-// has r entries at or above it in that wave, so the smallest of the waves'
-// has `need`: only the bins that reach it are read again (from the L2), and
-// what reaches it there is ranked.
-template <bool kF32, typename Put>
-__device__ __forceinline__ void select_top(const char* part, int lo, int n, int first, int chunks,
-                                           const uint32_t* bins, uint64_t best, int need, TopLds& t,
-                                           Put put) {
-  constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
+// The `need` largest entries of a part, among the returned number of candidates in
+// t.cand (all different). bins [steps][kThreads]: key of the maximum of each
+// thread's vectors of each step; best: the thread's largest bin as (key, first
+// position of the step), an upper bound in that coarser order for all its
+// entries, and attained by one of them unless they are all NaN. The r-th largest
+// of them in each of w full waves, r = need / w rounded up, has r entries at or
+// above it in that wave, so the smallest of the waves' has `need`: only the
+// bins that reach it are read again (from the L2).
+// The code is kept short: a few rows run all of it once, and fetching it costs
+// as much as running it (one row of 131072 with 20 entries 12.4 us from a graph,
+// 14.1 with the steps below unrolled and entries taken from registers; 6.0
+// without entries, where a launch alone takes 4).
+template <bool kF32>
+__device__ __forceinline__ int select_top(const char* part, int lo, int n, int first, int steps,
+                                          const uint32_t* bins, uint64_t best, int need, TopLds& t) {
+  constexpr int kE = Elem<kF32>::kE, kVecs = Elem<kF32>::kVecs;
   const int tid = threadIdx.x, wave = tid >> 6;
   const int full = min(kWaves, n / kE / 64);  // waves whose lanes all hold an entry
   if (full) {
-    const uint64_t r = wave_rth(best, (need + full - 1) / full);
-    if ((tid & 63) == 0) t.wave[wave] = r;
+    uint32_t key = (uint32_t)(best >> 32), step = best ? (idx_of(best) - (uint32_t)first) / kUnit : 0;
+    wave_rth<kF32>(key, step, (need + full - 1) / full);
+    if ((tid & 63) == 0) t.wave[wave] = pair_of(key, (uint32_t)first + step * kUnit);
   }
   if (tid == 0) t.n_items = t.n_cand = 0;
   __syncthreads();
   uint64_t t0 = full ? ~0ull : 0;
+#pragma unroll 1
   for (int w = 0; w < full; ++w) t0 = t.wave[w] < t0 ? t.wave[w] : t0;
-  auto coarse = [&](uint32_t key, int b) { return pair_of(key, (uint32_t)(first + b * kChunk)); };
-  for (int b = 0; b < chunks; ++b) {
+  auto coarse = [&](uint32_t key, int b) { return pair_of(key, (uint32_t)(first + b * kUnit)); };
+#pragma unroll 1
+  for (int b = 0; b < steps; ++b) {
     const uint32_t key = bins[b * kThreads + tid];
     if (key && coarse(key, b) >= t0) {
       const int i = atomicAdd(&t.n_items, 1);
@@ -328,50 +346,58 @@ __device__ __forceinline__ void select_top(const char* part, int lo, int n, int 
     }
   }
   __syncthreads();
-  const int items = t.n_items;
-  // f(key, position, step) over the entries of the bins listed, or of all
-  auto each = [&](bool all, auto f) {
-    const int units = (all ? chunks * kThreads : items) * kVecs;
-    for (int w = tid; w < units; w += kThreads) {
-      const int it = all ? w / kVecs : t.items[w / kVecs];
-      const int b = it / kThreads, v = (b * kVecs + w % kVecs) * kThreads + it % kThreads;
+  // Pass -1 collects the entries at or above t0 of the bins listed. Where those are
+  // too many (equal entries), or, with NaN, too few, each further pass takes
+  // the next entry in order, of the bins listed or of all.
+  bool all = t.n_items > kMaxItems;
+  uint64_t prev = ~0ull;
+#pragma unroll 1
+  for (int pass = all ? 0 : -1; pass < need; ++pass) {
+    const int bins_here = all ? steps * kThreads : t.n_items;
+    const float zt = all ? -kInf : of_key((uint32_t)(t0 >> 32));  // NaN for 0: everything
+    uint64_t top = 0;
+#pragma unroll 1
+    for (int w = tid; w < bins_here * kVecs; w += kThreads) {
+      const int it = all ? w / kVecs : t.items[w / kVecs], b = it / kThreads;
+      const int v = (b * kVecs + w % kVecs) * kThreads + it % kThreads;
       if (v * kE >= n) continue;
       const u32x4 x = load_vec<kF32>(part, v, lo, n);
+      uint32_t hits = 0;
 #pragma unroll
-      for (int i = 0; i < kE; ++i)
-        if (v * kE + i >= lo && v * kE + i < n) f(key_of(elem<kF32>(x, i)), (uint32_t)(first + v * kE + i), b);
+      for (int i = 0; i < kE; ++i) hits |= !(elem<kF32>(x, i) < zt) ? 1u << i : 0u;
+#pragma unroll 1
+      while (hits) {
+        const int at = v * kE + __builtin_ctz(hits);
+        hits &= hits - 1;
+        if (at < lo || at >= n) continue;
+        const uint32_t key = key_of(load_elem<kF32>(part, at));
+        const uint64_t p = pair_of(key, (uint32_t)(first + at));
+        if (pass >= 0) {
+          if (p < prev && p > top) top = p;
+        } else if (coarse(key, b) >= t0) {
+          const int c = atomicAdd(&t.n_cand, 1);
+          if (c < kMaxCand) t.cand[c] = p;
+        }
+      }
     }
-  };
-  bool all = items > kMaxItems;
-  if (!all)
-    each(false, [&](uint32_t key, uint32_t idx, int b) {
-      if (coarse(key, b) < t0) return;
-      const int i = atomicAdd(&t.n_cand, 1);
-      if (i < kMaxCand) t.cand[i] = pair_of(key, idx);
-    });
-  __syncthreads();
-  const int count = t.n_cand;
-  if (!all && count >= need && count <= kMaxCand) {
-    rank_candidates(t, count, need, put);
-    return;
-  }
-  // Many equal entries, or NaN: one entry after another.
-  all = all || count < need;
-  uint64_t prev = ~0ull;
-  for (int r = 0; r < need; ++r) {
-    uint64_t top = 0;
-    each(all, [&](uint32_t key, uint32_t idx, int) {
-      const uint64_t p = pair_of(key, idx);
-      if (p < prev && p > top) top = p;
-    });
-    top = wave_largest(top);
+    if (pass >= 0) {
+      top = wave_largest(top);
+      if ((tid & 63) == 0) t.wave[wave] = top;
+    }
     __syncthreads();
-    if ((tid & 63) == 0) t.wave[wave] = top;
-    __syncthreads();
-    for (int w = 0; w < kWaves; ++w) top = larger(top, t.wave[w]);
-    if (tid == 0) put(r, top);
-    prev = top;
+    if (pass < 0) {
+      const int count = t.n_cand;
+      if (count >= need && count <= kMaxCand) return count;
+      all = count < need;
+    } else {
+#pragma unroll 1
+      for (int w = 0; w < kWaves; ++w) top = larger(top, t.wave[w]);
+      if (tid == 0) t.cand[pass] = top;
+      prev = top;
+      __syncthreads();
+    }
   }
+  return need;
 }
 
 // One (row, part) per workgroup. Where a row has several, each stores its
@@ -383,7 +409,7 @@ __device__ __forceinline__ void select_top(const char* part, int lo, int n, int 
 // kBins: steps whose maxima are kept for the largest entries; 0 for none.
 template <bool kF32, int kOp, bool kTop, bool kPast>
 __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
-  constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
+  constexpr int kE = Elem<kF32>::kE, kVecs = Elem<kF32>::kVecs;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   __shared__ Soft s_soft[kWaves];
   __shared__ int s_last, s_twice;
@@ -393,11 +419,19 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   const int shift = in.shift, first = in.first, lo = in.lo, n = in.n, split = first / a.part;
   const char* zrow = a.Z + row * a.ldz;
   const char* part = zrow + (int64_t)(first - shift) * Elem<kF32>::kBytes;
-  const int chunks = (n + kChunk - 1) / kChunk;
+  const int steps = (n + kUnit - 1) / kUnit;
   const float c2 = a.c2;
 
+  float zy = 0.0f;  // the target's logit
+  bool counts = false;
+  if (kOp == kLogprobs && a.logp) {
+    const int64_t y = a.target[row];
+    counts = y >= 0 && y < a.V;
+    if (counts) zy = load_elem<kF32>(zrow, y);
+  }
   TopLds& top = *reinterpret_cast<TopLds*>(dyn);
   uint32_t* bins = reinterpret_cast<uint32_t*>(dyn + sizeof(TopLds));
+  uint64_t* s_lists = reinterpret_cast<uint64_t*>(bins);  // after the part's own selection: [S][n_top]
   uint32_t* mask = reinterpret_cast<uint32_t*>(dyn);  // bit i: position first + i is on the list
   if constexpr (kOp == kDistillRest) {
     if (tid == 0) s_twice = 0;
@@ -414,11 +448,11 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
 
   Soft acc = kNone;  // without the listed entries where the list's rest is a class
   uint64_t best = 0;
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = 0; c < steps; ++c) {
+    float z[kVecs * kE];
     u32x4 r[kVecs];
     const int v0 = c * kVecs * kThreads + tid;
     load_step<kF32, kPast>(r, part, c, v0, lo, n);
-    float z[kVecs * kE];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
 #pragma unroll
@@ -443,7 +477,7 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
     if constexpr (kTop) {
       const uint32_t key = v0 * kE < n ? key_of(m) : 0;
       bins[c * kThreads + tid] = key;
-      if (key) best = larger(best, pair_of(key, (uint32_t)(first + c * kChunk)));
+      if (key) best = larger(best, pair_of(key, (uint32_t)(first + c * kUnit)));
     }
     m = fmaxf(m, acc.m);
     const float base = base_of(m);
@@ -485,21 +519,53 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   for (int w = 1; w < kWaves; ++w) acc = joined(acc, s_soft[w], c2);
   bool twice = kOp == kDistillRest && s_twice;  // an id is twice on the list
 
-  if (a.S > 1) {
-    const int64_t at = row * a.S + split;
-    if constexpr (kTop) {
-      const int need = min(a.n_top, n - lo);
-      uint64_t* mine = a.lists + at * a.n_top;
-      auto put = [&](int r, uint64_t p) {
-        __hip_atomic_store(mine + r, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      };
-      if (tid >= need && tid < a.n_top) put(tid, 0);
-      if (need > 0) select_top<kF32>(part, lo, n, first, chunks, bins, best, need, top, put);
+  int count = 0, need = kTop ? min(a.n_top, n - lo) : 0;
+  if (kTop && need > 0) count = select_top<kF32>(part, lo, n, first, steps, bins, best, need, top);
+  bool whole = a.S == 1;  // the row's statistics, and not a part's
+#pragma unroll 1
+  for (;;) {
+    const bool empty = acc.m == -kInf && acc.s == 0.0f;
+    float l = 0.0f;
+    if (kOp == kLogprobs && whole) {
+      l = empty ? 0.0f : logf(acc.s);
+      if (tid == 0) {
+        const float H = empty ? 0.0f : l - (float)kLn2 * (acc.u / acc.s);
+        if (a.entropy) a.entropy[row] = H;
+        if (a.stats) {
+          a.stats[row * 3] = acc.m;
+          a.stats[row * 3 + 1] = l;
+          a.stats[row * 3 + 2] = H;
+        }
+        if (a.logp) a.logp[row] = !counts ? 0.0f : empty ? -kInf : (zy - acc.m) * a.inv_t - l;
+      }
     }
+    if constexpr (kTop) {  // the candidates' ranks, and the first of them to their places
+      __syncthreads();
+#pragma unroll 1
+      for (int i = tid; i < count; i += kThreads) {
+        const uint64_t mine = top.cand[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) rank += top.cand[j] > mine;
+        if (rank >= need) continue;
+        if (whole) {
+          a.top_ids[row * a.n_top + rank] = (int64_t)idx_of(mine) - shift;
+          a.top_logp[row * a.n_top + rank] = empty ? -kInf : (of_key((uint32_t)(mine >> 32)) - acc.m) * a.inv_t - l;
+        } else {
+          __hip_atomic_store(a.lists + (int64_t)blockIdx.x * a.n_top + rank, mine, __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
+    }
+    if (whole) break;
+    if (kTop && tid >= need && tid < a.n_top)
+      __hip_atomic_store(a.lists + (int64_t)blockIdx.x * a.n_top + tid, (uint64_t)0, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
     if (tid == 0) {
-      put_agent(a.sums + at * 4, acc.m);
-      put_agent(a.sums + at * 4 + 1, acc.s);
-      put_agent(a.sums + at * 4 + 2, kOp == kLogprobs ? acc.u : twice ? 1.0f : 0.0f);
+      float* p = a.sums + (int64_t)blockIdx.x * 4;
+      put_agent(p, acc.m);
+      put_agent(p + 1, acc.s);
+      put_agent(p + 2, kOp == kLogprobs ? acc.u : twice ? 1.0f : 0.0f);
     }
     // every store of the workgroup acknowledged before its flag
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -532,56 +598,35 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       acc.s = get_agent(p + 1);
       third = get_agent(p + 2);
     }
+    if constexpr (kTop) {
+      // the parts' lists are sorted, and all but the last are whole: each has
+      // r = n_top / (S - 1) rounded up entries at or above its r-th
+      const uint64_t* lists = a.lists + row * a.S * a.n_top;
+      need = a.n_top;
+      const int total = a.S * need, r = (need + a.S - 2) / (a.S - 1);
+#pragma unroll 1
+      for (int i = tid; i < total; i += kThreads)
+        s_lists[i] = __hip_atomic_load(lists + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (tid == 0) top.n_cand = 0;
+      __syncthreads();
+      uint64_t t0 = ~0ull;
+#pragma unroll 4
+      for (int w = 0; w < a.S - 1; ++w) t0 = s_lists[w * need + r - 1] < t0 ? s_lists[w * need + r - 1] : t0;
+#pragma unroll 1
+      for (int i = tid; i < total; i += kThreads) {
+        const uint64_t p = s_lists[i];
+        if (p && p >= t0) top.cand[atomicAdd(&top.n_cand, 1)] = p;
+      }
+      __syncthreads();
+      count = top.n_cand;
+    }
     if constexpr (kOp == kLogprobs) acc.u = third;
     twice = __any(kOp == kDistillRest && third != 0.0f);
     acc = wave_join(acc, c2);
+    whole = true;
   }
 
-  if constexpr (kOp == kLogprobs) {
-    const bool empty = acc.m == -kInf && acc.s == 0.0f;
-    const float l = empty ? 0.0f : logf(acc.s);
-    auto logp_of = [&](float z) { return empty ? -kInf : (z - acc.m) * a.inv_t - l; };
-    if (tid == 0) {
-      const float H = empty ? 0.0f : l - (float)kLn2 * (acc.u / acc.s);
-      if (a.entropy) a.entropy[row] = H;
-      if (a.stats) {
-        a.stats[row * 3] = acc.m;
-        a.stats[row * 3 + 1] = l;
-        a.stats[row * 3 + 2] = H;
-      }
-      if (a.logp) {
-        const int64_t y = a.target[row];
-        a.logp[row] = y >= 0 && y < a.V ? logp_of(load_elem<kF32>(zrow, y)) : 0.0f;
-      }
-    }
-    if constexpr (kTop) {
-      auto put = [&](int r, uint64_t p) {
-        a.top_ids[row * a.n_top + r] = (int64_t)idx_of(p) - shift;
-        a.top_logp[row * a.n_top + r] = logp_of(of_key((uint32_t)(p >> 32)));
-      };
-      if (a.S == 1) {
-        select_top<kF32>(part, lo, n, 0, chunks, bins, best, a.n_top, top, put);
-      } else {
-        // the parts' lists are sorted, and all but the last are whole: each has
-        // r = n_top / (S - 1) rounded up entries at or above its r-th
-        const uint64_t* lists = a.lists + row * a.S * a.n_top;
-        const int r = (a.n_top + a.S - 2) / (a.S - 1);
-        auto get = [&](int i) {
-          return __hip_atomic_load(lists + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        };
-        const uint64_t t0 = ~wave_largest(lane < a.S - 1 ? ~get(lane * a.n_top + r - 1) : 0);
-        __syncthreads();
-        if (tid == 0) top.n_cand = 0;
-        __syncthreads();
-        for (int i = tid; i < a.S * a.n_top; i += kThreads) {
-          const uint64_t p = get(i);
-          if (p && p >= t0) top.cand[atomicAdd(&top.n_cand, 1)] = p;
-        }
-        __syncthreads();
-        rank_candidates(top, top.n_cand, a.n_top, put);
-      }
-    }
-  } else {
+  if constexpr (kOp != kLogprobs) {
     // up to four list entries a lane, in 64 bits
     constexpr int kPer = 4;
     const int64_t at = row * a.k;
@@ -725,14 +770,14 @@ __device__ __forceinline__ u32x4 pack_vec(const float* f) {
 // them does not wait for the stores.
 template <bool kF32, bool kPast, typename F>
 __device__ __forceinline__ void map_part(const char* z, char* dz, int lo, int n, F f) {
-  constexpr int kE = Elem<kF32>::kE, kChunk = Elem<kF32>::kChunk;
+  constexpr int kE = Elem<kF32>::kE, kVecs = Elem<kF32>::kVecs;
   const int tid = (int)threadIdx.x;
   u32x4 r[kVecs];
   load_step<kF32, kPast>(r, z, 0, tid, lo, n);
-  for (int c = 0; c * kChunk < n; ++c) {
+  for (int c = 0; c * kUnit < n; ++c) {
     const int v0 = c * kVecs * kThreads + tid;
     u32x4 next[kVecs];
-    if ((c + 1) * kChunk < n) load_step<kF32, kPast>(next, z, c + 1, v0 + kVecs * kThreads, lo, n);
+    if ((c + 1) * kUnit < n) load_step<kF32, kPast>(next, z, c + 1, v0 + kVecs * kThreads, lo, n);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int v = v0 + u * kThreads;
@@ -905,7 +950,11 @@ hipError_t run_fwd(const RowsFwd& a, const Logits& z, hipStream_t stream) {
     const size_t n = (size_t)std::min(a.part, a.V + 7);  // positions of a part
     size_t lds = 0;
     if (kOp == kDistillRest) lds = (n + 127) / 128 * 16;
-    if (kTop) lds = sizeof(TopLds) + (n + Elem<kF32>::kChunk - 1) / Elem<kF32>::kChunk * kThreads * 4;
+    if (kTop) {
+      const size_t bins = (n + kUnit - 1) / kUnit * kThreads * 4;
+      const size_t lists = a.S > 1 ? (size_t)a.S * a.n_top * 8 : 0;
+      lds = sizeof(TopLds) + std::max(bins, lists);
+    }
     rows_fwd_kernel<kF32, kOp, kTop, decltype(past)::value>
         <<<dim3((unsigned)(z.T * a.S)), dim3(kThreads), lds, stream>>>(a);
     return hipGetLastError();
