@@ -710,21 +710,16 @@ def qlora_fp8_linear_bwd(dY, X8, T, W, A=None, B=None, scale=1.0, fmt=ACT8_E4M3,
 _FLOATS = {torch.bfloat16: 0, torch.float32: 1}  # QLORA_LOGITS_BF16, QLORA_LOGITS_F32
 
 
-def _on(t, dev, name):
-    if t.device != dev:
-        raise QloraError(f"{name} must be on {dev}")
-
-
 def _matrix(t, name, dtypes=_FLOATS):
     """(rows, columns, leading dimension, device) of a matrix on the current
     device whose rows are contiguous."""
     if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda:
         raise QloraError(f"{name} must be a matrix of {' or '.join(map(str, dtypes))} on the GPU")
-    if t.device.index != torch._C._cuda_getDevice():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise QloraError(f"{name} must be on the current device")
     M, K = t.shape
     ld, step = t.stride()
-    if K > 1 and step != 1:
+    if step != 1 and K > 1:
         raise QloraError(f"{name} must have contiguous rows")
     if M <= 1:  # one row: the stride has no meaning
         return M, K, K, t.device
@@ -750,17 +745,17 @@ class Int4Weight:
 
 
 def _need_int4(w, dev):
+    """(N, K) of a weight whose tensors are checked, one condition to each."""
     N, K = w.shape
+    c, s, z = w.codes, w.scales, w.zeros
     groups = -(-K // w.group) if w.group > 0 else -1
-    for t, shape, dtype, name in ((w.codes, (N, K // 2), torch.uint8, "codes"),
-                                  (w.scales, (N, groups), torch.bfloat16, "scales"),
-                                  (w.zeros, (N, groups), torch.uint8, "zeros")):
-        if t is None and name == "zeros":
-            continue
-        _need(t, dtype, f"the weight's {name}")
-        if t.shape != shape:
-            raise QloraError(f"the weight's {name} must have shape {shape}")
-        _on(t, dev, f"the weight's {name}")
+    if c.dtype is not torch.uint8 or c.shape != (N, K // 2) or c.device != dev or not c.is_contiguous():
+        raise QloraError(f"the weight's codes must be a contiguous uint8 tensor of shape {(N, K // 2)} on {dev}")
+    if s.dtype is not torch.bfloat16 or s.shape != (N, groups) or s.device != dev or not s.is_contiguous():
+        raise QloraError(f"the weight's scales must be a contiguous bfloat16 tensor of shape {(N, groups)} on {dev}")
+    if z is not None and (z.dtype is not torch.uint8 or z.shape != (N, groups) or z.device != dev
+                          or not z.is_contiguous()):
+        raise QloraError(f"the weight's zeros must be a contiguous uint8 tensor of shape {(N, groups)} on {dev}")
     return N, K
 
 
@@ -823,11 +818,8 @@ def _logits(Z, name="Z"):
 
 def _row(t, shape, dtype, dev, name):
     """A given tensor of one number (or list) per row, or None."""
-    if t is not None:
-        _need(t, dtype, name)
-        _on(t, dev, name)
-        if t.shape != shape:
-            raise QloraError(f"{name} must have shape {shape}")
+    if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous()):
+        raise QloraError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
     return t
 
 
@@ -856,8 +848,9 @@ def logits_workspace(T, V, n_top, device):
 def _logits_ws(ws, T, V, n_top, dev):
     if ws is None:
         return logits_workspace(T, V, n_top, dev)
-    _on(ws, dev, "ws")
-    return _given_ws(ws)
+    if ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise QloraError(f"ws must be a contiguous uint8 tensor on {dev}")
+    return ws
 
 
 def qlora_logprobs_fwd(Z, target=None, temperature=1.0, n_top=0, want_entropy=True, want_stats=True,
