@@ -407,6 +407,32 @@ def test_gradients_by_differences(q):
             assert np.abs((f[0][i] - f[1][i]) / (2 * e) - _np(d)[:, j]).max() <= tol
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_logits_that_outgrow_the_caches(q, dtype):
+    """Above 128 MiB logits and gradients pass the caches: the same bits as in two
+    halves that do not."""
+    T, V, k = (2100, 40003, 40) if dtype is BF else (2050, 20003, 40)
+    Z, rng = _rows(T, V, dtype)
+    assert T * V * Z.element_size() > 128 << 20 > T // 2 * V * Z.element_size()
+    y = torch.randint(-1, V, (T,), generator=rng, device=Z.device)
+    ids = torch.randint(0, V, (T, k), generator=rng, device=Z.device)
+    values = torch.randn(T, k, generator=rng, device=Z.device) * 3
+    lse = torch.full((T,), 9.0, device=Z.device)
+    g, h = (torch.randn(T, generator=rng, device=Z.device) for _ in range(2))
+
+    def run(a, b):
+        z = Z[a:b]
+        s = q.qlora_logprobs_fwd(z, y[a:b], 0.9, n_top=9)
+        d = q.qlora_distill_fwd(z, ids[a:b], values[a:b], lse[a:b], 0.9)
+        e = q.qlora_distill_fwd(z, ids[a:b], values[a:b], None, 0.9)
+        return [*s, *d, *e, q.qlora_logprobs_bwd(z, y[a:b], s[4], g[a:b], h[a:b], 0.9),
+                q.qlora_distill_bwd(z, ids[a:b], values[a:b], d[1], g[a:b], 0.9)]
+
+    whole, first, second = run(0, T), run(0, T // 2), run(T // 2, T)
+    for w, a, b in zip(whole, first, second):
+        assert torch.equal(w, torch.cat([a, b]))
+
+
 def test_many_rows_past_32_bit_offsets(q):
     """Rows beyond 4 GiB of logits, checked by themselves."""
     T, V = 40000, 60000
