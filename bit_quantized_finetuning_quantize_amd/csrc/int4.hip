@@ -150,7 +150,7 @@ int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __rest
   const int col = (int)(u % per) * 8;
   const uint32_t b = (uint32_t)row * ng + col / kG;
   const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (row * K + col) / 2);
-  const float s = bf16_to_f32(scales[b]), z = zeros ? (float)zeros[b] : 8.0f;
+  const float s = bf16_to_f32(scales[b]), z = zeros ? (float)(zeros[b] & 15u) : 8.0f;
   u32x4 v;
 #pragma unroll
   for (int i = 0; i < 4; ++i)

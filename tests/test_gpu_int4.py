@@ -158,6 +158,17 @@ def test_quantized_product_is_the_dequantized_ones(q):
     assert ((y.double() - x.double() @ d.T.contiguous()).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_upper_bits_of_zero_points_are_not_read(q, G):
+    g = _gen(7, G)
+    w = _weight(q, g, 70, 416, G, False, True)
+    x = torch.randint(-8, 9, (5, 416), generator=g, device=device()).to(BF)
+    y, d = q.qlora_int4_linear_fwd(x, w, F32), q.qlora_int4_dequantize(w)
+    w.zeros |= torch.randint(0, 16, w.zeros.shape, generator=g, device=device(), dtype=torch.uint8) << 4
+    assert (w.zeros > 15).any()
+    assert torch.equal(q.qlora_int4_linear_fwd(x, w, F32), y) and torch.equal(q.qlora_int4_dequantize(w), d)
+
+
 def test_not_finite_tokens_stay_in_their_rows(q):
     g = _gen(4)
     w = _weight(q, g, 100, 256, 64, False, True)
