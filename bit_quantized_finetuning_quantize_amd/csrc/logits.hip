@@ -30,7 +30,9 @@ constexpr int kMaxTop = 64;
 constexpr int kMaxItems = 2048;
 constexpr int kMaxCand = kMaxParts * kMaxTop;
 constexpr float kInf = __builtin_huge_valf();
-constexpr float kLow = -1e30f;       // 0 * kLow is 0 where 0 * -inf would be NaN
+// 2^y is 0 below this, where 2^y y would be NaN for -inf: a bound no lower than
+// needed, since a gradient's factor times it must stay finite as well.
+constexpr float kLow = -1000.0f;
 constexpr double kLn2 = 0.693147180559945309417;
 
 // A row is cut into vectors of 16 bytes where its addresses are multiples of 16:

@@ -193,6 +193,23 @@ def test_logprobs_bwd(q, T, V, dtype):
             _close(got, ref, _grad_tol(ref, p, logp, l, coef, dtype, hot), "dz")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_large_entropy_gradients_leave_masked_logits_at_0(q, dtype):
+    """A scaled loss at a low temperature: g / t = 2^40 times p log p is far from
+    float32's range, and what is masked has no part of it."""
+    Z, _ = _rows(4, 5000, dtype)
+    Z = Z.clone()
+    Z[:, 1000:] = -INF
+    Z[2, 500:] = torch.finfo(dtype).min
+    y = torch.full((4,), 3, device=Z.device)
+    t = 2.0 ** -10
+    stats = q.qlora_logprobs_fwd(Z, y, t)[4]
+    h = torch.full((4,), 2.0 ** 30, device=Z.device)
+    for g in (None, h):
+        d = _np(q.qlora_logprobs_bwd(Z, y, stats, g, h, t))
+        assert np.isfinite(d).all() and (d[:, 1000:] == 0).all() and (d[2, 500:] == 0).all()
+
+
 def _teacher(Z, g, k, t, rest):
     full = Z.float() + torch.randn(Z.shape, generator=g, device=Z.device)
     full = torch.where(torch.isinf(full), torch.full_like(full, -30.0), full)
