@@ -115,7 +115,7 @@ int check_logits(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz
   if (!Z || T <= 0 || V <= 0 || ldz < V) return QLORA_ERR_INVALID_ARG;
   if (dtype != QLORA_LOGITS_BF16 && dtype != QLORA_LOGITS_F32) return QLORA_ERR_INVALID_ARG;
   if (!(temperature > 0.0f) || std::isinf(temperature)) return QLORA_ERR_INVALID_ARG;
-  if (T > (int64_t)1 << 24 || V > (int64_t)1 << 21 || ldz > (int64_t)1 << 32) return QLORA_ERR_UNSUPPORTED;
+  if (T > (int64_t)1 << 23 || V > (int64_t)1 << 21 || ldz > (int64_t)1 << 32) return QLORA_ERR_UNSUPPORTED;
   if (temperature < 0x1p-40f || temperature > 0x1p40f) return QLORA_ERR_UNSUPPORTED;
   if (!aligned(Z, dtype == QLORA_LOGITS_F32 ? 4 : 2)) return QLORA_ERR_UNSUPPORTED;
   *z = qlora::Logits{Z, dtype == QLORA_LOGITS_F32, T, V, ldz, temperature};
@@ -672,7 +672,7 @@ int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8
 }
 
 size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top) {
-  if (T <= 0 || V <= 0 || T > (int64_t)1 << 24 || V > (int64_t)1 << 21) return 0;
+  if (T <= 0 || V <= 0 || T > (int64_t)1 << 23 || V > (int64_t)1 << 21) return 0;
   if (n_top < 0 || n_top > QLORA_MAX_TOP_LOGITS || n_top > V) return 0;
   return qlora::logits_workspace_bytes(T, V, n_top);
 }

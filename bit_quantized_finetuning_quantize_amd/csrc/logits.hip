@@ -26,6 +26,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kUnit = 8192;          // entries of a step of a workgroup; parts of a row are multiples of it
 constexpr int kMaxUnits = 16;        // ... and at most this many of them
 constexpr int kMaxParts = 32;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 32) / kThreads - 1;
 constexpr int kMaxTop = 64;
 constexpr int kMaxItems = 2048;
 constexpr int kMaxCand = kMaxParts * kMaxTop;
@@ -912,10 +913,11 @@ Parts fwd_parts(int64_t T, int64_t V, int shift) {
   return split_row(units, std::max(S, (units + kMaxUnits - 1) / kMaxUnits));
 }
 // In the backward passes one unit to a workgroup (us with one, two and four:
-// 4096 x 32768 98, 106, 111, 1024 x 98304 76, 81, 87), as long as the grid holds them.
+// 4096 x 32768 98, 106, 111, 1024 x 98304 76, 81, 87), as long as a grid holds
+// them: its threads are counted in 32 bits.
 Parts bwd_parts(int64_t T, int64_t V, int shift) {
-  const int64_t units = units_of(V, shift), per = T * units >> 30 ? 4 : 1;
-  return split_row(units, (units + per - 1) / per);
+  const int64_t units = units_of(V, shift), most = std::max<int64_t>(kMaxGrid / T, 1);
+  return split_row(units, std::min(units, most));
 }
 int largest_shift(const Logits& z) {
   const int64_t bytes = z.f32 ? 4 : 2;

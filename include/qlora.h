@@ -686,7 +686,7 @@ int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8
  * -inf has no distribution: log p = -inf, entropy 0, gradient 0; a distillation
  * loss is +inf if it has targets, else 0. A row with a NaN or +inf has NaN.
  *
- * Sizes: 1 <= T <= 2^24, 1 <= V <= 2^21, 1 <= n_top <= 64 (and <= V), 1 <= k <=
+ * Sizes: 1 <= T <= 2^23, 1 <= V <= 2^21, 1 <= n_top <= 64 (and <= V), 1 <= k <=
  * 256, 2^-40 <= t <= 2^40.
  *
  * Workspace of the two forward passes: at least

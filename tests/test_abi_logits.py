@@ -41,7 +41,7 @@ def test_rows_rejected(lib, f):
     for kw in (dict(Z=None), dict(T=0), dict(T=-1), dict(V=0, n=0) if f is _lp else dict(V=0), dict(ld=99), dict(dt=2),
                dict(dt=-1), dict(t=0.0), dict(t=-1.0), dict(t=INF), dict(t=NAN)):
         assert f(lib, **kw) == INVALID, kw
-    for kw in (dict(Z=ODD), dict(dt=1, Z=ctypes.c_void_p((1 << 20) + 2)), dict(T=(1 << 24) + 1),
+    for kw in (dict(Z=ODD), dict(dt=1, Z=ctypes.c_void_p((1 << 20) + 2)), dict(T=(1 << 23) + 1),
                dict(V=(1 << 21) + 1, ld=1 << 22, **({"ldd": 1 << 22} if "bwd" in f.__name__ else {})),
                dict(ld=(1 << 32) + 1), dict(t=1e-13), dict(t=2e12)):
         assert f(lib, **kw) == UNSUPPORTED, kw
@@ -85,10 +85,10 @@ def test_distill_bwd_rejected(lib):
 
 def test_workspace_query(lib):
     f = lib.qlora_logits_workspace_bytes
-    for T, V, n in ((0, 10, 0), (1, 0, 0), (1, 10, 11), (1, 100, 65), (1, 10, -1), ((1 << 24) + 1, 10, 0),
+    for T, V, n in ((0, 10, 0), (1, 0, 0), (1, 10, 11), (1, 100, 65), (1, 10, -1), ((1 << 23) + 1, 10, 0),
                     (1, (1 << 21) + 1, 0)):
         assert f(T, V, n) == 0, (T, V, n)
-    assert f(1, 1, 1) > 0 and f(1 << 24, 1 << 21, 64) > 0
+    assert f(1, 1, 1) > 0 and f(1 << 23, 1 << 21, 64) > 0
     assert f(1, 131072, 20) > f(1, 131072, 0) > f(1, 8192, 0) > 0
 
 

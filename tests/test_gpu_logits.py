@@ -468,3 +468,20 @@ def test_many_rows_past_32_bit_offsets(q):
     want = q.qlora_logprobs_bwd(Z[T - 1:], y[T - 1:], stats[T - 1:], g[T - 1:])
     q.qlora_logprobs_bwd(Z, y, stats, g, dZ=Z)
     assert torch.equal(Z[T - 1:], want)
+
+
+def test_the_most_rows(q):
+    """2^23 rows, a workgroup to each, of one and of five logits."""
+    T = 1 << 23
+    for V in (1, 5):
+        print(f"[case] {T} x {V}", flush=True)
+        Z, _ = _rows(1 << 13, V, BF)
+        few = q.qlora_logprobs_fwd(Z, n_top=1)
+        Z = Z.repeat(1 << 10, 1)
+        many = q.qlora_logprobs_fwd(Z, n_top=1)
+        for a, b in zip(few[1:], many[1:]):
+            assert torch.equal(a.repeat(1 << 10, *[1] * (a.dim() - 1)), b)
+        h = torch.ones(T, device=Z.device)
+        d = q.qlora_logprobs_bwd(Z, None, many[4], None, h)
+        assert torch.equal(d.view(1 << 10, 1 << 13, V), d[:1 << 13].expand(1 << 10, -1, -1))
+        assert torch.equal(d[:1 << 13], q.qlora_logprobs_bwd(Z[:1 << 13], None, few[4], None, h[:1 << 13]))
