@@ -134,7 +134,8 @@ int check_top_logits(const int64_t* ids, const void* values, int32_t dtype, int3
 int check_dlogits(const void* dZ, int64_t lddz, const qlora::Logits& z) {
   if (!dZ || lddz < z.V) return QLORA_ERR_INVALID_ARG;
   if (lddz > (int64_t)1 << 32 || !aligned(dZ, z.f32 ? 4 : 2)) return QLORA_ERR_UNSUPPORTED;
-  return QLORA_OK;
+  // in place each workgroup writes only what itself has read
+  return dZ == z.Z && z.T > 1 && lddz != z.ldz ? QLORA_ERR_INVALID_ARG : QLORA_OK;
 }
 
 int check_logits_ws(const qlora::Logits& z, int n_top, const void* ws, size_t ws_bytes) {

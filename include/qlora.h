@@ -719,8 +719,8 @@ size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top);
  *            and same row distance). Rows whose gradients are both 0 become 0,
  *            whatever their logits.
  * Errors: INVALID_ARG (null required pointer, no output, n_top without both outputs or
- * above V, sizes not positive, ldz or lddz < V, unknown dtype, t not a positive
- * finite number); UNSUPPORTED (a size, temperature or alignment outside the
+ * above V, sizes not positive, ldz or lddz < V, dZ = Z with another row distance, unknown
+ * dtype, t not a positive finite number); UNSUPPORTED (a size, temperature or alignment outside the
  * above); WORKSPACE. */
 int qlora_logprobs_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
                        const int64_t* target, float temperature, float* logp, float* entropy,

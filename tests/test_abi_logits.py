@@ -83,6 +83,11 @@ def test_distill_bwd_rejected(lib):
         assert _kd_bwd(lib, **kw) == UNSUPPORTED, kw
 
 
+@pytest.mark.parametrize("f", [_lp_bwd, _kd_bwd])
+def test_in_place_needs_the_same_rows(lib, f):
+    assert f(lib, ldd=101) == INVALID and f(lib, ld=101) == INVALID
+
+
 def test_workspace_query(lib):
     f = lib.qlora_logits_workspace_bytes
     for T, V, n in ((0, 10, 0), (1, 0, 0), (1, 10, 11), (1, 100, 65), (1, 10, -1), ((1 << 23) + 1, 10, 0),
