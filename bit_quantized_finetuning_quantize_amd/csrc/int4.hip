@@ -526,17 +526,35 @@ hipError_t run_linear(const Int4Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Workgroups of 16 kNR weight rows and 16 kMT tokens.
+int64_t blocks(const Int4Args& a, int kMT, int kNR) {
+  return ((a.N + 16 * kNR - 1) / (16 * kNR)) * ((a.M + 16 * kMT - 1) / (16 * kMT));
+}
+constexpr int64_t kUnits = 256;  // compute units, each of which holds one
+
 // 16, 32 or 48 weight rows to a workgroup: as few as leave one workgroup to a
-// compute unit, since every workgroup reads all of the tokens (us from a graph,
+// compute unit, since every workgroup reads all of its tokens (us from a graph,
 // with 16, 32 and 48: 48 tokens x 11008 x 4096 25.3, 24.9, 18.8; x 4096 x 4096
 // 10.4, 12.2, 14.5; 16 x 11008 x 4096 11.8, 12.6, 11.1). Four tokens or fewer
 // cost little to read, and 16 rows do better at any size (4 x 11008 x 4096 8.9,
 // 10.1, 9.3).
 template <int kG, int kMT, int kX>
 hipError_t run_rows(const Int4Args& a, hipStream_t stream) {
-  if (a.N <= 16 * 256) return run_linear<kG, kMT, 1, 1, kX>(a, stream);
-  if (a.N <= 32 * 256) return run_linear<kG, kMT, 2, 1, kX>(a, stream);
+  if (blocks(a, kMT, 1) <= kUnits) return run_linear<kG, kMT, 1, 1, kX>(a, stream);
+  if (blocks(a, kMT, 2) <= kUnits) return run_linear<kG, kMT, 2, 1, kX>(a, stream);
   return run_linear<kG, kMT, 3, 1, kX>(a, stream);
+}
+// More tokens than 48: 64 of them with 16 or 32 weight rows (48 do not fit the
+// registers), or 32 with 48, whose workgroups take 4/5 of the time of 64 with 32
+// and are the better choice if they come in few rounds more (us with 64 x 32 and
+// 32 x 48: 64 x 11008 x 4096 26.8, 21.8; 64 x 32768 x 8192 98, 112; 128 x 8192 x
+// 4096 26.5, 33.5).
+template <int kG>
+hipError_t run_many(const Int4Args& a, hipStream_t stream) {
+  const auto rounds = [&](int kMT, int kNR) { return (blocks(a, kMT, kNR) + kUnits - 1) / kUnits; };
+  if (blocks(a, 4, 1) <= kUnits) return run_linear<kG, 4, 1, 1, 16>(a, stream);
+  if (5 * rounds(4, 2) <= 4 * rounds(2, 3)) return run_linear<kG, 4, 2, 1, 16>(a, stream);
+  return run_linear<kG, 2, 3, 1, 8>(a, stream);
 }
 
 template <typename F>
@@ -582,7 +600,7 @@ hipError_t launch_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, con
     if (M <= 16) return run_rows<kG, 1, 4>(a, stream);
     if (M <= 32) return run_rows<kG, 2, 8>(a, stream);
     if (M <= 48) return run_rows<kG, 3, 12>(a, stream);
-    return run_rows<kG, 4, 16>(a, stream);
+    return run_many<kG>(a, stream);
   });
 }
 

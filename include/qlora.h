@@ -660,8 +660,8 @@ int qlora_int4_dequantize(const uint8_t* codes, const uint16_t* scales, const ui
 
 /* qlora_int4_linear_fwd — Y = X W^T for few tokens, in one launch and without a
  * workspace. The products x (q - z) are exact and summed in float32, each
- * group's sum times s in float32. Any M is served, 64 tokens to a pass over the
- * weight. A token with an infinity or NaN has NaN in all of its row of Y, and one
+ * group's sum times s in float32. Any M is served, up to 64 tokens to a pass over
+ * the weight. A token with an infinity or NaN has NaN in all of its row of Y, and one
  * above 2^110 may (its products are formed with 16 + q and 16 + z apart).
  *   X        device bf16 [M x K], rows ldx >= K elements apart, ldx a multiple of 8
  *            and the base 16-byte aligned

@@ -99,7 +99,9 @@ LINEAR = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 100, 128), (5, 1001, 1504), 
           (1, 4096, 4096), (33, 130, 1056), (48, 300, 2048), (64, 65, 8224), (65, 40, 256), (130, 70, 416),
           (1, 24, 11008), (300, 17, 64),
           # 32 and 48 rows to a workgroup
-          (9, 4100, 96), (20, 8191, 160), (33, 8300, 128), (50, 8200, 96), (70, 5000, 64), (4, 9000, 224)]
+          (9, 4100, 96), (20, 8191, 160), (33, 8300, 128), (50, 8200, 96), (70, 5000, 64), (4, 9000, 224),
+          # 64 tokens and 32 rows
+          (49, 8000, 96), (130, 4100, 160)]
 
 
 @pytest.mark.parametrize("sym", [False, True])
