@@ -328,7 +328,8 @@ __device__ __forceinline__ int select_top(const char* part, int lo, int n, int f
                                           const uint32_t* bins, uint64_t best, int need, TopLds& t) {
   constexpr int kE = Elem<kF32>::kE, kVecs = Elem<kF32>::kVecs;
   const int tid = threadIdx.x, wave = tid >> 6;
-  const int full = min(kWaves, n / kE / 64);  // waves whose lanes all hold an entry
+  // waves whose lanes all hold an entry; a part that fills none has as many lanes as vectors
+  const int full = n / kE >= 64 ? min(kWaves, n / kE / 64) : (n + kE - 1) / kE >= need;
   if (full) {
     uint32_t key = (uint32_t)(best >> 32), step = best ? (idx_of(best) - (uint32_t)first) / kUnit : 0;
     wave_rth<kF32>(key, step, (need + full - 1) / full);
@@ -839,7 +840,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(RowsBwd a) {
 // read before, after that.
 template <bool kF32, bool kPast>
 __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(RowsBwd a) {
-  __shared__ int s_id[kThreads];
+  __shared__ __attribute__((aligned(16))) int s_id[kThreads];
   __shared__ float s_q[kThreads];
   const int tid = threadIdx.x;
   const Part in = part_of<kF32>(a.Z, a.ldz, a.S, a.part, a.V);
@@ -872,7 +873,16 @@ __global__ void __launch_bounds__(kThreads) distill_bwd_kernel(RowsBwd a) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   bool mine = id >= 0;
-  if (mine) {  // an id twice: its first entry takes the sum
+  int times = 0;
+  if (mine) {
+#pragma unroll 4
+    for (int i = 0; i < a.k; i += 4) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(s_id + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) times += (int)v[e] == id;
+    }
+  }
+  if (times > 1) {  // its first entry takes the sum
     q = 0.0f;
     for (int i = 0; i < a.k; ++i) {
       const bool same = s_id[i] == id;
