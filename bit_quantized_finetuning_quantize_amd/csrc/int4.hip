@@ -51,6 +51,8 @@ __device__ __forceinline__ void split_index(uint32_t first, uint32_t i, uint32_t
 //               z = rint(-lo / s) in [0, 15]
 //   symmetric   s = bf16(max|w| / 7), z = 8
 //   q = rint(w / s) + z in [0, 15]; where s = 0, z = 0 (symmetric 8) and q = z.
+// Bounded by memory: 4096 x 11008 in groups of 128 24 us, 4.8 TB/s, a copy's rate
+// (with 8 values to a lane, a division to each value and shifts 43).
 template <int kG, bool kSym>
 __global__ void __launch_bounds__(kThreads)
 int4_quantize_kernel(const uint16_t* __restrict__ W, int64_t ldw, int K, uint32_t ng, uint32_t groups,
@@ -137,7 +139,8 @@ int4_quantize_kernel(const uint16_t* __restrict__ W, int64_t ldw, int K, uint32_
   }
 }
 
-// bf16(s (q - z)): the product of 8 and 5 bits is exact before that.
+// bf16(s (q - z)): the product of 8 and 5 bits is exact before that. Bounded by
+// memory: 4096 x 11008 19 us, 6.0 TB/s.
 template <int kG>
 __global__ void __launch_bounds__(kThreads)
 int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
@@ -180,6 +183,14 @@ int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __rest
 // is scaled in float32.
 //
 // Rows and tokens past the end repeat the last one; their sums are not stored.
+//
+// What bounds it (us from a graph, where a launch takes 4). Few tokens: the loads;
+// 32768 x 8192, one token, 31 us, 4.6 TB/s, without its sums 28; 4096 x 4096 5.4. More
+// tokens: the few steps of each wave, one after the other; 48 x 11008 x 4096 in
+// groups of 32 18.6, of which the matrix units work 3.5 and the vector
+// instructions 6; in groups of 128 16.2, without the sums 12.3, without the tokens' and
+// scales' loads 12.5, without either 8.9. Two steps' loads in flight: 1 x 32768 x
+// 8192 29.8 for 30.1, but 2 x 8192 x 8192 14.6 for 12.3.
 
 constexpr int kWaves = 8;
 
