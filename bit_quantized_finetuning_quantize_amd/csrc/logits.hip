@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   constexpr int kE = Elem<kF32>::kE, kVecs = Elem<kF32>::kVecs;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   __shared__ Soft s_soft[kWaves];
-  __shared__ int s_last, s_twice;
+  __shared__ int s_last, s_twice, s_list[kOp == kLogprobs ? 1 : 3 * kThreads];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Part in = part_of<kF32>(a.Z, a.ldz, a.S, a.part, a.V);
   const int64_t row = in.row;
@@ -444,17 +444,27 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   uint32_t* bins = reinterpret_cast<uint32_t*>(dyn + sizeof(TopLds));
   uint64_t* s_lists = reinterpret_cast<uint64_t*>(bins);  // after the part's own selection: [S][n_top]
   uint32_t* mask = reinterpret_cast<uint32_t*>(dyn);  // bit i: position first + i is on the list
+  // the list, an entry to a thread (k <= kThreads)
+  const int64_t entry = row * a.k + tid;
+  int id = -1;
+  float ti = -kInf, zi = -kInf;
+  if (kOp != kLogprobs && tid < a.k) {
+    const int64_t j = a.ids[entry];
+    if (j >= 0 && j < a.V) id = (int)j;
+  }
   if constexpr (kOp == kDistillRest) {
     if (tid == 0) s_twice = 0;
     const int words = (n + 127) / 128 * 4;
     for (int i = tid * 4; i < words; i += kThreads * 4) *reinterpret_cast<u32x4*>(mask + i) = u32x4{0, 0, 0, 0};
     __syncthreads();
-    if (tid < a.k) {  // k <= kThreads
-      const int64_t at = a.ids[row * a.k + tid] + shift - first;
-      const uint32_t bit = 1u << (at & 31);
-      if (at >= lo && at < n && (atomicOr(mask + (at >> 5), bit) & bit)) s_twice = 1;
-    }
+    const int at = id + shift - first;
+    const uint32_t bit = 1u << (at & 31);
+    if (id >= 0 && at >= lo && at < n && (atomicOr(mask + (at >> 5), bit) & bit)) s_twice = 1;
     __syncthreads();
+  }
+  if (kOp != kLogprobs && id >= 0) {  // in flight with the row's loads: a barrier would wait for them
+    ti = a.values_f32 ? load_elem<true>(a.values, entry) : load_elem<false>(a.values, entry);
+    zi = load_elem<kF32>(zrow, id);
   }
 
   Soft acc = kNone;  // without the listed entries where the list's rest is a class
@@ -523,6 +533,11 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   // is to come
   acc = wave_join(acc, c2);
   if (lane == 0) s_soft[wave] = acc;
+  if constexpr (kOp != kLogprobs) {
+    s_list[tid] = id;
+    s_list[kThreads + tid] = __builtin_bit_cast(int, ti);
+    s_list[2 * kThreads + tid] = __builtin_bit_cast(int, zi);
+  }
   __syncthreads();
   if (!kTop && wave) return;
   acc = s_soft[0];
@@ -640,21 +655,15 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   if constexpr (kOp != kLogprobs) {
     // up to four list entries a lane, in 64 bits
     constexpr int kPer = 4;
-    const int64_t at = row * a.k;
-    int64_t id[kPer];
     bool ok[kPer];
     float t[kPer], z[kPer];
     float tm = -kInf, zm = -kInf;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = i * 64 + lane;
-      id[i] = e < a.k ? a.ids[at + e] : -1;
-      ok[i] = id[i] >= 0 && id[i] < a.V;
-      t[i] = z[i] = -kInf;
-      if (ok[i]) {
-        t[i] = a.values_f32 ? load_elem<true>(a.values, at + e) : load_elem<false>(a.values, at + e);
-        z[i] = load_elem<kF32>(zrow, id[i]);
-      }
+      ok[i] = s_list[e] >= 0;
+      t[i] = __builtin_bit_cast(float, s_list[kThreads + e]);
+      z[i] = __builtin_bit_cast(float, s_list[2 * kThreads + e]);
       tm = fmaxf(tm, t[i]);
       zm = fmaxf(zm, z[i]);
     }
@@ -669,7 +678,7 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       for (int i = 0; i < kPer; ++i) {
         bool once = ok[i];
         if (twice)  // uniform
-          for (int e = 0; e < i * 64 + lane && once; ++e) once = a.ids[at + e] != id[i];
+          for (int e = 0; e < i * 64 + lane && once; ++e) once = s_list[e] != s_list[i * 64 + lane];
         if (once) on += exp2_((z[i] - base) * c2);
       }
       on = wave_sum(on);
