@@ -548,10 +548,16 @@ constexpr int64_t kUnits = 256;  // compute units, each of which holds one
 // with 16, 32 and 48: 48 tokens x 11008 x 4096 25.3, 24.9, 18.8; x 4096 x 4096
 // 10.4, 12.2, 14.5; 16 x 11008 x 4096 11.8, 12.6, 11.1). Four tokens or fewer
 // cost little to read, and 16 rows do better at any size (4 x 11008 x 4096 8.9,
-// 10.1, 9.3).
+// 10.1, 9.3). Up to 16 tokens with 16 weight rows, each step takes two runs of 128
+// columns if every wave has two such steps (one run and two: 8 x 4096 x 4096 6.1,
+// 5.2; 12 x 4096 x 11008 12.6, 10.8; 5 x 1001 x 1504 3.5, 3.8).
 template <int kG, int kMT, int kX>
 hipError_t run_rows(const Int4Args& a, hipStream_t stream) {
-  if (blocks(a, kMT, 1) <= kUnits) return run_linear<kG, kMT, 1, 1, kX>(a, stream);
+  if (blocks(a, kMT, 1) <= kUnits) {
+    if constexpr (kMT == 1)
+      if (a.K >= 2 * kWaves * 256) return run_linear<kG, kMT, 1, 2, 2 * kX>(a, stream);
+    return run_linear<kG, kMT, 1, 1, kX>(a, stream);
+  }
   if (blocks(a, kMT, 2) <= kUnits) return run_linear<kG, kMT, 2, 1, kX>(a, stream);
   return run_linear<kG, kMT, 3, 1, kX>(a, stream);
 }
@@ -608,6 +614,7 @@ hipError_t launch_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, con
     constexpr int kG = decltype(g)::value;
     if (M <= 2) return run_linear<kG, 1, 1, 2, 1>(a, stream);
     if (M <= 4) return run_linear<kG, 1, 1, 2, 2>(a, stream);
+    if (M <= 8) return run_rows<kG, 1, 2>(a, stream);
     if (M <= 16) return run_rows<kG, 1, 4>(a, stream);
     if (M <= 32) return run_rows<kG, 2, 8>(a, stream);
     if (M <= 48) return run_rows<kG, 3, 12>(a, stream);

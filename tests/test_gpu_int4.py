@@ -100,6 +100,8 @@ LINEAR = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 100, 128), (5, 1001, 1504), 
           (1, 24, 11008), (300, 17, 64),
           # 32 and 48 rows to a workgroup
           (9, 4100, 96), (20, 8191, 160), (33, 8300, 128), (50, 8200, 96), (70, 5000, 64), (4, 9000, 224),
+          # two runs to a step, the rows' end in the first or the second
+          (5, 40, 4096), (8, 100, 4320), (9, 30, 4224), (16, 70, 8352),
           # 64 tokens and 32 rows
           (49, 8000, 96), (130, 4100, 160)]
 
