@@ -217,3 +217,17 @@ def test_largest_weight(q):
     part = q.Int4Weight(w.codes[rows], w.scales[rows], w.zeros[rows], (len(rows), K), 128)
     want = host_f32(x).astype(np.float64) @ _dense(part).T
     assert np.array_equal(host_f32(y[:, rows]), want)
+
+
+def test_largest_quantization(q):
+    """Nearly 2^32 values: groups at both ends as they come by themselves."""
+    K = 16384
+    N = (1 << 32) // K - 1
+    w = torch.empty(N, K, dtype=BF, device=device())
+    w.normal_(0, 0.02)
+    st = q.qlora_int4_quantize(w, 32)
+    d = q.qlora_int4_dequantize(st)
+    for rows in (slice(0, 2), slice(N // 2, N // 2 + 2), slice(N - 2, N)):
+        few = q.qlora_int4_quantize(w[rows], 32)
+        assert torch.equal(few.codes, st.codes[rows]) and torch.equal(few.scales, st.scales[rows])
+        assert torch.equal(few.zeros, st.zeros[rows]) and torch.equal(q.qlora_int4_dequantize(few), d[rows])

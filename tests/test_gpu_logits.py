@@ -485,3 +485,63 @@ def test_the_most_rows(q):
         d = q.qlora_logprobs_bwd(Z, None, many[4], None, h)
         assert torch.equal(d.view(1 << 10, 1 << 13, V), d[:1 << 13].expand(1 << 10, -1, -1))
         assert torch.equal(d[:1 << 13], q.qlora_logprobs_bwd(Z[:1 << 13], None, few[4], None, h[:1 << 13]))
+
+
+def test_distillation_past_32_bit_offsets(q):
+    """Rows beyond 4 GiB of logits and their gradients, checked by themselves."""
+    T, V, k = 40000, 60000, 30
+    Z = torch.empty(T, V, dtype=BF, device=device())
+    Z.normal_(0, 2)
+    ids = torch.randint(0, V, (T, k), device=Z.device)
+    values = torch.randn(T, k, device=Z.device)
+    lse = torch.full((T,), 12.0, device=Z.device)
+    g = torch.ones(T, device=Z.device)
+    loss, stats = q.qlora_distill_fwd(Z, ids, values, lse)
+    for r in (0, T // 2, T - 1):
+        one = slice(r, r + 1)
+        a, b = q.qlora_distill_fwd(Z[one], ids[one], values[one], lse[one])
+        # one row is split into parts: both within 2^-24 (600 + 6 k) of the exact loss, as above
+        assert torch.allclose(loss[one], a, rtol=1e-4, atol=1e-4) and torch.allclose(stats[one], b, rtol=1e-4, atol=1e-4)
+    last = slice(T - 1, T)
+    want = q.qlora_distill_bwd(Z[last], ids[last], values[last], stats[last], g[last])
+    q.qlora_distill_bwd(Z, ids, values, stats, g, dZ=Z)
+    assert torch.equal(Z[last], want)
+
+
+def test_calls_of_several_threads(q):
+    """Host threads on streams of their own, each call with its own workspace."""
+    import threading
+    Z, rng = _rows(3, 70000, BF)
+    ids, values, lse = _teacher(Z, rng, 16, 1.0, True)
+    y = torch.tensor([5, 6, 7], device=Z.device)
+    w = q.qlora_int4_quantize((torch.randn(9000, 512, generator=rng, device=Z.device) * 0.02).to(BF))
+    x = torch.randn(60, 512, generator=rng, device=Z.device).to(BF)
+
+    def calls():
+        a = q.qlora_logprobs_fwd(Z, y, n_top=9)
+        b = q.qlora_distill_fwd(Z, ids, values, lse)
+        # all sizes of a workgroup's LDS
+        c = [q.qlora_int4_linear_fwd(x[:m], w) for m in (1, 7, 16, 20, 48, 60)]
+        return [*a, *b, *c]
+
+    want = calls()
+    torch.cuda.synchronize()
+    bad = []
+
+    def run():
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(10):
+                    got = calls()
+                    s.synchronize()
+                    assert all(torch.equal(u, v) for u, v in zip(got, want))
+        except BaseException as e:  # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=run) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
