@@ -718,10 +718,10 @@ size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top);
  *   dZ       device, the type of Z, rows lddz >= V elements apart; may be Z (same base
  *            and same row distance). Rows whose gradients are both 0 become 0,
  *            whatever their logits.
- * Errors: INVALID_ARG (null required pointer, no output, n_top without both outputs or
- * above V, sizes not positive, ldz or lddz < V, dZ = Z with another row distance, unknown
- * dtype, t not a positive finite number); UNSUPPORTED (a size, temperature or alignment outside the
- * above); WORKSPACE. */
+ * Errors: INVALID_ARG (null required pointer, no output, n_top without both
+ * outputs or above V, sizes not positive, ldz or lddz < V, dZ = Z with another
+ * row distance, unknown dtype, t not a positive finite number); UNSUPPORTED (a
+ * size, temperature or alignment outside the above); WORKSPACE. */
 int qlora_logprobs_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
                        const int64_t* target, float temperature, float* logp, float* entropy,
                        int32_t n_top, int64_t* top_ids, float* top_logp, float* stats, void* ws,
@@ -747,9 +747,10 @@ int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64
  *            t^2: that is the caller's g.
  *   stats    device float [T x 6], (m, l, w, w - q_r / p_r, tm, tl) with w = sum q +
  *            q_r, which the backward pass takes; or NULL
- * Where the student has no mass off the list (p_r = 0) the rest's term is left out and
- * w = sum q. q_r / p_r is kept in float32's range: where the student's mass off the list
- * is below 1e-38, the gradient there is smaller than the formula's. A row without entries has loss 0 without teacher_lse.
+ * Where the student has no mass off the list (p_r = 0) the rest's term is left
+ * out and w = sum q. q_r / p_r is kept in float32's range: where the student's
+ * mass off the list is below 1e-38, the gradient there is smaller than the
+ * formula's. A row without entries has loss 0 without teacher_lse.
  * qlora_distill_bwd — dz_j = g / t (w p_j - q_j) for j on the list, and g / t
  * (w - q_r / p_r) p_j off it.
  *   g        device float [T], the gradient of loss; a row with g = 0 becomes 0
