@@ -350,9 +350,10 @@ __device__ __forceinline__ int select_top(const char* part, int lo, int n, int f
     }
   }
   __syncthreads();
-  // Pass -1 collects the entries at or above t0 of the bins listed. Where those are
-  // too many (equal entries), or, with NaN, too few, each further pass takes
-  // the next entry in order, of the bins listed or of all.
+  // Pass -1 collects the numbers at or above t0 of the bins listed. Where those are
+  // too many (equal entries), each further pass takes the next entry in order of
+  // the bins listed; where the part has fewer numbers than `need`, of all its
+  // bins, since the NaNs that come next lie in bins not listed too.
   bool all = t.n_items > kMaxItems;
   uint64_t prev = ~0ull;
 #pragma unroll 1
@@ -378,7 +379,7 @@ __device__ __forceinline__ int select_top(const char* part, int lo, int n, int f
         const uint64_t p = pair_of(key, (uint32_t)(first + at));
         if (pass >= 0) {
           if (p < prev && p > top) top = p;
-        } else if (coarse(key, b) >= t0) {
+        } else if (key && coarse(key, b) >= t0) {
           const int c = atomicAdd(&t.n_cand, 1);
           if (c < kMaxCand) t.cand[c] = p;
         }
