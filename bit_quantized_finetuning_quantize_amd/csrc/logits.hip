@@ -417,7 +417,8 @@ __device__ __forceinline__ int select_top(const char* part, int lo, int n, int f
 // flag holding the dispatch's tag, and looks at all the row's flags: stores and
 // looks are performed in one memory, so the workgroup whose flag comes last
 // sees them all, and goes on with the row (if two see them all, both write the
-// same values). None waits for another, and the flags need no clearing.
+// same values). None waits for another. Whoever goes on sets the row's flags to
+// 0; before a call they may hold anything.
 // kTop: with the largest entries. kPast: loads past the caches.
 template <bool kF32, int kOp, bool kTop, bool kPast>
 __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
@@ -617,6 +618,10 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       last = s_last;
     }
     if (!last) return;
+    // whoever looks later sees no full set and leaves, and no later call finds one
+    // that it could take for its own
+    if (wave == 0 && lane < a.S)
+      __hip_atomic_store(a.flags + row * a.S + lane, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     acc = kNone;
     float third = 0.0f;
     if (lane < a.S) {
