@@ -555,9 +555,12 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
     const bool empty = acc.m == -kInf && acc.s == 0.0f;
     float l = 0.0f;
     if (kOp == kLogprobs && whole) {
-      l = empty ? 0.0f : logf(acc.s);
+      // s holds the largest logit's 1, whatever it was rounded to
+      const float s = acc.s < 1.0f ? 1.0f : acc.s;
+      l = empty ? 0.0f : logf(s);
       if (tid == 0) {
-        const float H = empty ? 0.0f : l - (float)kLn2 * (acc.u / acc.s);
+        float H = empty ? 0.0f : l - (float)kLn2 * (acc.u / s);
+        H = H < 0.0f ? 0.0f : H;
         if (a.entropy) a.entropy[row] = H;
         if (a.stats) {
           a.stats[row * 3] = acc.m;
@@ -720,6 +723,7 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       } else {
         l = log((double)acc.s);
       }
+      if (l < 0.0) l = 0.0;  // by rounding of the sums alone
     }
     double q_sum = 0.0, loss = 0.0;
 #pragma unroll

@@ -679,7 +679,8 @@ int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8
  * apart. For a row z and a temperature t
  *   m = max z,   x = (z - m) / t,   l = log sum exp x,   log p_j = x_j - l.
  * Sums are float32 (a row's few numbers in a distillation float64); every logit is
- * read once. Rows and pointers need their elements' alignment only.
+ * read once. No log p is above 0 and no entropy below it, whatever the sums round
+ * to. Rows and pointers need their elements' alignment only.
  *
  * Masked and other special rows. A logit of -inf, or so low that exp underflows,
  * has p = 0 and adds nothing to an entropy or a gradient. A row whose logits are all
