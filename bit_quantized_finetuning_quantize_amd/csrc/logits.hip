@@ -319,6 +319,11 @@ struct TopLds {
 // of them in each of w full waves, r = need / w rounded up, has r entries at or
 // above it in that wave, so the smallest of the waves' has `need`: only the
 // bins that reach it are read again (from the L2).
+// Equal entries at t0 beyond what t.cand holds take a pass to each entry, and so
+// do parts with fewer numbers than `need`. Masked logits are such entries where a
+// part has fewer others than the bound asks for: one row of 131072 with 200 of its
+// tokens allowed, 1, 5, 20 and 64 entries, 25, 54, 165 and 486 us from a graph,
+// against 9.6, 10.2, 11.8 and 15.7 with 20000 allowed.
 // The code is kept short: a few rows run all of it once, and fetching it costs
 // as much as running it (one row of 131072 with 20 entries 12.4 us from a graph,
 // 14.1 with the steps below unrolled and entries taken from registers; 6.0
@@ -405,9 +410,10 @@ __device__ __forceinline__ int select_top(const char* part, int lo, int n, int f
   return need;
 }
 
-// One (row, part) per workgroup. Rows of 1024 or more are not split; fewer are, into
-// about 1024 workgroups (with 2048 and 4096: 600 x 50000 with 20 entries 26.5 us
-// -> 29.5 and 36, 1030 x 32000 17.5 -> 17.9 and 18.9, 449 x 30637 13.3 -> 11.8).
+// One (row, part) per workgroup. Rows that do not fit 16 steps (131072 positions)
+// are split, and where there are fewer than 1024 rows also shorter ones, into about
+// 1024 workgroups (with 2048 and 4096: 600 x 50000 with 20 entries 26.5 us -> 29.5
+// and 36, 1030 x 32000 17.5 -> 17.9 and 18.9, 449 x 30637 13.3 -> 11.8).
 // Large calls are bounded by memory: 4096 x 32768 in bf16 48 us in a graph, 5.6
 // TB/s, where reads alone reach 6.2; the operations, nine a logit, take 29 us
 // of that. A row of 131072 takes 6.0 us, where a launch takes 4, and 9.4, 11.9

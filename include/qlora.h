@@ -693,9 +693,9 @@ int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8
  * Workspace of the two forward passes: at least
  *   qlora_logits_workspace_bytes(T, V, n_top)
  * bytes of device memory, 256-byte aligned (n_top = 0 without alternatives and for a
- * distillation; 0 for a shape the calls reject). Few rows are split over
- * workgroups and joined in the same launch by way of it. Its contents on entry do
- * not matter. */
+ * distillation; 0 for a shape the calls reject). Fewer than 1024 rows, and rows of
+ * more than 131072 logits, are split over workgroups and joined in the same launch
+ * by way of it. Its contents on entry do not matter. */
 #define QLORA_LOGITS_BF16 0
 #define QLORA_LOGITS_F32 1
 #define QLORA_MAX_TOP_LOGITS 64
@@ -751,7 +751,9 @@ int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64
  * Where the student has no mass off the list (p_r = 0) the rest's term is left
  * out and w = sum q. q_r / p_r is kept in float32's range: where the student's
  * mass off the list is below 1e-38, the gradient there is smaller than the
- * formula's. A row without entries has loss 0 without teacher_lse.
+ * formula's. A row without entries has loss 0 without teacher_lse. The student's
+ * float32 sums leave an error of a few 1e-7 in a loss, so that one near 0 may come
+ * out below it.
  * qlora_distill_bwd — dz_j = g / t (w p_j - q_j) for j on the list, and g / t
  * (w - q_r / p_r) p_j off it.
  *   g        device float [T], the gradient of loss; a row with g = 0 becomes 0
