@@ -15,6 +15,7 @@ _c_i64 = ctypes.c_int64
 _c_i32 = ctypes.c_int32
 _c_int = ctypes.c_int
 _c_f32 = ctypes.c_float
+_c_f64 = ctypes.c_double
 _c_size = ctypes.c_size_t
 _vp = ctypes.c_void_p
 
@@ -88,14 +89,14 @@ SIGNATURES = {
     "qlora_int4_linear_fwd": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp, _c_i64, _c_i64, _c_i32, _vp,
                                        _c_i32, _c_i64, _vp]),
     "qlora_logits_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i32]),
-    "qlora_logprobs_fwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _c_f32, _vp, _vp, _c_i32,
+    "qlora_logprobs_fwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _c_f64, _vp, _vp, _c_i32,
                                     _vp, _vp, _vp, _vp, _c_size, _vp]),
-    "qlora_logprobs_bwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _c_f32, _vp, _vp, _vp,
+    "qlora_logprobs_bwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _c_f64, _vp, _vp, _vp,
                                     _vp, _c_i64, _vp]),
     "qlora_distill_fwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i32, _c_i32, _vp,
-                                   _c_f32, _vp, _vp, _vp, _c_size, _vp]),
+                                   _c_f64, _vp, _vp, _vp, _c_size, _vp]),
     "qlora_distill_bwd": (_c_int, [_vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i32, _c_i32,
-                                   _c_f32, _vp, _vp, _vp, _c_i64, _vp]),
+                                   _c_f64, _vp, _vp, _vp, _c_i64, _vp]),
     "qlora_gemv_wait_limit": (_c_int, [_c_i64]),
     "qlora_status_string": (ctypes.c_char_p, [_c_int]),
     "qlora_last_hip_error": (_c_int, []),

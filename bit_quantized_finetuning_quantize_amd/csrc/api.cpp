@@ -110,13 +110,13 @@ int check_int4(const void* codes, const void* scales, int64_t N, int64_t K, int3
 }
 
 // Rows of logits.
-int check_logits(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz, float temperature,
+int check_logits(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz, double temperature,
                  qlora::Logits* z) {
   if (!Z || T <= 0 || V <= 0 || ldz < V) return QLORA_ERR_INVALID_ARG;
   if (dtype != QLORA_LOGITS_BF16 && dtype != QLORA_LOGITS_F32) return QLORA_ERR_INVALID_ARG;
-  if (!(temperature > 0.0f) || std::isinf(temperature)) return QLORA_ERR_INVALID_ARG;
+  if (!(temperature > 0.0) || std::isinf(temperature)) return QLORA_ERR_INVALID_ARG;
   if (T > (int64_t)1 << 23 || V > (int64_t)1 << 21 || ldz > (int64_t)1 << 32) return QLORA_ERR_UNSUPPORTED;
-  if (temperature < 0x1p-40f || temperature > 0x1p40f) return QLORA_ERR_UNSUPPORTED;
+  if (temperature < 0x1p-40 || temperature > 0x1p40) return QLORA_ERR_UNSUPPORTED;
   if (!aligned(Z, dtype == QLORA_LOGITS_F32 ? 4 : 2)) return QLORA_ERR_UNSUPPORTED;
   *z = qlora::Logits{Z, dtype == QLORA_LOGITS_F32, T, V, ldz, temperature};
   return QLORA_OK;
@@ -679,7 +679,7 @@ size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top) {
 }
 
 int qlora_logprobs_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
-                       const int64_t* target, float temperature, float* logp, float* entropy,
+                       const int64_t* target, double temperature, float* logp, float* entropy,
                        int32_t n_top, int64_t* top_ids, float* top_logp, float* stats, void* ws,
                        size_t ws_bytes, void* stream) {
   qlora::Logits z;
@@ -699,7 +699,7 @@ int qlora_logprobs_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64
 }
 
 int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
-                       const int64_t* target, float temperature, const float* stats,
+                       const int64_t* target, double temperature, const float* stats,
                        const float* g_logp, const float* g_entropy, void* dZ, int64_t lddz,
                        void* stream) {
   qlora::Logits z;
@@ -715,7 +715,7 @@ int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64
 
 int qlora_distill_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
                       const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
-                      const float* teacher_lse, float temperature, float* loss, float* stats,
+                      const float* teacher_lse, double temperature, float* loss, float* stats,
                       void* ws, size_t ws_bytes, void* stream) {
   qlora::Logits z;
   qlora::TopLogits t;
@@ -732,7 +732,7 @@ int qlora_distill_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_
 
 int qlora_distill_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
                       const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
-                      float temperature, const float* stats, const float* g, void* dZ,
+                      double temperature, const float* stats, const float* g, void* dZ,
                       int64_t lddz, void* stream) {
   qlora::Logits z;
   qlora::TopLogits t;

@@ -238,7 +238,7 @@ struct Logits {
   const void* Z;
   bool f32;
   int64_t T, V, ldz;
-  float temperature;
+  double temperature;
 };
 // A teacher's k largest logits of each row and their ids, [T x k].
 struct TopLogits {

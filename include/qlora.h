@@ -678,6 +678,8 @@ int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8
  * uint16_t bit patterns) or float32 (QLORA_LOGITS_F32), rows ldz >= V elements
  * apart. For a row z and a temperature t
  *   m = max z,   x = (z - m) / t,   l = log sum exp x,   log p_j = x_j - l.
+ * The temperature is a double: rounded to float32 it would be off by up to 2^-24,
+ * which a teacher's log sum exp at 0.7 and its logits, divided by that, do not share.
  * Sums are float32 (a row's few numbers in a distillation float64); every logit is
  * read once. No log p is above 0 and no entropy below it, whatever the sums round
  * to. Rows and pointers need their elements' alignment only.
@@ -724,11 +726,11 @@ size_t qlora_logits_workspace_bytes(int64_t T, int64_t V, int32_t n_top);
  * row distance, unknown dtype, t not a positive finite number); UNSUPPORTED (a
  * size, temperature or alignment outside the above); WORKSPACE. */
 int qlora_logprobs_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
-                       const int64_t* target, float temperature, float* logp, float* entropy,
+                       const int64_t* target, double temperature, float* logp, float* entropy,
                        int32_t n_top, int64_t* top_ids, float* top_logp, float* stats, void* ws,
                        size_t ws_bytes, void* stream);
 int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
-                       const int64_t* target, float temperature, const float* stats,
+                       const int64_t* target, double temperature, const float* stats,
                        const float* g_logp, const float* g_entropy, void* dZ, int64_t lddz,
                        void* stream);
 
@@ -761,11 +763,11 @@ int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64
  * Errors: as qlora_logprobs_fwd and _bwd. */
 int qlora_distill_fwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
                       const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
-                      const float* teacher_lse, float temperature, float* loss, float* stats,
+                      const float* teacher_lse, double temperature, float* loss, float* stats,
                       void* ws, size_t ws_bytes, void* stream);
 int qlora_distill_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64_t ldz,
                       const int64_t* ids, const void* values, int32_t values_dtype, int32_t k,
-                      float temperature, const float* stats, const float* g, void* dZ,
+                      double temperature, const float* stats, const float* g, void* dZ,
                       int64_t lddz, void* stream);
 
 /* qlora_gemv_wait_limit — how long, in microseconds, the row-tile
