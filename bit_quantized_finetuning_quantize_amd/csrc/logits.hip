@@ -199,6 +199,11 @@ __device__ __forceinline__ T wave_reduce(T v, T none, F f) {
     return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
   }
 }
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)w, lane), hi = __builtin_amdgcn_readlane((int)(w >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
 __device__ __forceinline__ float wave_max(float v) {
   return wave_reduce(v, -kInf, [](float a, float b) { return fmaxf(a, b); });
 }
@@ -211,6 +216,21 @@ __device__ __forceinline__ Soft wave_join(const Soft& a, float c2) {
   r.s = wave_sum(r.s);
   r.u = wave_sum(r.u);
   return r;
+}
+
+// The mass of a part of a distillation's row, sum s 2^((z - m) c), s in 64 bits: the
+// loss is a difference of values near each other.
+struct Mass {
+  float m;
+  double s;
+};
+constexpr Mass kNoMass{-kInf, 0.0};
+// The lanes' masses as one, in every lane.
+__device__ __forceinline__ Mass wave_join(const Mass& a, double c) {
+  const float m = wave_max(a.m);
+  // 2^d by the hardware's exp2 of d's fraction, 1 where d is 0
+  const double d = fmax(((double)a.m - base_of(m)) * c, -1100.0), n = rint(d);
+  return Mass{m, wave_sum(a.s * ldexp((double)exp2_((float)(d - n)), (int)n))};
 }
 
 // ---------------------------------------------------------------------------
@@ -267,9 +287,114 @@ __device__ __forceinline__ void wave_rth(uint32_t& key, uint32_t& step, int r) {
 }
 
 // ---------------------------------------------------------------------------
+// 1 / d, exp x and log of a positive s in 64 bits, to 3e-13 of the value: two of Newton's
+// steps from the hardware's inverse; Taylor's series of x less its nearest multiple of
+// ln 2 (at most 0.35) up to the tenth power; 2 artanh((m - 1) / (m + 1)), s = 2^e m, m
+// in [sqrt(1/2), sqrt 2), up to the 15th. A dozen or two operations one after the
+// other, for a row's end waits for them (the library's took 1.3 us more of 4096 x
+// 1000 with 32 entries, 0.3 of 7 x 50001).
+__device__ __forceinline__ double inverse(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+__device__ __forceinline__ double exp_(double x) {
+  x = x < -800.0 ? -800.0 : x;  // 0 (keeps a NaN)
+  const double n = rint(x * 1.44269504088896340736);
+  constexpr double kHi = 2977044471.0 / 4294967296.0, kLo = 1.9082149292705877e-10;  // ln 2 to 32 bits, and the rest
+  const double r = __builtin_fma(n, -kLo, __builtin_fma(n, -kHi, x));
+  double p = 1.0 / 3628800;
+  constexpr double kInverse[10] = {1.0,       1.0,       1.0 / 2,    1.0 / 6,     1.0 / 24,
+                                   1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880};  // of i!
+#pragma unroll
+  for (int i = 9; i >= 0; --i) p = __builtin_fma(p, r, kInverse[i]);
+  return ldexp(p, (int)n);
+}
+__device__ __forceinline__ double log_(double s) {
+  double m = __builtin_amdgcn_frexp_mant(s);
+  int e = __builtin_amdgcn_frexp_exp(s);
+  const bool low = m < 0.70710678118654752440;
+  m = low ? 2.0 * m : m;
+  e -= low;
+  const double f = (m - 1.0) * inverse(m + 1.0), g = f * f;
+  double p = 2.0 / 15;
+#pragma unroll
+  for (int i = 13; i >= 3; i -= 2) p = __builtin_fma(p, g, 2.0 / i);
+  return __builtin_fma((double)e, kLn2, __builtin_fma(p * g, f, 2.0 * f));
+}
+
+// A teacher's list in LDS: ids (-1: no entry), the teacher's and the student's logits,
+// kThreads each.
+constexpr int kPer = kThreads / 64;  // entries to a lane
+__device__ __forceinline__ float list_logit(const int* list, int which, int e) {
+  return __builtin_bit_cast(float, list[which * kThreads + e]);
+}
+// The student's mass on the list over its largest logit zm where an id is on it twice:
+// each token once.
+__device__ __noinline__ double list_mass(const int* list, int k, int lane, float zm, double inv_t) {
+  double on = 0.0;
+#pragma unroll 1
+  for (int i = lane; i < k; i += 64) {
+    bool once = list[i] >= 0;
+    for (int e = 0; e < i && once; ++e) once = list[e] != list[i];
+    if (once) on += exp_(((double)list_logit(list, 2, i) - base_of(zm)) * inv_t);
+  }
+  return wave_sum(on);
+}
+// What a row's end takes of its list, by one wave, in 64 bits (a loss is a sum of
+// values that nearly cancel): the largest logits tm and zm (tm 0 for none), tl, the
+// student's mass `on` over zm if no id is on it twice, w = sum q_i, c = sum q_i (log
+// q_i - (z_i - zm) / t), and with kRest q_r and its logarithm.
+struct ListSums {
+  float tm, zm;
+  double on, tl, w, c, qr, ln_qr;
+};
+template <bool kRest>
+__device__ __forceinline__ ListSums list_sums(const int* list, int k, int lane, double inv_t, const float* teacher_lse,
+                                              int64_t row) {
+  float tm = -kInf, zm = -kInf;
+#pragma unroll 1
+  for (int i = lane; i < k; i += 64) {
+    tm = fmaxf(tm, list_logit(list, 1, i));
+    zm = fmaxf(zm, list_logit(list, 2, i));
+  }
+  tm = base_of(wave_max(tm));
+  zm = wave_max(zm);
+  // e_i = exp((t_i - tm) / t), q_i = e_i scale
+  const double base = base_of(zm);
+  double on = 0.0, e = 0.0, d = 0.0;
+#pragma unroll 1
+  for (int i = lane; i < k; i += 64) {
+    // no entry and a teacher's logit of -inf have e_i = 0
+    const double x = ((double)list_logit(list, 1, i) - tm) * inv_t, u = ((double)list_logit(list, 2, i) - base) * inv_t;
+    const double y = exp_(x);
+    on += exp_(u);
+    e += y;
+    d += y <= 0.0 ? 0.0 : y * (x - u);
+  }
+  on = wave_sum(on);
+  e = wave_sum(e);
+  d = wave_sum(d);
+  ListSums s{tm, zm, on, 0.0, 0.0, 0.0, 0.0, 0.0};
+  if (kRest) s.tl = (double)teacher_lse[row] - (double)tm * inv_t;
+  else if (e > 0.0) s.tl = log_(e);
+  const double scale = kRest ? exp_(-s.tl) : inverse(e);
+  s.w = e == 0.0 ? 0.0 : e * scale;
+  if (!(s.w <= 0.0)) s.c = d * scale - s.w * s.tl;
+  if (kRest) {
+    s.qr = 1.0 - s.w;
+    if (s.qr < 0.0) s.qr = 0.0;
+    s.ln_qr = log_(s.qr);
+  }
+  return s;
+}
+
+// ---------------------------------------------------------------------------
 // Forward.
 
 enum { kLogprobs, kDistill, kDistillRest };
+// a distillation has a wave more, for its list
+constexpr int fwd_threads(int op) { return kThreads + (op == kLogprobs ? 0 : 64); }
 
 struct RowsFwd {
   const char* Z;
@@ -288,11 +413,11 @@ struct RowsFwd {
   const void* values;
   int values_f32, k;
   const float* teacher_lse;
-  double inv_t64;
+  double inv_t64, c64;
   float* loss;
   // where rows are split
   uint64_t* flags;  // [T][S]
-  float* sums;      // [T][S][4]
+  float* sums;      // [T][S][4]: m, s, u, or m, s in 64 bits, whether an id is twice on the list
   uint64_t* lists;  // [T][S][n_top]
 };
 
@@ -425,12 +550,23 @@ __device__ __forceinline__ int select_top(const char* part, int lo, int n, int f
 // sees them all, and goes on with the row (if two see them all, both write the
 // same values). None waits for another. Whoever goes on sets the row's flags to
 // 0; before a call they may hold anything.
+//
+// A distillation's loss is a difference of values near each other, so the tokens of
+// the list, which hold most of the mass, are left out of the float32 sums and taken in
+// 64 bits, and what the sums hold moves the loss by their error times |w p_r - q_r|
+// only: of 1500 drawn calls the losses were off by 3e-8 at the median and 1.1e-6 at
+// most, at 2e-4; with the list in the sums 2e-7 and 5e-5, at 3e-3. A wave of its own makes the list's mask while the row's first loads are in
+// flight, and its sums beside the row's; without it (the list with the row's waves)
+// 1024 x 18000 with 64 entries and the rest 15.8 us and 300 x 100003 19.8, with it
+// 14.2 and 18.3; 4096 x 1000 with 32 20.7 and 21.0.
 // kTop: with the largest entries. kPast: loads past the caches.
 template <bool kF32, int kOp, bool kTop, bool kPast>
-__global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
+__global__ void __launch_bounds__(fwd_threads(kOp)) rows_fwd_kernel(RowsFwd a) {
   constexpr int kE = Elem<kF32>::kE, kVecs = Elem<kF32>::kVecs;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   __shared__ Soft s_soft[kWaves];
+  __shared__ Mass s_mass[kWaves];
+  __shared__ ListSums s_sums;
   __shared__ int s_last, s_twice, s_list[kOp == kLogprobs ? 1 : 3 * kThreads];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Part in = part_of<kF32>(a.Z, a.ldz, a.S, a.part, a.V);
@@ -452,53 +588,82 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
   uint32_t* bins = reinterpret_cast<uint32_t*>(dyn + sizeof(TopLds));
   uint64_t* s_lists = reinterpret_cast<uint64_t*>(bins);  // after the part's own selection: [S][n_top]
   uint32_t* mask = reinterpret_cast<uint32_t*>(dyn);  // bit i: position first + i is on the list
-  // the list, an entry to a thread (k <= kThreads)
-  const int64_t entry = row * a.k + tid;
-  int id = -1;
-  float ti = -kInf, zi = -kInf;
-  if (kOp != kLogprobs && tid < a.k) {
-    const int64_t j = a.ids[entry];
-    if (j >= 0 && j < a.V) id = (int)j;
-  }
-  if constexpr (kOp == kDistillRest) {
-    if (tid == 0) s_twice = 0;
-    const int words = (n + 127) / 128 * 4;
-    for (int i = tid * 4; i < words; i += kThreads * 4) *reinterpret_cast<u32x4*>(mask + i) = u32x4{0, 0, 0, 0};
+  u32x4 r[kVecs];
+  if constexpr (kOp != kLogprobs) {
+    if (wave == kWaves) {
+      // the list's wave, up to four entries to a lane
+      int id[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        id[i] = -1;
+        if (i * 64 + lane < a.k) {
+          const int64_t j = a.ids[row * a.k + i * 64 + lane];
+          if (j >= 0 && j < a.V) id[i] = (int)j;
+        }
+      }
+      // LDS accesses of one wave complete in order
+      const int words = (n + 127) / 128 * 4;
+      for (int i = lane * 4; i < words; i += 256) *reinterpret_cast<u32x4*>(mask + i) = u32x4{0, 0, 0, 0};
+      asm volatile("" ::: "memory");
+      bool twice = false;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = id[i] + shift - first;
+        const uint32_t bit = 1u << (at & 31);
+        if (id[i] >= 0 && at >= lo && at < n) twice |= (atomicOr(mask + (at >> 5), bit) & bit) != 0;
+      }
+      twice = __any(twice);
+      if (lane == 0) s_twice = twice;
+      __syncthreads();
+      float t[kPer], z[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        t[i] = z[i] = -kInf;
+        const int64_t entry = row * a.k + i * 64 + lane;
+        if (id[i] < 0) continue;
+        t[i] = a.values_f32 ? load_elem<true>(a.values, entry) : load_elem<false>(a.values, entry);
+        z[i] = load_elem<kF32>(zrow, id[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        s_list[i * 64 + lane] = id[i];
+        s_list[kThreads + i * 64 + lane] = __builtin_bit_cast(int, t[i]);
+        s_list[2 * kThreads + i * 64 + lane] = __builtin_bit_cast(int, z[i]);
+      }
+      asm volatile("" ::: "memory");
+      const ListSums sums = list_sums<kOp == kDistillRest>(s_list, a.k, lane, a.inv_t64, a.teacher_lse, row);
+      if (lane == 0) s_sums = sums;
+      __syncthreads();
+      return;
+    }
+    if (steps > 0) load_step<kF32, kPast>(r, part, 0, tid, lo, n);  // in flight while the mask is made
     __syncthreads();
-    const int at = id + shift - first;
-    const uint32_t bit = 1u << (at & 31);
-    if (id >= 0 && at >= lo && at < n && (atomicOr(mask + (at >> 5), bit) & bit)) s_twice = 1;
-    __syncthreads();
-  }
-  if (kOp != kLogprobs && id >= 0) {  // in flight with the row's loads: a barrier would wait for them
-    ti = a.values_f32 ? load_elem<true>(a.values, entry) : load_elem<false>(a.values, entry);
-    zi = load_elem<kF32>(zrow, id);
   }
 
-  Soft acc = kNone;  // without the listed entries where the list's rest is a class
+  Soft acc = kNone;  // in a distillation without the listed entries
   uint64_t best = 0;
   for (int c = 0; c < steps; ++c) {
     float z[kVecs * kE];
-    u32x4 r[kVecs];
     const int v0 = c * kVecs * kThreads + tid;
-    load_step<kF32, kPast>(r, part, c, v0, lo, n);
+    if (kOp == kLogprobs || c > 0) load_step<kF32, kPast>(r, part, c, v0, lo, n);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u)
 #pragma unroll
       for (int i = 0; i < kE; ++i) z[u * kE + i] = elem<kF32>(r[u], i);
-    if constexpr (kOp == kDistillRest) {
+    if constexpr (kOp != kLogprobs) {
+      uint32_t b[kVecs];  // all read before the branches
 #pragma unroll
       for (int u = 0; u < kVecs; ++u) {
-        const int v = v0 + u * kThreads;
-        uint32_t b = 0;
-        if (v * kE < n)
-          b = kF32 ? (reinterpret_cast<const uint8_t*>(mask)[v >> 1] >> (4 * (v & 1))) & 15u
-                   : reinterpret_cast<const uint8_t*>(mask)[v];
-        if (b) {
-#pragma unroll
-          for (int i = 0; i < kE; ++i) z[u * kE + i] = (b >> i) & 1 ? -kInf : z[u * kE + i];
-        }
+        const int v = v0 + u * kThreads < (n + kE - 1) / kE ? v0 + u * kThreads : 0;
+        const uint8_t byte = reinterpret_cast<const uint8_t*>(mask)[kF32 ? v >> 1 : v];
+        b[u] = kF32 ? (byte >> (4 * (v & 1))) & 15u : byte;
       }
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (b[u]) {
+#pragma unroll
+          for (int i = 0; i < kE; ++i) z[u * kE + i] = (b[u] >> i) & 1 ? -kInf : z[u * kE + i];
+        }
     }
     float m = z[0];
 #pragma unroll
@@ -539,19 +704,24 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
 
   // the workgroup's statistics; one wave goes on with them, all where a selection
   // is to come
-  acc = wave_join(acc, c2);
-  if (lane == 0) s_soft[wave] = acc;
-  if constexpr (kOp != kLogprobs) {
-    s_list[tid] = id;
-    s_list[kThreads + tid] = __builtin_bit_cast(int, ti);
-    s_list[2 * kThreads + tid] = __builtin_bit_cast(int, zi);
+  Mass mass = kNoMass;
+  if constexpr (kOp == kLogprobs) {
+    acc = wave_join(acc, c2);
+    if (lane == 0) s_soft[wave] = acc;
+  } else {
+    mass = wave_join(Mass{acc.m, acc.s}, a.c64);
+    if (lane == 0) s_mass[wave] = mass;
   }
   __syncthreads();
   if (!kTop && wave) return;
-  acc = s_soft[0];
+  if constexpr (kOp == kLogprobs) {
+    acc = s_soft[0];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) acc = joined(acc, s_soft[w], c2);
-  bool twice = kOp == kDistillRest && s_twice;  // an id is twice on the list
+    for (int w = 1; w < kWaves; ++w) acc = joined(acc, s_soft[w], c2);
+  } else {
+    mass = wave_join(lane < kWaves ? s_mass[lane] : kNoMass, a.c64);
+  }
+  bool twice = kOp != kLogprobs && s_twice;  // an id is twice on the list
 
   int count = 0, need = kTop ? min(a.n_top, n - lo) : 0;
   if (kTop && need > 0) count = select_top<kF32>(part, lo, n, first, steps, bins, best, need, top);
@@ -600,9 +770,17 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
                          __HIP_MEMORY_SCOPE_AGENT);
     if (tid == 0) {
       float* p = a.sums + (int64_t)blockIdx.x * 4;
-      put_agent(p, acc.m);
-      put_agent(p + 1, acc.s);
-      put_agent(p + 2, kOp == kLogprobs ? acc.u : twice ? 1.0f : 0.0f);
+      if constexpr (kOp == kLogprobs) {
+        put_agent(p, acc.m);
+        put_agent(p + 1, acc.s);
+        put_agent(p + 2, acc.u);
+      } else {
+        const uint64_t s = __builtin_bit_cast(uint64_t, mass.s);
+        put_agent(p, mass.m);
+        put_agent(p + 1, __builtin_bit_cast(float, (uint32_t)s));
+        put_agent(p + 2, __builtin_bit_cast(float, (uint32_t)(s >> 32)));
+        put_agent(p + 3, twice ? 1.0f : 0.0f);
+      }
     }
     // every store of the workgroup acknowledged before its flag
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -632,12 +810,17 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
     if (wave == 0 && lane < a.S)
       __hip_atomic_store(a.flags + row * a.S + lane, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     acc = kNone;
-    float third = 0.0f;
+    mass = kNoMass;
+    float last_of = 0.0f;
     if (lane < a.S) {
       const float* p = a.sums + (row * a.S + lane) * 4;
-      acc.m = get_agent(p);
-      acc.s = get_agent(p + 1);
-      third = get_agent(p + 2);
+      if constexpr (kOp == kLogprobs) {
+        acc = Soft{get_agent(p), get_agent(p + 1), get_agent(p + 2)};
+      } else {
+        const uint32_t s0 = __builtin_bit_cast(uint32_t, get_agent(p + 1)), s1 = __builtin_bit_cast(uint32_t, get_agent(p + 2));
+        mass = Mass{get_agent(p), __builtin_bit_cast(double, ((uint64_t)s1 << 32) | s0)};
+        last_of = get_agent(p + 3);
+      }
     }
     if constexpr (kTop) {
       // the parts' lists are sorted, and all but the last are whole: each has
@@ -661,110 +844,46 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(RowsFwd a) {
       __syncthreads();
       count = top.n_cand;
     }
-    if constexpr (kOp == kLogprobs) acc.u = third;
-    twice = __any(kOp == kDistillRest && third != 0.0f);
-    acc = wave_join(acc, c2);
+    if constexpr (kOp == kLogprobs) {
+      acc = wave_join(acc, c2);
+    } else {
+      twice = __any(last_of != 0.0f);
+      mass = wave_join(mass, a.c64);
+    }
     whole = true;
   }
 
   if constexpr (kOp != kLogprobs) {
-    // up to four list entries a lane, in 64 bits
-    constexpr int kPer = 4;
-    bool ok[kPer];
-    float t[kPer], z[kPer];
-    float tm = -kInf, zm = -kInf;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = i * 64 + lane;
-      ok[i] = s_list[e] >= 0;
-      t[i] = __builtin_bit_cast(float, s_list[kThreads + e]);
-      z[i] = __builtin_bit_cast(float, s_list[2 * kThreads + e]);
-      tm = fmaxf(tm, t[i]);
-      zm = fmaxf(zm, z[i]);
-    }
-    tm = wave_max(tm);
-    if (tm == -kInf) tm = 0.0f;
-    // the student's mass on the list, each token once
-    float on = 0.0f;
-    if constexpr (kOp == kDistillRest) {
-      zm = wave_max(zm);
-      const float base = base_of(zm);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        bool once = ok[i];
-        if (twice)  // uniform
-          for (int e = 0; e < i * 64 + lane && once; ++e) once = s_list[e] != s_list[i * 64 + lane];
-        if (once) on += exp2_((z[i] - base) * c2);
-      }
-      on = wave_sum(on);
-    }
-    double q[kPer], sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      ok[i] = ok[i] && t[i] != -kInf;
-      q[i] = 0.0;
-      if (kOp == kDistill && ok[i]) sum += q[i] = exp(((double)t[i] - tm) * a.inv_t64);
-    }
-    double tl;
-    if constexpr (kOp == kDistillRest) {
-      tl = (double)a.teacher_lse[row] - (double)tm * a.inv_t64;
-    } else {
-      sum = wave_sum(sum);
-      tl = sum > 0.0 ? log(sum) : 0.0;
-    }
-    // the student's log sums over m = the larger maximum: of the rest, of the list
-    const float m = kOp == kDistillRest ? fmaxf(acc.m, zm) : acc.m;
-    const bool empty = m == -kInf && acc.s == 0.0f && on == 0.0f;
-    double l = 0.0, logr = 0.0;
-    bool rest = false;
-    if (!empty) {
-      if constexpr (kOp == kDistillRest) {
-        rest = acc.s != 0.0f;
-        const double r = rest ? log((double)acc.s) + ((double)acc.m - m) * a.inv_t64 : -(double)kInf;
-        const double g = on != 0.0f ? log((double)on) + ((double)zm - m) * a.inv_t64 : -(double)kInf;
-        const double hi = r > g ? r : g, lo = r > g ? g : r, d = log1p(exp(lo - hi));
-        l = hi + d;
-        logr = r > g ? -d : (r - g) - d;
-        if (r != r || g != g) l = logr = r + g;
-      } else {
-        l = log((double)acc.s);
-      }
-      if (l < 0.0) l = 0.0;  // by rounding of the sums alone
-    }
-    double q_sum = 0.0, loss = 0.0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (!ok[i]) continue;
-      const double logq = ((double)t[i] - tm) * a.inv_t64 - tl;
-      const double qi = kOp == kDistill ? q[i] / sum : exp(logq);
-      const double logp = empty ? -(double)kInf : ((double)z[i] - m) * a.inv_t64 - l;
-      q_sum += qi;
-      if (!(qi <= 0.0)) loss += qi * (logq - logp);
-    }
-    q_sum = wave_sum(q_sum);
-    loss = wave_sum(loss);
-    double w = q_sum, off = q_sum;
-    if constexpr (kOp == kDistillRest) {
-      double qr = 1.0 - q_sum;
-      if (qr < 0.0) qr = 0.0;
-      if (rest && !(qr <= 0.0)) {
-        const double logq = log(qr);
-        loss += qr * (logq - logr);
-        w += qr;
-        off = w - exp(logq - logr);
-      }
+    const ListSums at = s_sums;
+    const double on = twice ? list_mass(s_list, a.k, lane, at.zm, a.inv_t64) : at.on;  // uniform
+    // The student's mass over m, the larger maximum: of the rest and of the list. Two
+    // lanes take the two exponentials, and the two logarithms.
+    const float m = fmaxf(mass.m, at.zm);
+    const bool empty = m == -kInf && mass.s == 0.0 && on == 0.0, odd = lane & 1;
+    const double base = base_of(m);
+    const double f = exp_(((double)(odd ? at.zm : mass.m) - base) * a.inv_t64);
+    const double r = mass.s * lane_of(f, 0), s = r + on * lane_of(f, 1);
+    const double ln = log_(odd ? mass.s : s);
+    double l = lane_of(ln, 0), loss = 0.0, w = at.w;
+    if (empty || l < 0.0) l = 0.0;  // below 0 by rounding of the sums alone
+    if (!(w <= 0.0)) loss = at.c + w * (empty ? (double)kInf : l - ((double)base_of(at.zm) - base) * a.inv_t64);
+    double off = w;
+    if (kOp == kDistillRest && mass.s != 0.0 && !(at.qr <= 0.0)) {
+      loss += at.qr * (at.ln_qr - (lane_of(ln, 1) + ((double)mass.m - base) * a.inv_t64 - l));
+      w += at.qr;
+      off = w - at.qr * s / r;
     }
     if (lane == 0) {
       constexpr double kTop32 = 3.402823466e38;
       a.loss[row] = (float)loss;
       if (a.stats) {
-        float* s = a.stats + row * 6;
-        s[0] = m;
-        s[1] = (float)l;
-        s[2] = (float)w;
-        s[3] = (float)(off < -kTop32 ? -kTop32 : off);
-        s[4] = tm;
-        s[5] = (float)tl;
+        float* p = a.stats + row * 6;
+        p[0] = m;
+        p[1] = (float)l;
+        p[2] = (float)w;
+        p[3] = (float)(off < -kTop32 ? -kTop32 : off);
+        p[4] = at.tm;
+        p[5] = (float)at.tl;
       }
     }
   }
@@ -993,14 +1112,14 @@ hipError_t run_fwd(const RowsFwd& a, const Logits& z, hipStream_t stream) {
     constexpr bool kF32 = decltype(f32)::value;
     const size_t n = (size_t)std::min(a.part, a.V + 7);  // positions of a part
     size_t lds = 0;
-    if (kOp == kDistillRest) lds = (n + 127) / 128 * 16;
+    if (kOp != kLogprobs) lds = (n + 127) / 128 * 16;
     if (kTop) {
       const size_t bins = (n + kUnit - 1) / kUnit * kThreads * 4;
       const size_t lists = a.S > 1 ? (size_t)a.S * a.n_top * 8 : 0;
       lds = sizeof(TopLds) + std::max(bins, lists);
     }
     rows_fwd_kernel<kF32, kOp, kTop, decltype(past)::value>
-        <<<dim3((unsigned)(z.T * a.S)), dim3(kThreads), lds, stream>>>(a);
+        <<<dim3((unsigned)(z.T * a.S)), dim3(fwd_threads(kOp)), lds, stream>>>(a);
     return hipGetLastError();
   });
 }
@@ -1037,8 +1156,9 @@ hipError_t launch_distill_fwd(const Logits& z, const TopLogits& t, const float* 
   a.ldz = z.ldz * (z.f32 ? 4 : 2);
   a.V = (int)z.V; a.S = p.S; a.part = p.part;
   a.inv_t64 = 1.0 / z.temperature;
+  a.c64 = a.inv_t64 / kLn2;
   a.inv_t = (float)a.inv_t64;
-  a.c2 = (float)(a.inv_t64 / kLn2);
+  a.c2 = (float)a.c64;
   a.stats = stats;
   a.ids = t.ids; a.values = t.values; a.values_f32 = t.f32; a.k = t.k;
   a.teacher_lse = teacher_lse; a.loss = loss;

@@ -680,8 +680,8 @@ int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8
  *   m = max z,   x = (z - m) / t,   l = log sum exp x,   log p_j = x_j - l.
  * The temperature is a double: rounded to float32 it would be off by up to 2^-24,
  * which a teacher's log sum exp at 0.7 and its logits, divided by that, do not share.
- * Sums are float32 (a row's few numbers in a distillation float64); every logit is
- * read once. No log p is above 0 and no entropy below it, whatever the sums round
+ * Sums are float32 (in a distillation float64 for the tokens on the list and a row's
+ * few numbers); every logit is read once. No log p is above 0 and no entropy below it, whatever the sums round
  * to. Rows and pointers need their elements' alignment only.
  *
  * Masked and other special rows. A logit of -inf, or so low that exp underflows,
@@ -753,9 +753,8 @@ int qlora_logprobs_bwd(const void* Z, int32_t dtype, int64_t T, int64_t V, int64
  * Where the student has no mass off the list (p_r = 0) the rest's term is left
  * out and w = sum q. q_r / p_r is kept in float32's range: where the student's
  * mass off the list is below 1e-38, the gradient there is smaller than the
- * formula's. A row without entries has loss 0 without teacher_lse. The student's
- * float32 sums leave an error of a few 1e-7 in a loss, so that one near 0 may come
- * out below it.
+ * formula's. A row without entries has loss 0 without teacher_lse. A loss that
+ * should be 0 may come out as far below it as 1e-12.
  * qlora_distill_bwd — dz_j = g / t (w p_j - q_j) for j on the list, and g / t
  * (w - q_r / p_r) p_j off it.
  *   g        device float [T], the gradient of loss; a row with g = 0 becomes 0
