@@ -661,7 +661,8 @@ int qlora_int4_dequantize(const uint8_t* codes, const uint16_t* scales, const ui
 /* qlora_int4_linear_fwd — Y = X W^T for few tokens, in one launch and without a
  * workspace. The products x (q - z) are exact and summed in float32, each
  * group's sum times s in float32. Any M is served, up to 64 tokens to a pass over
- * the weight. A token with an infinity or NaN has NaN in all of its row of Y, and one
+ * the weight; from about 256 on decoding it once for a library product takes less
+ * time. A token with an infinity or NaN has NaN in all of its row of Y, and one
  * above 2^110 may (its products are formed with 16 + q and 16 + z apart).
  *   X        device bf16 [M x K], rows ldx >= K elements apart, ldx a multiple of 8
  *            and the base 16-byte aligned
@@ -681,8 +682,9 @@ int qlora_int4_linear_fwd(const uint16_t* X, int64_t M, int64_t ldx, const uint8
  * The temperature is a double: rounded to float32 it would be off by up to 2^-24,
  * which a teacher's log sum exp at 0.7 and its logits, divided by that, do not share.
  * Sums are float32 (in a distillation float64 for the tokens on the list and a row's
- * few numbers); every logit is read once. No log p is above 0 and no entropy below it, whatever the sums round
- * to. Rows and pointers need their elements' alignment only.
+ * few numbers); every logit is read once. No log p is above 0 and no entropy below
+ * it, whatever the sums round to. Rows and pointers need their elements' alignment
+ * only.
  *
  * Masked and other special rows. A logit of -inf, or so low that exp underflows,
  * has p = 0 and adds nothing to an entropy or a gradient. A row whose logits are all
