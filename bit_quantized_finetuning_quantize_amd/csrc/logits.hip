@@ -299,7 +299,7 @@ __device__ __forceinline__ double inverse(double d) {
   return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 __device__ __forceinline__ double exp_(double x) {
-  x = x < -800.0 ? -800.0 : x;  // 0 (keeps a NaN)
+  x = x < -800.0 ? -800.0 : x > 800.0 ? 800.0 : x;  // 0 and infinity; keeps a NaN
   const double n = rint(x * 1.44269504088896340736);
   constexpr double kHi = 2977044471.0 / 4294967296.0, kLo = 1.9082149292705877e-10;  // ln 2 to 32 bits, and the rest
   const double r = __builtin_fma(n, -kLo, __builtin_fma(n, -kHi, x));
@@ -343,11 +343,12 @@ __device__ __noinline__ double list_mass(const int* list, int k, int lane, float
 }
 // What a row's end takes of its list, by one wave, in 64 bits (a loss is a sum of
 // values that nearly cancel): the largest logits tm and zm (tm 0 for none), tl, the
-// student's mass `on` over zm if no id is on it twice, w = sum q_i, c = sum q_i (log
-// q_i - (z_i - zm) / t), and with kRest q_r and its logarithm.
+// student's mass `on` over zm if no id is on it twice, e = sum e_i with e_i = exp((t_i -
+// tm) / t), d = sum e_i ((t_i - tm) - (z_i - zm)) / t, scale and tl (q_i = e_i scale, log
+// scale = -tl), w = sum q_i, and with kRest q_r and its logarithm.
 struct ListSums {
   float tm, zm;
-  double on, tl, w, c, qr, ln_qr;
+  double on, e, d, scale, tl, w, qr, ln_qr;
 };
 template <bool kRest>
 __device__ __forceinline__ ListSums list_sums(const int* list, int k, int lane, double inv_t, const float* teacher_lse,
@@ -360,7 +361,6 @@ __device__ __forceinline__ ListSums list_sums(const int* list, int k, int lane, 
   }
   tm = base_of(wave_max(tm));
   zm = wave_max(zm);
-  // e_i = exp((t_i - tm) / t), q_i = e_i scale
   const double base = base_of(zm);
   double on = 0.0, e = 0.0, d = 0.0;
 #pragma unroll 1
@@ -375,12 +375,11 @@ __device__ __forceinline__ ListSums list_sums(const int* list, int k, int lane, 
   on = wave_sum(on);
   e = wave_sum(e);
   d = wave_sum(d);
-  ListSums s{tm, zm, on, 0.0, 0.0, 0.0, 0.0, 0.0};
+  ListSums s{tm, zm, on, e, d, 0.0, 0.0, 0.0, 0.0, 0.0};
   if (kRest) s.tl = (double)teacher_lse[row] - (double)tm * inv_t;
   else if (e > 0.0) s.tl = log_(e);
-  const double scale = kRest ? exp_(-s.tl) : inverse(e);
-  s.w = e == 0.0 ? 0.0 : e * scale;
-  if (!(s.w <= 0.0)) s.c = d * scale - s.w * s.tl;
+  s.scale = kRest ? exp_(-s.tl) : inverse(e);
+  s.w = e == 0.0 ? 0.0 : e * s.scale;
   if (kRest) {
     s.qr = 1.0 - s.w;
     if (s.qr < 0.0) s.qr = 0.0;
@@ -866,7 +865,8 @@ __global__ void __launch_bounds__(fwd_threads(kOp)) rows_fwd_kernel(RowsFwd a) {
     const double ln = log_(odd ? mass.s : s);
     double l = lane_of(ln, 0), loss = 0.0, w = at.w;
     if (empty || l < 0.0) l = 0.0;  // below 0 by rounding of the sums alone
-    if (!(w <= 0.0)) loss = at.c + w * (empty ? (double)kInf : l - ((double)base_of(at.zm) - base) * a.inv_t64);
+    const double far = empty ? (double)kInf : l - ((double)base_of(at.zm) - base) * a.inv_t64;
+    if (!(w <= 0.0)) loss = at.scale * (at.d + at.e * (far - at.tl));
     double off = w;
     if (kOp == kDistillRest && mass.s != 0.0 && !(at.qr <= 0.0)) {
       loss += at.qr * (at.ln_qr - (lane_of(ln, 1) + ((double)mass.m - base) * a.inv_t64 - l));
